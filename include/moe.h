@@ -277,6 +277,118 @@ int32_t moe_layer_forward(const moe_config* cfg, const moe_layer_weights* wts, c
 int32_t moe_layer_forward_noalloc(const moe_config* cfg, const moe_layer_weights* wts, const float* x, int32_t T,
                                   float* y, const moe_taps* taps, hipStream_t stream);
 
+/* moe_layer_forward with a routing given by the caller (from moe_route, or any other) in place of the layer's own
+ * router: ids [T][K] and w [T][K] on the device; a slot whose id is outside [0, E) is dropped, and its weight is not
+ * used. Expert kernels, results and workspace as moe_layer_forward's: with the ids and weights that its own router
+ * gives, the output is the same bit for bit. router_w and router_bias of wts are not read (may be NULL), nor are
+ * cfg's n_group, topk_group, routed_scaling_factor and topp used beyond their checks. taps: topk_ids, topk_w and
+ * near_tie must be NULL (there is nothing to tap). */
+int32_t moe_layer_forward_routed(const moe_config* cfg, const moe_layer_weights* wts, const float* x, int32_t T,
+                                 const int32_t* ids, const float* w, float* y, void* ws, size_t ws_bytes,
+                                 const moe_taps* taps, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Routing from logits, for routers that moe_router does not compute and for
+ * training one: the caller has the logits z [T][E] (a product of its own), the
+ * experts run under the result through moe_layer_forward_routed.
+ *
+ *   live    an expert whose logit is NaN, -inf or the lowest finite value of its type is masked: it is never
+ *           chosen and counts in no sum. A token without live experts, and one with valid[t] == 0, has no slots.
+ *   score   s_e = 1 / (1 + exp(-z_e)), or exp(z_e) / sum over the live experts
+ *   choice  c_e = fl32(s_e) + bias_e (s in 64 bits, rounded once; fp32 addition); without a bias experts are
+ *           ordered by z_e, of which the score is a monotone function. A bias of -inf (or NaN) excludes an expert.
+ *   groups  n_group runs of n_experts / n_group experts; a group's score is the sum of the two largest (of one,
+ *           where it has one) or the largest c of its live experts (without a bias: fl32(s), or z for the largest);
+ *           the topk_group best groups stay.
+ *   slots   the top_k largest c of the groups that stay, in descending order. Ties go to the lower index, of
+ *           groups and of experts. Slots without an expert: id -1, weight 0.
+ *   weight  scale * s, or with renorm scale * s / (sum of s over the slots). The quotient is taken relative to
+ *           the largest chosen logit and so is defined where every score underflows.
+ * ---------------------------------------------------------------------- */
+/* element types of the tensors that may be fp32, bf16 or fp16 */
+#define MOE_DTYPE_F32 0
+#define MOE_DTYPE_BF16 1
+#define MOE_DTYPE_F16 2
+
+#define MOE_SCORE_SIGMOID 0
+#define MOE_SCORE_SOFTMAX 1
+#define MOE_GROUP_TOP2 0 /* group score: sum of its two largest */
+#define MOE_GROUP_MAX 1  /* group score: its largest */
+
+typedef struct moe_route_config {
+  int32_t n_experts;   /* E: 1..1024 */
+  int32_t n_group;     /* 1..64, divides n_experts */
+  int32_t topk_group;  /* 1..n_group */
+  int32_t top_k;       /* K: 1..32 and K <= topk_group * n_experts / n_group */
+  int32_t score;       /* MOE_SCORE_* */
+  int32_t group_score; /* MOE_GROUP_*; read when n_group > 1 */
+  int32_t renorm;      /* 0 or 1 */
+  float scale;         /* finite, > 0 */
+} moe_route_config;
+
+/* Bytes of workspace of moe_route with load or importance, for up to max_tokens tokens; 0 for an invalid config. */
+size_t moe_route_workspace_bytes(const moe_route_config* cfg, int32_t max_tokens);
+
+/* logits [T][E] of `dtype`, rows ld elements apart (ld >= E); bias [E] fp32 and valid [T] bytes may be NULL.
+ * Writes ids [T][K] and w [T][K] and, where not NULL, load [E] (slots of each expert) and importance [E] (sum over
+ * the tokens of s_e / sum_e s_e, fp32): what the balance of a batch is judged by and what its auxiliary loss is
+ * made of. Only these two need the workspace (256-byte aligned). Sums run in a fixed order: equal calls give equal
+ * bits. T >= 1. Errors: MOE_E_NULL, MOE_E_SHAPE, MOE_E_ARG (score, group_score, renorm, scale, dtype, ld or
+ * alignment), MOE_E_WORKSPACE, MOE_E_HIP. */
+int32_t moe_route(const moe_route_config* cfg, const void* logits, int32_t dtype, int64_t ld, int32_t T,
+                  const float* bias, const uint8_t* valid, int32_t* ids, float* w, int32_t* load, float* importance,
+                  void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Gradient of the logits: d_logits [T][E] (`dtype`, rows ld_d apart, may not overlap logits) from the gradients d_w
+ * [T][K] of moe_route's weights and d_importance [E] of its importance sums, one of which may be NULL. logits,
+ * valid and ids are those of the forward call; the choice itself has no gradient, and neither has the bias. Slots
+ * with id outside [0, E) or a masked expert add nothing, and masked experts and padding get zeros. A token's ids
+ * are distinct (moe_route's are). Errors as moe_route's. */
+int32_t moe_route_backward(const moe_route_config* cfg, const void* logits, int32_t dtype, int64_t ld, int32_t T,
+                           const uint8_t* valid, const int32_t* ids, const float* d_w, const float* d_importance,
+                           void* d_logits, int64_t ld_d, hipStream_t stream);
+
+/* Gradient of the routing weights through the combine of a layer: d_w [T][K], d_w[t][k] = sum over h of
+ * dy[t][h] * e_out[t*K + k][h], 0 where ids[t][k] < 0 (that row of e_out is not read). e_out is the tap of that name
+ * (its first T*K rows), dy [T][H] the gradient of the layer's output. H a multiple of 4; e_out and dy 16-byte
+ * aligned. Errors: MOE_E_NULL, MOE_E_SHAPE, MOE_E_ARG, MOE_E_HIP. */
+int32_t moe_slot_weight_grad(const float* e_out, const int32_t* ids, const float* dy, int32_t T, int32_t K, int32_t H,
+                             float* d_w, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A product over the library's weight codes outside the experts: dense layers, projections, heads.
+ *   y = act(W x + bias) + residual,  W [rows][cols] row-tiled int4 or int8 with row scales, or int4 with group
+ * scales (the layouts above), x [T][cols] in fp32, bf16 or fp16 and not quantized, sums in fp32; one rounding to the
+ * type of y. MOE_ACT_SWIGLU takes W's first half of rows as gate and its second as up rows (the order of w13):
+ * y = silu(gate) * up + residual, [T][rows / 2].
+ * ---------------------------------------------------------------------- */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_RELU 1
+#define MOE_ACT_SILU 2
+#define MOE_ACT_GELU 3      /* v/2 (1 + erf(v / sqrt 2)) */
+#define MOE_ACT_GELU_TANH 4 /* v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */
+#define MOE_ACT_SWIGLU 5
+
+typedef struct moe_linear_config {
+  int32_t rows;        /* N: multiple of 64, at most 2^20 */
+  int32_t cols;        /* K: multiple of 32, at most 65536 */
+  int32_t weight_bits; /* 4 (<= 0 selects it) or 8 */
+  int32_t group_size;  /* <= 0: one scale per row; else int4 only, 32 * 2^k dividing cols */
+  int32_t act;         /* MOE_ACT_* */
+} moe_linear_config;
+
+/* Bytes of workspace for up to max_tokens tokens of any type; 0 for an invalid config. */
+size_t moe_linear_workspace_bytes(const moe_linear_config* cfg, int32_t max_tokens);
+
+/* x, residual and y are of `dtype`, with rows ldx, ldr and ldy elements apart; bias [rows] fp32 and residual may be
+ * NULL; residual may be y itself (same pointer and stride). y may not overlap x. codes 16-byte aligned, the others
+ * aligned to their elements; ws 256-byte aligned. The sums W x of a token whose x holds an infinity or NaN are all
+ * infinite or NaN; other tokens are not touched by it. 1 <= T <= 2^20.
+ * Errors: MOE_E_NULL, MOE_E_SHAPE, MOE_E_ARG, MOE_E_WORKSPACE, MOE_E_HIP. */
+int32_t moe_linear(const moe_linear_config* cfg, const uint8_t* codes, const float* scales, const float* bias,
+                   const void* x, int64_t ldx, int32_t T, int32_t dtype, const void* residual, int64_t ldr, void* y,
+                   int64_t ldy, void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* ------------------------------------------------------------------------
  * Per-layer LRU expert cache [A][C]: routed experts live in pinned host
  * memory; an HBM pool of n_slots expert slots holds the recently used ones.

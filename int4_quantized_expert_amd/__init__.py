@@ -3,4 +3,4 @@ on Q8_0 int8 activations, weighted combine; optional per-layer LRU expert cache 
 
 The work runs in libmoe.so (include/moe.h); this package is its ctypes binding."""
 from ._lib import *  # noqa: F401,F403
-from ._lib import Config, MoeError, EXPORTED, LIB_PATH  # noqa: F401
+from ._lib import Config, LinearConfig, MoeError, RouteConfig, EXPORTED, LIB_PATH  # noqa: F401

@@ -16,6 +16,10 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 MOE_OK, MOE_E_NULL, MOE_E_SHAPE, MOE_E_WORKSPACE, MOE_E_HIP, MOE_E_NOMEM, MOE_E_UNSUPPORTED, MOE_E_ARG = (
     0, -1, -2, -3, -4, -5, -6, -7)
 MOE_TIE_EXPERT, MOE_TIE_GROUP, MOE_TIE_ORDER = 1, 2, 4
+MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_F16 = 0, 1, 2
+MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
+MOE_GROUP_TOP2, MOE_GROUP_MAX = 0, 1
+(MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_SWIGLU) = range(6)
 MOE_N_STAGES = 9
 STAGES = ("router", "topk", "dispatch", "q8_x", "gateup_gemv", "down_gemv", "gateup_mfma", "down_mfma",
           "combine")
@@ -43,6 +47,15 @@ class moe_config(ctypes.Structure):
 class moe_layer_weights(ctypes.Structure):
     _fields_ = [(n, P) for n in ("router_w", "router_bias", "w13", "s13", "w2", "s2", "sh_w13", "sh_s13", "sh_w2",
                                  "sh_s2")]
+
+
+class moe_route_config(ctypes.Structure):
+    _fields_ = [("n_experts", I32), ("n_group", I32), ("topk_group", I32), ("top_k", I32), ("score", I32),
+                ("group_score", I32), ("renorm", I32), ("scale", F32)]
+
+
+class moe_linear_config(ctypes.Structure):
+    _fields_ = [("rows", I32), ("cols", I32), ("weight_bits", I32), ("group_size", I32), ("act", I32)]
 
 
 class moe_taps(ctypes.Structure):
@@ -82,6 +95,13 @@ _sig("moe_router", I32, [P, P, I32, P, P, P, P, P, P, SZ, P])
 _sig("moe_dispatch", I32, [P, P, I32, P, P, P, P, P, P, P, SZ, P])
 _sig("moe_layer_forward", I32, [P, P, P, I32, P, P, SZ, P, P])
 _sig("moe_layer_forward_noalloc", I32, [P, P, P, I32, P, P, P])
+_sig("moe_layer_forward_routed", I32, [P, P, P, I32, P, P, P, P, SZ, P, P])
+_sig("moe_route_workspace_bytes", SZ, [P, I32])
+_sig("moe_route", I32, [P, P, I32, I64, I32, P, P, P, P, P, P, P, SZ, P])
+_sig("moe_route_backward", I32, [P, P, I32, I64, I32, P, P, P, P, P, I64, P])
+_sig("moe_slot_weight_grad", I32, [P, P, P, I32, I32, I32, P, P])
+_sig("moe_linear_workspace_bytes", SZ, [P, I32])
+_sig("moe_linear", I32, [P, P, P, P, P, I64, I32, I32, P, I64, P, I64, P, SZ, P])
 _sig("moe_expert_cache_create", I32, [P, I32, I32, ctypes.POINTER(P)])
 _sig("moe_expert_cache_forward", I32, [P, P, P, P, I32, P, P, SZ, P, P, P, P])
 _sig("moe_expert_cache_stats", I32, [P, P])
@@ -100,7 +120,9 @@ _sig("moe_peakbench_valu_fma", I32, [I32, I32, ctypes.c_float, ctypes.c_float, P
 EXPORTED = ("moe_version", "moe_strerror", "moe_last_hip_error", "moe_workspace_bytes", "moe_quantize_int4",
             "moe_quantize_int8", "moe_quantize_int4_grouped", "moe_quantize_q8_0",
             "moe_tile_int4", "moe_tile_int8", "moe_tile_group_scales", "moe_router", "moe_dispatch", "moe_layer_forward",
-            "moe_layer_forward_noalloc", "moe_expert_cache_create",
+            "moe_layer_forward_noalloc", "moe_layer_forward_routed", "moe_route_workspace_bytes", "moe_route",
+            "moe_route_backward", "moe_slot_weight_grad", "moe_linear_workspace_bytes", "moe_linear",
+            "moe_expert_cache_create",
             "moe_expert_cache_forward", "moe_expert_cache_stats", "moe_expert_cache_usage", "moe_expert_cache_set_usage",
             "moe_expert_cache_pin_hottest", "moe_expert_cache_destroy", "moe_prof_enable",
             "moe_prof_read", "moe_prof_disable", "moe_membench_read", "moe_membench_copy",
@@ -414,6 +436,194 @@ def moe_layer_forward_noalloc(cfg: Config, weights: moe_layer_weights, x, y, tap
     return _check("moe_layer_forward_noalloc",
                   _lib.moe_layer_forward_noalloc(ctypes.byref(c), ctypes.byref(weights), _ptr(x), T, _ptr(y),
                                                  ctypes.byref(tap) if tap else None, _stream(stream)))
+
+
+def _matrix(t, name, cols):
+    """A [rows][cols] device tensor of one of the three float types, rows possibly strided: (dtype code, stride)."""
+    import torch
+    codes = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
+    if t is None or not getattr(t, "is_cuda", False):
+        raise ArgError(f"{name}: must be a GPU tensor")
+    if t.dtype not in codes:
+        raise ArgError(f"{name}: dtype {t.dtype}, expected float32, bfloat16 or float16")
+    if t.dim() != 2 or t.shape[1] != cols or t.shape[0] < 1:
+        raise ArgError(f"{name}: shape {tuple(t.shape)}, expected [>= 1, {cols}]")
+    ld = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
+    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+        raise ArgError(f"{name}: strides {t.stride()}, expected rows of adjacent elements")
+    return codes[t.dtype], ld
+
+
+def _same_device(*named):
+    """Tensors of one call: raw pointers of another GPU would be read through the wrong device."""
+    dev = None
+    for t, name in named:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ArgError(f"{name}: on {t.device}, the other tensors on {dev}")
+    return dev
+
+
+def _op_stream(stream, dev):
+    """The given stream, else the current stream of the tensors' device."""
+    if stream is None:
+        import torch
+        return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    return _stream(stream)
+
+
+def _on(dev):
+    """Kernels launch on the current device: make it the tensors' for the call."""
+    import torch
+    return torch.cuda.device(dev)
+
+
+def moe_layer_forward_routed(cfg: Config, weights: moe_layer_weights, x, ids, w, y, ws, tap: moe_taps | None = None,
+                             stream=None, T: int | None = None):
+    """moe_layer_forward under a given routing: ids [T][K] int32 (outside [0, E): slot dropped), w [T][K] fp32."""
+    c = cfg.c()
+    T = x.shape[0] if T is None else T
+    _check_forward_args(cfg, x, y, T, ws, tap)
+    _need(ids, "ids", "i32", max(T, 0) * max(cfg.top_k, 0))
+    _need(w, "w", "f32", max(T, 0) * max(cfg.top_k, 0))
+    dev = _same_device((x, "x"), (ids, "ids"), (w, "w"), (y, "y"), (ws, "ws"))
+    with _on(dev):
+        return _check("moe_layer_forward_routed",
+                      _lib.moe_layer_forward_routed(ctypes.byref(c), ctypes.byref(weights), _ptr(x), T, _ptr(ids),
+                                                    _ptr(w), _ptr(y), _ptr(ws), ws.numel() * ws.element_size(),
+                                                    ctypes.byref(tap) if tap else None, _op_stream(stream, dev)))
+
+
+@dataclass
+class RouteConfig:
+    """moe_route_config: softmax or sigmoid scores, group limiting, renormalised weights."""
+    n_experts: int
+    top_k: int
+    n_group: int = 1
+    topk_group: int = 1
+    score: int = MOE_SCORE_SIGMOID
+    group_score: int = MOE_GROUP_TOP2
+    renorm: bool = True
+    scale: float = 1.0
+
+    def c(self):
+        return moe_route_config(self.n_experts, self.n_group, self.topk_group, self.top_k, self.score,
+                                self.group_score, int(self.renorm), self.scale)
+
+
+def moe_route_workspace_bytes(cfg: RouteConfig, max_tokens: int) -> int:
+    c = cfg.c()
+    return int(_lib.moe_route_workspace_bytes(ctypes.byref(c), int(max_tokens)))
+
+
+def moe_route(cfg: RouteConfig, logits, ids, w, bias=None, valid=None, load=None, importance=None, ws=None,
+              stream=None):
+    """Top-K routing of logits [T][E] (fp32, bf16 or fp16; rows may be strided) into ids and w [T][K]. load [E] int32
+    and importance [E] fp32 need the workspace ws of moe_route_workspace_bytes."""
+    c = cfg.c()
+    dt, ld = _matrix(logits, "logits", cfg.n_experts)
+    T, E, K = logits.shape[0], cfg.n_experts, max(cfg.top_k, 0)
+    _need(ids, "ids", "i32", T * K)
+    _need(w, "w", "f32", T * K)
+    _opt(bias, "bias", "f32", E)
+    _opt(valid, "valid", "u8", T)
+    _opt(load, "load", "i32", E)
+    _opt(importance, "importance", "f32", E)
+    _opt(ws, "ws", None, 0)
+    dev = _same_device((logits, "logits"), (ids, "ids"), (w, "w"), (bias, "bias"), (valid, "valid"), (load, "load"),
+                       (importance, "importance"), (ws, "ws"))
+    with _on(dev):
+        return _check("moe_route", _lib.moe_route(ctypes.byref(c), _ptr(logits), dt, ld, T, _ptr(bias), _ptr(valid),
+                                                  _ptr(ids), _ptr(w), _ptr(load), _ptr(importance), _ptr(ws),
+                                                  0 if ws is None else ws.numel() * ws.element_size(),
+                                                  _op_stream(stream, dev)))
+
+
+def moe_route_backward(cfg: RouteConfig, logits, ids, d_logits, d_w=None, d_importance=None, valid=None, stream=None):
+    """Gradient of the logits from those of moe_route's weights and importance sums (one of the two may be None)."""
+    c = cfg.c()
+    dt, ld = _matrix(logits, "logits", cfg.n_experts)
+    dt_d, ld_d = _matrix(d_logits, "d_logits", cfg.n_experts)
+    T, E, K = logits.shape[0], cfg.n_experts, max(cfg.top_k, 0)
+    if dt_d != dt or d_logits.shape[0] < T:
+        raise ArgError(f"d_logits: {d_logits.dtype} {tuple(d_logits.shape)}, expected {logits.dtype} [>= {T}, {E}]")
+    _need(ids, "ids", "i32", T * K)
+    _opt(d_w, "d_w", "f32", T * K)
+    _opt(d_importance, "d_importance", "f32", E)
+    _opt(valid, "valid", "u8", T)
+    dev = _same_device((logits, "logits"), (d_logits, "d_logits"), (ids, "ids"), (d_w, "d_w"),
+                       (d_importance, "d_importance"), (valid, "valid"))
+    with _on(dev):
+        return _check("moe_route_backward",
+                      _lib.moe_route_backward(ctypes.byref(c), _ptr(logits), dt, ld, T, _ptr(valid), _ptr(ids),
+                                              _ptr(d_w), _ptr(d_importance), _ptr(d_logits), ld_d,
+                                              _op_stream(stream, dev)))
+
+
+def moe_slot_weight_grad(e_out, ids, dy, d_w, stream=None):
+    """d_w [T][K] = <dy[t], e_out[t*K + k]>, 0 for dropped slots; e_out is the layer's tap (its first T*K rows)."""
+    _need(ids, "ids", "i32")
+    _need(dy, "dy", "f32")
+    _need(e_out, "e_out", "f32")
+    if ids.dim() != 2 or dy.dim() != 2 or dy.shape[0] < ids.shape[0]:
+        raise ArgError(f"ids {tuple(ids.shape)}, dy {tuple(dy.shape)}: expected [T, K] and [>= T, H]")
+    (T, K), H = ids.shape, dy.shape[1]
+    _need(e_out, "e_out", "f32", rows=T * K, cols=H)
+    _need(d_w, "d_w", "f32", T * K)
+    dev = _same_device((e_out, "e_out"), (ids, "ids"), (dy, "dy"), (d_w, "d_w"))
+    with _on(dev):
+        return _check("moe_slot_weight_grad", _lib.moe_slot_weight_grad(_ptr(e_out), _ptr(ids), _ptr(dy), T, K, H,
+                                                                        _ptr(d_w), _op_stream(stream, dev)))
+
+
+@dataclass
+class LinearConfig:
+    """moe_linear_config: weight codes [rows][cols] and the activation of the epilogue."""
+    rows: int
+    cols: int
+    weight_bits: int = 4
+    group_size: int = 0
+    act: int = MOE_ACT_NONE
+
+    def c(self):
+        return moe_linear_config(self.rows, self.cols, self.weight_bits, self.group_size, self.act)
+
+
+def moe_linear_workspace_bytes(cfg: LinearConfig, max_tokens: int) -> int:
+    c = cfg.c()
+    return int(_lib.moe_linear_workspace_bytes(ctypes.byref(c), int(max_tokens)))
+
+
+def moe_linear(cfg: LinearConfig, codes, scales, x, y, ws, bias=None, residual=None, stream=None):
+    """y [T][N] = act(W x + bias) + residual (N = rows / 2 with MOE_ACT_SWIGLU) over row-tiled codes; x, y and
+    residual of one type (fp32, bf16 or fp16), rows possibly strided. residual may be y."""
+    c = cfg.c()
+    dt, ldx = _matrix(x, "x", cfg.cols)
+    out = cfg.rows // 2 if cfg.act == MOE_ACT_SWIGLU else cfg.rows
+    dt_y, ldy = _matrix(y, "y", out)
+    T, ldr = x.shape[0], 0
+    if dt_y != dt or y.shape[0] < T:
+        raise ArgError(f"y: {y.dtype} {tuple(y.shape)}, expected {x.dtype} [>= {T}, {out}]")
+    if residual is not None:
+        dt_r, ldr = _matrix(residual, "residual", out)
+        if dt_r != dt or residual.shape[0] < T:
+            raise ArgError(f"residual: {residual.dtype} {tuple(residual.shape)}, expected {x.dtype} [>= {T}, {out}]")
+    _need(ws, "ws")
+    if _lib.moe_linear_workspace_bytes(ctypes.byref(c), 1) > 0:  # an invalid configuration is the library's to reject
+        bits = 8 if cfg.weight_bits == 8 else 4
+        groups = cfg.cols // cfg.group_size if cfg.group_size > 0 else 1
+        _need(codes, "codes", "u8", cfg.rows * cfg.cols * bits // 8)
+        _need(scales, "scales", "f32", cfg.rows * groups)
+        _opt(bias, "bias", "f32", cfg.rows)
+    dev = _same_device((x, "x"), (y, "y"), (codes, "codes"), (scales, "scales"), (bias, "bias"),
+                       (residual, "residual"), (ws, "ws"))
+    with _on(dev):
+        return _check("moe_linear", _lib.moe_linear(ctypes.byref(c), _ptr(codes), _ptr(scales), _ptr(bias), _ptr(x),
+                                                    ldx, T, dt, _ptr(residual), ldr, _ptr(y), ldy, _ptr(ws),
+                                                    ws.numel() * ws.element_size(), _op_stream(stream, dev)))
 
 
 def moe_prof_enable(max_calls: int, stages=None):

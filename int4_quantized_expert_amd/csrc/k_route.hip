@@ -1,0 +1,645 @@
+// k_route.hip — routing from given logits (softmax or sigmoid scores, selection bias, groups, top-K, load
+// statistics), its gradient, and the gradient of the routing weights from the experts' outputs.
+//
+// One wavefront works on one token: lane l holds the NE consecutive experts l*NE .. l*NE + NE-1, so the lowest
+// lane and, in it, the lowest register that hold a value hold its lowest expert, which is the tie rule.
+#include <type_traits>
+
+#include "moe_float.h"
+#include "moe_internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kWaves = 4;  // wavefronts per workgroup
+
+// ------------------------------------------------------------ wavefront reductions
+// A row of 16 lanes by quad permutes and mirrors, then the rows by the two row broadcasts; lane 63 holds the
+// result of all 64 lanes and readlane makes it uniform. No LDS round trip.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_i(int old, int v) {
+  return __builtin_amdgcn_update_dpp(old, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_max_i(int v) {
+  v = max(v, dpp_i<0xB1, 0xF>(v, v));   // quad_perm [1,0,3,2]
+  v = max(v, dpp_i<0x4E, 0xF>(v, v));   // quad_perm [2,3,0,1]
+  v = max(v, dpp_i<0x141, 0xF>(v, v));  // row_half_mirror
+  v = max(v, dpp_i<0x140, 0xF>(v, v));  // row_mirror
+  v = max(v, dpp_i<0x142, 0xA>(v, v));  // row_bcast15 into rows 1 and 3
+  v = max(v, dpp_i<0x143, 0xC>(v, v));  // row_bcast31 into rows 2 and 3
+  return __builtin_amdgcn_readlane(v, 63);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __builtin_bit_cast(float, dpp_i<CTRL, ROWS>(0, __builtin_bit_cast(int, v)));
+}
+__device__ __forceinline__ float readlane_f(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+// fixed order: pairs, quads, halves, rows
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_add<0xB1, 0xF>(v);
+  v = dpp_add<0x4E, 0xF>(v);
+  v = dpp_add<0x141, 0xF>(v);
+  v = dpp_add<0x140, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);
+  v = dpp_add<0x143, 0xC>(v);
+  return readlane_f(v, 63);
+}
+__device__ __forceinline__ double wave_sum_d(double v) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// Order-preserving signed integer of a float that is not NaN (-0 has to be made +0 by the caller).
+__device__ __forceinline__ int okey(float f) {
+  const int b = __float_as_int(f);
+  return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float unkey(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF)); }
+constexpr int kDead = INT32_MIN;  // below the key of every number (-inf is 0x807FFFFF)
+
+// ------------------------------------------------------------ one token's row
+// Lane's NE logits as fp32 (+inf becomes the largest fp32) and, in the result, a bit per live one. vec: the lane's
+// run is whole, in one vector load.
+template <int NE, class TZ>
+struct alignas(NE * sizeof(TZ) < 16 ? NE * sizeof(TZ) : 16) Run {
+  TZ v[NE];
+};
+template <int NE, class TZ>
+__device__ __forceinline__ uint32_t load_row(const TZ* row, int E, bool vec, int lane, float (&z)[NE]) {
+  const int e0 = lane * NE;
+  Run<NE, TZ> r;
+  if (vec) {
+    if (e0 < E) r = *reinterpret_cast<const Run<NE, TZ>*>(row + e0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (e0 + i < E) r.v[i] = row[e0 + i];
+  }
+  uint32_t live = 0;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    float f = e0 + i < E ? to_f32<TZ>(r.v[i]) : kNegInf;
+    const bool on = f > lowest<TZ>();
+    z[i] = on ? fminf(f, 3.402823466e38f) + 0.0f : kNegInf;
+    live |= on ? 1u << i : 0u;
+  }
+  return live;
+}
+
+template <int NE>
+__device__ __forceinline__ float row_max(const float (&z)[NE]) {
+  int m = kDead;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) m = max(m, okey(z[i]));
+  return unkey(wave_max_i(m));
+}
+
+// ------------------------------------------------------------ forward
+struct RouteArgs {
+  const void* logits;
+  int64_t ld;
+  int32_t T, E, G, KG, K;
+  int32_t group_max, renorm, vec;
+  float scale;
+  const float* bias;
+  const uint8_t* valid;
+  int32_t* ids;
+  float* w;
+  int32_t* load;   // [E], or null
+  float* imp;      // [E], or null
+  int32_t* pload;  // [blocks][E] partial counts, and
+  float* pimp;     // [blocks][E] partial sums of the workgroups
+};
+
+// Group limiting: which lanes' experts stay. g[i] is the value that the groups are scored by (kDead where masked).
+// The score is the sum of the two largest of a group (of the one, where it has one) or the largest; the KG best
+// groups stay, the lower index first on equal scores. Returns a bit per kept expert of the lane; *near is set where
+// two groups lie closer than thr + 1e-6 (|a| + |b|).
+template <int NE>
+__device__ __forceinline__ uint32_t keep_groups(const int (&g)[NE], int E, int G, int KG, bool gmax, int lane,
+                                                float* s_row, float thr, bool* near) {
+  const int n = E / G;
+  // lane group g of the first G lanes scans its group's run in LDS
+#pragma unroll
+  for (int i = 0; i < NE; ++i)
+    if (lane * NE + i < E) s_row[lane * NE + i] = unkey(g[i]);
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  float score = kNegInf;
+  if (lane < G) {
+    float a = kNegInf, b = kNegInf;
+    for (int j = 0; j < n; ++j) {
+      const float v = s_row[lane * n + j];
+      const bool on = v > kNegInf;
+      b = on ? fmaxf(b, fminf(a, v)) : b;
+      a = on ? fmaxf(a, v) : a;
+    }
+    score = gmax || !(b > kNegInf) ? a : __fadd_rn(a, b);
+  }
+  int rank = 0;
+  bool close = false;
+  for (int h = 0; h < G; ++h) {
+    const float o = readlane_f(score, h);
+    rank += (o > score) || (o == score && h < lane);
+    close |= h != lane && o > kNegInf && score > kNegInf && fabsf(o - score) <= thr + 1e-6f * (fabsf(o) + fabsf(score));
+  }
+  *near = __ballot(lane < G && close) != 0;
+  const uint64_t kept = __ballot(lane < G && rank < KG && score > kNegInf);
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const int e = lane * NE + i;
+    if (e < E && (kept >> (e / n) & 1)) r |= 1u << i;
+  }
+  __builtin_amdgcn_wave_barrier();  // s_row is written again by the next call
+  return r;
+}
+
+// The definition compares fl32(score) + bias, the score taken in 64 bits, so that every implementation chooses the
+// same experts. Taking 256 exponentials a token in 64 bits is most of the work; so the choice is made once with
+// 32-bit scores, and if two neighbours in the order (or two groups) lie closer than twice the error of those, once
+// more with the definition's. The bound: see thr below.
+template <int NE, class TZ, bool SOFTMAX, bool STATS>
+__global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
+  __shared__ float s_row[kWaves][64 * NE];
+  __shared__ int s_load[STATS ? 64 * NE : 1];
+  __shared__ float s_imp[STATS ? kWaves : 1][STATS ? 64 * NE : 1];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int E = a.E, K = a.K;
+  float bias[NE], imp[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    bias[i] = a.bias && lane * NE + i < E ? a.bias[lane * NE + i] : 0.0f;
+    imp[i] = 0.0f;
+  }
+  if (STATS) {
+    for (int e = threadIdx.x; e < 64 * NE; e += 64 * kWaves) s_load[e] = 0;
+    __syncthreads();
+  }
+  const bool by_sum = a.G > 1 && !a.group_max;
+  const bool scored = a.bias || by_sum;  // the choice compares scores, not logits
+  for (int t = blockIdx.x * kWaves + wave; t < a.T; t += gridDim.x * kWaves) {
+    float z[NE];
+    uint32_t live = load_row<NE, TZ>(static_cast<const TZ*>(a.logits) + (size_t)t * a.ld, E, a.vec, lane, z);
+    if (a.valid && a.valid[t] == 0) {
+      live = 0;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) z[i] = kNegInf;
+    }
+    const float m = row_max<NE>(z);  // -inf: nothing to choose from
+    float s[NE];
+    float rs = 0.0f;  // softmax: 1 / sum
+    if (SOFTMAX) {
+      if (scored || STATS || !a.renorm) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+          s[i] = live >> i & 1 ? exp_neg(z[i] - m) : 0.0f;
+          sum += s[i];
+        }
+        rs = safe_rcp(wave_sum(sum));
+#pragma unroll
+        for (int i = 0; i < NE; ++i) s[i] *= rs;
+      }
+    } else if (scored || STATS) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        float miss;
+        sigmoid2(z[i], s[i], miss);
+        s[i] = live >> i & 1 ? s[i] : 0.0f;
+      }
+    }
+    if (STATS) {
+      float q[NE], sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        q[i] = s[i];
+        if (!SOFTMAX && m < -40.0f) q[i] = live >> i & 1 ? sigmoid_rel(z[i], m) : 0.0f;
+        sum += q[i];
+      }
+      const float r = SOFTMAX ? 1.0f : safe_rcp(wave_sum(sum));
+#pragma unroll
+      for (int i = 0; i < NE; ++i) imp[i] = fmaf(q[i], r, imp[i]);
+    }
+    // Twice the error of a 32-bit score. Sigmoid: e^-|z| 2e-7, the sum, reciprocal and product 2.5e-7, weighted by
+    // at most 1/2 and 1: below 4e-7, and 6e-8 for rounding the 64-bit score. Softmax: the sum of up to 1024 terms
+    // (21 roundings along a path) 1.3e-6, the exponential, reciprocal and product 4e-7, of the largest score rs.
+    const float thr = SOFTMAX ? 4.5e-6f * rs + 1e-7f : 1.0e-6f;
+    int my_id = -1;
+    float my_z = 0.0f;
+    int n_sel = 0;
+    for (int attempt = 0; attempt < 2; ++attempt) {
+      if (attempt == 1) {  // the definition's scores
+        double d[NE], sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+          const bool on = live >> i & 1;
+          if (SOFTMAX) {
+            d[i] = on ? exp((double)z[i] - (double)m) : 0.0;
+            sum += d[i];
+          } else {
+            d[i] = on ? 1.0 / (1.0 + exp(-(double)z[i])) : 0.0;
+          }
+        }
+        if (SOFTMAX) sum = wave_sum_d(sum);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) s[i] = (float)(SOFTMAX ? d[i] / sum : d[i]);
+      }
+      int key[NE], gk[NE];
+      bool near = false;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        const bool on = live >> i & 1;
+        const float c = a.bias ? __fadd_rn(s[i], bias[i]) + 0.0f : z[i];
+        key[i] = on && c > kNegInf ? okey(c) : kDead;
+        gk[i] = on && by_sum && !a.bias ? okey(s[i]) : key[i];
+      }
+      if (a.G > 1) {
+        const uint32_t keep =
+            keep_groups<NE>(gk, E, a.G, a.KG, a.group_max, lane, s_row[wave], scored ? 2.0f * thr : -1.0f, &near);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) key[i] = keep >> i & 1 ? key[i] : kDead;
+        near = near && scored;
+      }
+      // K rounds of a largest key; lane k keeps slot k. Round K only finds the best expert left out.
+      int my_key = kDead;
+      n_sel = 0;
+      my_id = -1;
+      for (int k = 0; k <= K; ++k) {
+        int lm = key[0];
+#pragma unroll
+        for (int i = 1; i < NE; ++i) lm = max(lm, key[i]);
+        const int mk = wave_max_i(lm);
+        if (mk == kDead) break;
+        if (lane == k) my_key = mk;
+        if (k == K) break;
+        const int win = __ffsll((unsigned long long)__ballot(lm == mk)) - 1;
+        int pos = 0;
+        float zs = 0.0f;
+        bool open = lane == win;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+          const bool hit = open && key[i] == mk;
+          pos = hit ? i : pos;
+          zs = hit ? z[i] : zs;
+          key[i] = hit ? kDead : key[i];
+          open = open && !hit;
+        }
+        const int e = win * NE + __builtin_amdgcn_readlane(pos, win);
+        const float ze = readlane_f(zs, win);
+        if (lane == k) {
+          my_id = e;
+          my_z = ze;
+        }
+        ++n_sel;
+      }
+      if (!a.bias || attempt == 1) {
+        if (!near || attempt == 1) break;
+        continue;
+      }
+      // neighbours in the order: lane k against lane k + 1
+      const int nk = __shfl_down(my_key, 1);
+      const float c0 = unkey(my_key), c1 = unkey(nk);
+      const bool close = lane < K && my_key != kDead && nk != kDead &&
+                         c0 - c1 <= thr + 5e-7f * (fabsf(c0) + fabsf(c1));
+      if (!near && __ballot(close) == 0) break;
+    }
+    // weights, lane k slot k
+    const bool on = lane < n_sel;
+    float r;
+    if (a.renorm) {
+      const float ref = unkey(wave_max_i(on ? okey(my_z) : kDead));
+      float q = 0.0f;
+      if (on) q = SOFTMAX ? exp_neg(my_z - ref) : sigmoid_rel(my_z, fminf(ref, 0.0f));
+      r = q * safe_rcp(wave_sum(q));
+    } else if (SOFTMAX) {
+      r = on ? exp_neg(my_z - m) * rs : 0.0f;
+    } else {
+      float miss;
+      sigmoid2(my_z, r, miss);
+    }
+    if (lane < K) {
+      a.ids[(size_t)t * K + lane] = on ? my_id : -1;
+      a.w[(size_t)t * K + lane] = on ? r * a.scale : 0.0f;
+      if (STATS && on) atomicAdd(&s_load[my_id], 1);
+    }
+  }
+  if (STATS) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) s_imp[wave][lane * NE + i] = imp[i];
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += 64 * kWaves) {
+      float v = s_imp[0][e];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) v += s_imp[w][e];
+      a.pload[(size_t)blockIdx.x * E + e] = s_load[e];
+      a.pimp[(size_t)blockIdx.x * E + e] = v;
+    }
+  }
+}
+
+// Sums the workgroups' partial statistics in a fixed order: 16 experts a workgroup, 16 lanes of rows each.
+__global__ __launch_bounds__(256) void k_route_stats(const int32_t* __restrict__ pload, const float* __restrict__ pimp,
+                                                     int blocks, int E, int32_t* __restrict__ load,
+                                                     float* __restrict__ imp) {
+  __shared__ int s_l[256];
+  __shared__ double s_i[256];
+  const int c = threadIdx.x & 15, r = threadIdx.x >> 4, e = blockIdx.x * 16 + c;
+  int l = 0;
+  double v = 0.0;
+  if (e < E)
+    for (int b = r; b < blocks; b += 16) {
+      l += pload[(size_t)b * E + e];
+      v += (double)pimp[(size_t)b * E + e];
+    }
+  s_l[threadIdx.x] = l;
+  s_i[threadIdx.x] = v;
+  __syncthreads();
+  if (r == 0 && e < E) {
+    for (int q = 1; q < 16; ++q) {
+      l += s_l[q * 16 + c];
+      v += s_i[q * 16 + c];
+    }
+    if (load) load[e] = l;
+    if (imp) imp[e] = (float)v;
+  }
+}
+
+// ------------------------------------------------------------ backward
+struct RouteGradArgs {
+  const void* logits;
+  int64_t ld, ld_d;
+  int32_t T, E, K, renorm, vec, vec_d;
+  float scale;
+  const uint8_t* valid;
+  const int32_t* ids;
+  const float* dw;    // [T][K], or null
+  const float* dimp;  // [E], or null
+  void* dz;
+};
+
+template <int NE, class TZ, bool SOFTMAX>
+__global__ __launch_bounds__(64 * kWaves) void k_route_grad(RouteGradArgs a) {
+  __shared__ float s_add[kWaves][64 * NE];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int E = a.E, K = a.K;
+  float* add = s_add[wave];
+  float dimp[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) dimp[i] = a.dimp && lane * NE + i < E ? a.dimp[lane * NE + i] : 0.0f;
+  const bool dense = a.dimp || (SOFTMAX && !a.renorm && a.dw);
+  for (int t = blockIdx.x * kWaves + wave; t < a.T; t += gridDim.x * kWaves) {
+    const TZ* row = static_cast<const TZ*>(a.logits) + (size_t)t * a.ld;
+    const bool dead = a.valid && a.valid[t] == 0;
+    float out[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) out[i] = 0.0f;
+    if (!dead) {
+      // slots: lane k holds slot k's expert, its logit and the gradient of its weight
+      int id = -1;
+      float zk = kNegInf, u = 0.0f;
+      if (a.dw && lane < K) {
+        id = a.ids[(size_t)t * K + lane];
+        if ((unsigned)id < (unsigned)E) {
+          const float f = to_f32<TZ>(row[id]);
+          if (f > lowest<TZ>()) {
+            zk = fminf(f, 3.402823466e38f);
+            u = a.dw[(size_t)t * K + lane] * a.scale;
+          } else {
+            id = -1;
+          }
+        } else {
+          id = -1;
+        }
+      }
+      const bool on = id >= 0;
+      float z[NE], p[NE];
+      uint32_t live = 0;
+      float m = 0.0f, rs = 0.0f;
+      if (dense) {
+        live = load_row<NE, TZ>(row, E, a.vec, lane, z);
+        m = row_max<NE>(z);
+        if (SOFTMAX) {
+          float sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < NE; ++i) {
+            p[i] = live >> i & 1 ? exp_neg(z[i] - m) : 0.0f;
+            sum += p[i];
+          }
+          rs = safe_rcp(wave_sum(sum));
+#pragma unroll
+          for (int i = 0; i < NE; ++i) p[i] *= rs;
+        }
+      }
+      // the slots' own part
+      float dk = 0.0f;
+      if (a.renorm) {
+        const float ref = unkey(wave_max_i(on ? okey(zk + 0.0f) : kDead));
+        float q = 0.0f, miss = 1.0f;
+        if (on) {
+          q = SOFTMAX ? exp_neg(zk - ref) : sigmoid_rel(zk, fminf(ref, 0.0f));
+          if (!SOFTMAX) {
+            float s;
+            sigmoid2(zk, s, miss);
+          }
+        }
+        const float r = q * safe_rcp(wave_sum(q));
+        const float mean = wave_sum(r * u);
+        dk = r * (u - mean) * miss;
+      } else if (SOFTMAX) {
+        // p_k u_k here, and -p_e sum_k p_k u_k over all experts below
+        dk = on ? exp_neg(zk - m) * rs * u : 0.0f;
+      } else if (on) {
+        float s, miss;
+        sigmoid2(zk, s, miss);
+        dk = u * s * miss;
+      }
+      if (a.dw) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) add[lane * NE + i] = 0.0f;
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (on) atomicAdd(&add[id], dk);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+        for (int i = 0; i < NE; ++i) out[i] = add[lane * NE + i];
+        __builtin_amdgcn_wave_barrier();
+      }
+      if (SOFTMAX && dense) {
+        float dot = a.renorm ? 0.0f : dk;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) dot = fmaf(p[i], dimp[i], dot);
+        dot = wave_sum(dot);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) out[i] += p[i] * (dimp[i] - dot);
+      } else if (dense) {
+        float miss[NE], sum = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+          sigmoid2(z[i], p[i], miss[i]);
+          if (m < -40.0f) p[i] = sigmoid_rel(z[i], m);
+          p[i] = live >> i & 1 ? p[i] : 0.0f;
+          sum += p[i];
+          dot = fmaf(p[i], dimp[i], dot);
+        }
+        rs = safe_rcp(wave_sum(sum));
+        dot = wave_sum(dot) * rs;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) out[i] += p[i] * rs * (dimp[i] - dot) * miss[i];
+      }
+    }
+    TZ* drow = static_cast<TZ*>(a.dz) + (size_t)t * a.ld_d;
+    const int e0 = lane * NE;
+    Run<NE, TZ> r;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) r.v[i] = from_f32<TZ>(out[i]);
+    if (a.vec_d) {
+      if (e0 < E) *reinterpret_cast<Run<NE, TZ>*>(drow + e0) = r;
+    } else {
+#pragma unroll
+      for (int i = 0; i < NE; ++i)
+        if (e0 + i < E) drow[e0 + i] = r.v[i];
+    }
+  }
+}
+
+// ------------------------------------------------------------ gradient of the routing weights
+// dw[t][k] = sum_h dy[t][h] e_out[t*K + k][h]. Reads every slot's row once: HBM-bound. One wavefront takes one
+// slot; the K slots of a token sit next to each other, so dy comes from the caches after the first.
+__global__ __launch_bounds__(256) void k_slot_grad(const float* __restrict__ eout, const int32_t* __restrict__ ids,
+                                                   const float* __restrict__ dy, int64_t slots, int K, int H,
+                                                   float* __restrict__ dw) {
+  const int lane = threadIdx.x & 63;
+  const int64_t j = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (j >= slots) return;
+  float v = 0.0f;
+  if (ids[j] >= 0) {
+    const float4* a = reinterpret_cast<const float4*>(eout + (size_t)j * H);
+    const float4* b = reinterpret_cast<const float4*>(dy + (size_t)(j / K) * H);
+    for (int h = lane; h < H / 4; h += 64) {
+      const float4 x = a[h], y = b[h];
+      v = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, v))));
+    }
+  }
+  v = wave_sum(v);
+  if (lane == 0) dw[j] = v;
+}
+
+}  // namespace
+
+// ------------------------------------------------------------ launches
+constexpr int kRouteMaxBlocks = 2048;  // persistent grid: 8 workgroups per compute unit
+
+static int route_blocks(int T) {
+  const int need = (T + kWaves - 1) / kWaves;
+  return need < kRouteMaxBlocks ? need : kRouteMaxBlocks;
+}
+
+size_t route_ws_bytes(int E, int T) { return (size_t)route_blocks(T) * E * 8; }
+
+static int elems_per_lane(int E) { return E <= 64 ? 1 : E <= 128 ? 2 : E <= 256 ? 4 : E <= 512 ? 8 : 16; }
+
+// a lane's run in one vector access: runs are whole, and base and row stride keep the run's alignment
+static bool vec_ok(const void* p, int64_t ld, int E, int ne, size_t size) {
+  const size_t al = ne * size < 16 ? ne * size : 16;
+  return E % ne == 0 && reinterpret_cast<uintptr_t>(p) % al == 0 && (size_t)ld * size % al == 0;
+}
+
+template <class F>
+static void by_shape(int E, int dtype, bool softmax, F f) {
+  auto by_sm = [&](auto ne, auto tz) {
+    if (softmax) f(ne, tz, std::true_type{});
+    else f(ne, tz, std::false_type{});
+  };
+  auto by_type = [&](auto ne) {
+    if (dtype == MOE_DTYPE_F32) by_sm(ne, float{});
+    else if (dtype == MOE_DTYPE_BF16) by_sm(ne, bf16_t{});
+    else by_sm(ne, _Float16{});
+  };
+  switch (elems_per_lane(E)) {
+    case 1: by_type(std::integral_constant<int, 1>{}); break;
+    case 2: by_type(std::integral_constant<int, 2>{}); break;
+    case 4: by_type(std::integral_constant<int, 4>{}); break;
+    case 8: by_type(std::integral_constant<int, 8>{}); break;
+    default: by_type(std::integral_constant<int, 16>{}); break;
+  }
+}
+
+static size_t dtype_size(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
+
+hipError_t launch_moe_route(const moe_route_config& c, const void* logits, int dtype, int64_t ld, int T,
+                            const float* bias, const uint8_t* valid, int32_t* ids, float* w, int32_t* load, float* imp,
+                            void* ws, hipStream_t st) {
+  RouteArgs a{};
+  a.logits = logits;
+  a.ld = ld;
+  a.T = T;
+  a.E = c.n_experts;
+  a.G = c.n_group;
+  a.KG = c.topk_group;
+  a.K = c.top_k;
+  a.group_max = c.group_score == MOE_GROUP_MAX;
+  a.renorm = c.renorm != 0;
+  a.vec = vec_ok(logits, ld, a.E, elems_per_lane(a.E), dtype_size(dtype));
+  a.scale = c.scale;
+  a.bias = bias;
+  a.valid = valid;
+  a.ids = ids;
+  a.w = w;
+  const int blocks = route_blocks(T);
+  const bool stats = load || imp;
+  if (stats) {
+    a.pload = static_cast<int32_t*>(ws);
+    a.pimp = reinterpret_cast<float*>(a.pload + (size_t)blocks * a.E);
+  }
+  by_shape(a.E, dtype, c.score == MOE_SCORE_SOFTMAX, [&](auto ne, auto tz, auto sm) {
+    constexpr int NE = decltype(ne)::value;
+    using TZ = decltype(tz);
+    constexpr bool SM = decltype(sm)::value;
+    if (stats) k_route<NE, TZ, SM, true><<<blocks, 64 * kWaves, 0, st>>>(a);
+    else k_route<NE, TZ, SM, false><<<blocks, 64 * kWaves, 0, st>>>(a);
+  });
+  if (stats) k_route_stats<<<(a.E + 15) / 16, 256, 0, st>>>(a.pload, a.pimp, blocks, a.E, load, imp);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_route_grad(const moe_route_config& c, const void* logits, int dtype, int64_t ld, int T,
+                                 const uint8_t* valid, const int32_t* ids, const float* dw, const float* dimp, void* dz,
+                                 int64_t ld_d, hipStream_t st) {
+  RouteGradArgs a{};
+  a.logits = logits;
+  a.ld = ld;
+  a.ld_d = ld_d;
+  a.T = T;
+  a.E = c.n_experts;
+  a.K = c.top_k;
+  a.renorm = c.renorm != 0;
+  a.vec = vec_ok(logits, ld, a.E, elems_per_lane(a.E), dtype_size(dtype));
+  a.vec_d = vec_ok(dz, ld_d, a.E, elems_per_lane(a.E), dtype_size(dtype));
+  a.scale = c.scale;
+  a.valid = valid;
+  a.ids = ids;
+  a.dw = dw;
+  a.dimp = dimp;
+  a.dz = dz;
+  by_shape(a.E, dtype, c.score == MOE_SCORE_SOFTMAX, [&](auto ne, auto tz, auto sm) {
+    k_route_grad<decltype(ne)::value, decltype(tz), decltype(sm)::value><<<route_blocks(T), 64 * kWaves, 0, st>>>(a);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_slot_grad(const float* eout, const int32_t* ids, const float* dy, int T, int K, int H, float* dw,
+                            hipStream_t st) {
+  const int64_t slots = (int64_t)T * K;
+  k_slot_grad<<<(unsigned)((slots + 3) / 4), 256, 0, st>>>(eout, ids, dy, slots, K, H, dw);
+  return hipGetLastError();
+}
+
+}  // namespace moe

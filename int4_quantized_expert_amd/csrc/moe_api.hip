@@ -175,7 +175,7 @@ static int prof_begin() {
 }
 
 int fwd_setup(const moe_config* cfg, const WeightView& wv, int32_t T, void* ws, size_t ws_bytes,
-              const moe_taps* tp, Fwd* f) {
+              const moe_taps* tp, Fwd* f, bool any_ids) {
   int rc;
   if ((rc = check_tokens(cfg, T))) return rc;
   f->cfg = cfg;
@@ -245,16 +245,17 @@ int fwd_setup(const moe_config* cfg, const WeightView& wv, int32_t T, void* ws, 
     a.sum_slot = -1;
   }
   const int gemm_min = f->gemm_min, tok_tile = f->tok_tile;
+  const int64_t max_bucket = any_ids ? L.TK : T;  // positions a bucket can hold
   const int64_t mfma_buckets = std::min<int64_t>(L.E, L.TK / gemm_min) + (T >= gemm_min ? L.NS : 0);
   f->grid_tiles =
-      (T >= gemm_min) ? (int)(L.TK / tok_tile + mfma_buckets + L.NS * ((T + tok_tile - 1) / tok_tile)) : 0;
+      (max_bucket >= gemm_min) ? (int)(L.TK / tok_tile + mfma_buckets + L.NS * ((T + tok_tile - 1) / tok_tile)) : 0;
   // GEMV work items: chunks of up to kGemvMaxN tokens of the buckets below the
   // threshold (one per bucket when no such bucket can hold more)
   const int64_t gemv_buckets = std::min<int64_t>(L.E, L.TK) + (T < gemm_min ? L.NS : 0);
   f->grid_gemv =
       (int)(gemm_min <= kGemvMaxN + 1 ? gemv_buckets
                                       : (L.TK + (T < gemm_min ? L.NS * T : 0)) / kGemvMaxN + gemv_buckets);
-  f->gemv_chunk = std::max(1, std::min({kGemvMaxN, gemm_min - 1, (int)T}));
+  f->gemv_chunk = (int)std::max<int64_t>(1, std::min<int64_t>({kGemvMaxN, gemm_min - 1, max_bucket}));
   // many buckets stream at once: the GEMV keeps more blocks in flight
   f->many = L.TK + L.NS > 40;
   return MOE_OK;
@@ -279,6 +280,19 @@ hipError_t fwd_front(Fwd& f, const float* x, const float* router_w, const float*
   if (e == hipSuccess && !dispatched && !defer_dispatch) e = launch_dispatch(da, *f.cfg, stream);
   prof_mark(call, 3, stream);
   if (e == hipSuccess && !q8_done) e = launch_q8_0_x(x, f.T, f.cfg->hidden, f.qx, f.dx, tp ? tp->qx : nullptr, stream);
+  if (e == hipSuccess && tp && tp->dx)
+    e = hipMemcpyAsync(tp->dx, f.dx, (size_t)f.T * (f.cfg->hidden / 32) * 4, hipMemcpyDeviceToDevice, stream);
+  return e;
+}
+
+// The same with the routing given: dispatch (unless deferred) and Q8_0(x).
+static hipError_t fwd_front_given(Fwd& f, const float* x, const moe_taps* tp, hipStream_t stream, int call,
+                                  bool defer_dispatch) {
+  prof_mark(call, 1, stream);
+  prof_mark(call, 2, stream);
+  hipError_t e = defer_dispatch ? hipSuccess : launch_dispatch(fwd_dispatch_args(f), *f.cfg, stream);
+  prof_mark(call, 3, stream);
+  if (e == hipSuccess) e = launch_q8_0_x(x, f.T, f.cfg->hidden, f.qx, f.dx, tp ? tp->qx : nullptr, stream);
   if (e == hipSuccess && tp && tp->dx)
     e = hipMemcpyAsync(tp->dx, f.dx, (size_t)f.T * (f.cfg->hidden / 32) * 4, hipMemcpyDeviceToDevice, stream);
   return e;
@@ -419,16 +433,22 @@ constexpr int kSelfDispatchMaxSlots = 512;
 // the helper stream beside the GEMV chain (fork/join); without it both chains
 // run one after the other on `stream` and nothing is created.
 int32_t layer_forward_impl(const moe_config* cfg, const moe_layer_weights* wts, const float* x, int32_t T, float* y,
-                           void* ws, size_t ws_bytes, const moe_taps* taps, hipStream_t stream, bool use_helper) {
+                           void* ws, size_t ws_bytes, const moe_taps* taps, hipStream_t stream, bool use_helper,
+                           const Routing* given) {
   int rc = validate_config(cfg);
   if (rc) return rc;
   if (!wts || !x || !y) return MOE_E_NULL;
-  if (!wts->router_w || !wts->router_bias || !wts->w13 || !wts->s13 || !wts->w2 || !wts->s2) return MOE_E_NULL;
+  if (given ? !given->ids || !given->w : !wts->router_w || !wts->router_bias) return MOE_E_NULL;
+  if (!wts->w13 || !wts->s13 || !wts->w2 || !wts->s2) return MOE_E_NULL;
   if (cfg->n_shared > 0 && (!wts->sh_w13 || !wts->sh_s13 || !wts->sh_w2 || !wts->sh_s2)) return MOE_E_NULL;
   if (!layer_ptrs_aligned(wts, x, y, true)) return MOE_E_ARG;
   WeightView wv{wts->w13, wts->s13, wts->w2, wts->s2, wts->sh_w13, wts->sh_s13, wts->sh_w2, wts->sh_s2, nullptr};
   Fwd f;
-  if ((rc = fwd_setup(cfg, wv, T, ws, ws_bytes, taps, &f))) return rc;
+  if ((rc = fwd_setup(cfg, wv, T, ws, ws_bytes, taps, &f, given != nullptr))) return rc;
+  if (given) {  // read only from here on
+    f.ids = const_cast<int32_t*>(given->ids);
+    f.w = const_cast<float*>(given->w);
+  }
   Helper hp;
   // Small batches: the gate/up GEMV workgroups find their buckets from the top-K ids, so the GEMV chain starts
   // right after top-K and the dispatch runs beside it (on the helper stream, ahead of the MFMA chain, or after
@@ -444,7 +464,8 @@ int32_t layer_forward_impl(const moe_config* cfg, const moe_layer_weights* wts, 
   }
   const int call = prof_begin();
   prof_mark(call, 0, stream);
-  hipError_t e = fwd_front(f, x, wts->router_w, wts->router_bias, taps, stream, call, self);
+  hipError_t e = given ? fwd_front_given(f, x, taps, stream, call, self)
+                       : fwd_front(f, x, wts->router_w, wts->router_bias, taps, stream, call, self);
   prof_mark(call, 4, stream);
   const int32_t* tiles = reinterpret_cast<const int32_t*>(f.wsb + f.L.tiles);
   const int32_t* n_tiles = &reinterpret_cast<Meta*>(f.wsb + f.L.meta)->n_tiles;
@@ -500,6 +521,14 @@ extern "C" {
 int32_t moe_layer_forward(const moe_config* cfg, const moe_layer_weights* wts, const float* x, int32_t T, float* y,
                           void* ws, size_t ws_bytes, const moe_taps* taps, hipStream_t stream) {
   return layer_forward_impl(cfg, wts, x, T, y, ws, ws_bytes, taps, stream, true);
+}
+
+int32_t moe_layer_forward_routed(const moe_config* cfg, const moe_layer_weights* wts, const float* x, int32_t T,
+                                 const int32_t* ids, const float* w, float* y, void* ws, size_t ws_bytes,
+                                 const moe_taps* taps, hipStream_t stream) {
+  if (taps && (taps->topk_ids || taps->topk_w || taps->near_tie)) return MOE_E_ARG;
+  const Routing given{ids, w};
+  return layer_forward_impl(cfg, wts, x, T, y, ws, ws_bytes, taps, stream, true, &given);
 }
 
 int32_t moe_prof_enable(int32_t max_calls, uint32_t stage_mask) {

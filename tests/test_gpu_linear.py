@@ -1,0 +1,228 @@
+"""moe_linear on the GPU against a plain 64-bit implementation (tests/ops_reference.py, which derives the bound), and
+bit for bit where every sum is a whole number that fp32 holds."""
+import numpy as np
+import pytest
+
+from tests import ops_reference as R
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import int4_quantized_expert_amd as moe  # noqa: E402
+
+DEV = torch.device("cuda:0")
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+ACT = {"none": moe.MOE_ACT_NONE, "relu": moe.MOE_ACT_RELU, "silu": moe.MOE_ACT_SILU, "gelu": moe.MOE_ACT_GELU,
+       "gelu_tanh": moe.MOE_ACT_GELU_TANH, "swiglu": moe.MOE_ACT_SWIGLU}
+
+
+def _weights(rng, N, K, bits, group, whole=False):
+    """Codes over their whole range, scales, and both on the device in the tiled layouts."""
+    lim = 8 if bits == 4 else 128
+    q = rng.integers(-lim, lim, (N, K)).astype(np.int8)
+    G = group or K
+    s = rng.choice([0.5, 1.0, 2.0], (N, K // G)) if whole else rng.uniform(0.2, 1.0, (N, K // G)) / (lim * np.sqrt(K))
+    s = s.astype(np.float32)
+    if bits == 4:
+        u = (q & 15).astype(np.uint8)
+        row = torch.from_numpy(u[:, 0::2] | (u[:, 1::2] << 4)).to(DEV)
+    else:
+        row = torch.from_numpy(q).to(DEV)
+    codes = torch.empty(row.numel(), dtype=torch.uint8, device=DEV)
+    (moe.moe_tile_int4 if bits == 4 else moe.moe_tile_int8)(row, codes)
+    sc = torch.from_numpy(s).to(DEV)
+    scales = sc.view(-1)
+    if group:
+        scales = torch.empty_like(scales)
+        moe.moe_tile_group_scales(sc, scales)
+    return q.astype(np.float64), s.astype(np.float64), codes, scales
+
+
+def _call(cfg, codes, scales, x, out, bias=None, res=None, y=None):
+    T = x.shape[0]
+    y = torch.full((T + 1, out + 3), 9.0, dtype=x.dtype, device=DEV) if y is None else y
+    ws = torch.full((moe.moe_linear_workspace_bytes(cfg, T),), 0xFF, dtype=torch.uint8, device=DEV)
+    moe.moe_linear(cfg, codes, scales, x, y[:T, :out], ws, bias=bias, residual=res)
+    torch.cuda.synchronize()
+    assert bool((y[T] == 9).all()) and bool((y[:, out:] == 9).all())  # nothing behind rows and columns
+    return y[:T, :out]
+
+
+def _x(rng, T, K, dtype, pad=0, shift=0, whole=False):
+    v = rng.integers(-8, 9, (T, K)).astype(np.float32) if whole else rng.normal(0, 1, (T, K)).astype(np.float32)
+    if not whole:
+        v[:, ::37] *= 50.0
+    t = torch.from_numpy(v).to(DT[dtype])
+    buf = torch.full((T * (K + pad) + shift,), float("nan"), dtype=DT[dtype], device=DEV)
+    d = buf[shift:].as_strided((T, K), (K + pad, 1))
+    d.copy_(t)
+    return d, t.double().numpy()
+
+
+SHAPES = [(1, 64, 32), (1, 192, 96), (2, 128, 2080), (3, 320, 64), (16, 64, 160), (17, 448, 224), (31, 128, 1024),
+          (33, 192, 512), (64, 576, 96), (65, 64, 320), (129, 320, 160), (200, 1088, 64), (300, 128, 544)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("bits,group", [(4, 0), (8, 0), (4, 32), (4, 64), (4, 128)])
+@pytest.mark.parametrize("T,N,K", SHAPES)
+def test_whole_numbers_are_exact(T, N, K, bits, group, dtype):
+    """Small whole activations and scales of 1/2, 1 and 2: every partial sum is a multiple of 1/2 below 2^23, so any
+    order of additions gives the same fp32 value, rounded once to the type."""
+    K = (K + group - 1) // group * group if group else K
+    rng = np.random.default_rng(T * 1000 + N + K)
+    q, s, codes, scales = _weights(rng, N, K, bits, group, whole=True)
+    x, x64 = _x(rng, T, K, dtype, whole=True)
+    y = _call(moe.LinearConfig(N, K, bits, group), codes, scales, x, N)
+    want = x64 @ (q * np.repeat(s, K // s.shape[1], axis=1)).T
+    assert torch.equal(y.cpu(), torch.from_numpy(want.astype(np.float32)).to(DT[dtype]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("act", list(ACT))
+@pytest.mark.parametrize("T,N,K,bits,group", [(1, 256, 544, 4, 0), (5, 64, 256, 4, 32), (16, 192, 96, 8, 0),
+                                              (30, 448, 256, 4, 64), (40, 128, 1024, 8, 0), (131, 320, 384, 4, 128),
+                                              (257, 576, 160, 4, 0)])
+def test_epilogues(T, N, K, bits, group, act, dtype):
+    rng = np.random.default_rng(N + K + T)
+    q, s, codes, scales = _weights(rng, N, K, bits, group)
+    x, x64 = _x(rng, T, K, dtype)
+    out = N // 2 if act == "swiglu" else N
+    cfg = moe.LinearConfig(N, K, bits, group, ACT[act])
+    b = rng.normal(0, 0.5, N).astype(np.float32)
+    r = torch.from_numpy(rng.normal(0, 1, (T, out)).astype(np.float32)).to(DT[dtype])
+    for bias, res in ((None, None), (b, None), (None, r), (b, r)):
+        y = _call(cfg, codes, scales, x, out, None if bias is None else torch.from_numpy(bias).to(DEV),
+                  None if res is None else res.to(DEV))
+        ref, err = R.linear(q, s, x64, act, None if bias is None else bias.astype(np.float64),
+                            None if res is None else res.double().numpy())
+        tiny = 2.0 ** -25 if dtype == "f16" else 1e-37
+        tol = err + R.HALF_STEP[dtype] * (np.abs(ref) + err) + tiny
+        assert np.all(np.abs(y.double().cpu().numpy() - ref) <= tol)
+
+
+@pytest.mark.parametrize("dtype,pad,shift", [("bf16", 8, 0), ("bf16", 3, 1), ("f32", 1, 3), ("f16", 0, 1), ("f16", 24, 8)])
+@pytest.mark.parametrize("T", [1, 6, 45])
+def test_strides(T, dtype, pad, shift):
+    rng = np.random.default_rng(pad + T)
+    N, K = 192, 352
+    q, s, codes, scales = _weights(rng, N, K, 4, 0, whole=True)
+    x, x64 = _x(rng, T, K, dtype, pad, shift, whole=True)
+    want = x64 @ (q * s).T
+    y = _call(moe.LinearConfig(N, K), codes, scales, x, N)
+    assert torch.equal(y.cpu(), torch.from_numpy(want.astype(np.float32)).to(DT[dtype]))
+    # residual with its own stride, and the output over the residual itself
+    buf = torch.full((T + 1, N + 3), 9.0, dtype=DT[dtype], device=DEV)
+    res = torch.from_numpy(rng.integers(-4, 5, (T, N)).astype(np.float32)).to(DT[dtype])
+    buf[:T, :N] = res.to(DEV)
+    wide = torch.zeros((T, N + 7), dtype=DT[dtype], device=DEV)
+    wide[:, :N] = res.to(DEV)
+    want = torch.from_numpy((want + res.double().numpy()).astype(np.float32)).to(DT[dtype])
+    assert torch.equal(_call(moe.LinearConfig(N, K), codes, scales, x, N, res=wide[:, :N]).cpu(), want)
+    assert torch.equal(_call(moe.LinearConfig(N, K), codes, scales, x, N, res=buf[:T, :N], y=buf).cpu(), want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T", [1, 9, 70])
+def test_extreme_activations(T, dtype):
+    """Zero tokens, tiny and huge ones next to each other, and a token with an infinity or NaN, which leaves the other
+    tokens as they are."""
+    rng = np.random.default_rng(T)
+    N, K = 128, 256
+    q, s, codes, scales = _weights(rng, N, K, 4, 64)
+    cfg = moe.LinearConfig(N, K, 4, 64)
+    big, small = {"f32": (1e30, 1e-30), "bf16": (1e30, 1e-30), "f16": (2000.0, 1e-3)}[dtype]
+    v = rng.normal(0, 1, (T, K)).astype(np.float32)
+    v[0] *= small
+    if T > 4:
+        v[1] = 0
+        v[2] *= big
+        v[3, ::2] *= small
+        v[4, 5] *= big
+    t = torch.from_numpy(v).to(DT[dtype])
+    y = _call(cfg, codes, scales, t.to(DEV), N).clone()
+    ref, err = R.linear(q, s, t.double().numpy())
+    # below the normal range of the output type a rounding is off by half of its smallest step
+    tiny = {"f32": 1e-37, "bf16": 1e-37, "f16": 2.0 ** -25}[dtype]
+    assert np.all(np.abs(y.double().cpu().numpy() - ref) <= err + R.HALF_STEP[dtype] * (np.abs(ref) + err) + tiny)
+    if T > 4:
+        assert bool((y[1] == 0).all())
+        for bad in (float("inf"), float("-inf"), float("nan")):
+            t2 = t.clone()
+            t2[5, 17] = bad
+            y2 = _call(cfg, codes, scales, t2.to(DEV), N)
+            assert not bool(torch.isfinite(y2[5]).any())
+            keep = [i for i in range(T) if i != 5]
+            assert torch.equal(y2[keep], y[keep])
+
+
+def test_codes_beyond_2_to_the_31_elements():
+    """Rows beyond 2^31 code elements apart (a head of 131,072 rows over 16,416 columns)."""
+    N, K, T = 131072, 16416, 2
+    codes = torch.randint(0, 256, (N * K // 2,), dtype=torch.uint8, device=DEV)
+    scales = torch.ones(N, device=DEV)
+    x = torch.zeros((T, K), dtype=torch.float32, device=DEV)
+    x[0, K - 1] = 1.0
+    x[1, 0] = 2.0
+    cfg = moe.LinearConfig(N, K)
+    y = torch.empty((T, N), device=DEV)
+    ws = torch.empty(moe.moe_linear_workspace_bytes(cfg, T), dtype=torch.uint8, device=DEV)
+    moe.moe_linear(cfg, codes, scales, x, y, ws)
+    tiles = codes.view(N // 64, K // 32, 64, 16)
+    last = (tiles[:, -1, :, 15] >> 4).to(torch.int16).reshape(-1)
+    first = (tiles[:, 0, :, 0] & 15).to(torch.int16).reshape(-1)
+    assert torch.equal(y[0], torch.where(last > 7, last - 16, last).float())
+    assert torch.equal(y[1], 2 * torch.where(first > 7, first - 16, first).float())
+
+
+@pytest.mark.parametrize("T", [1, 20, 70])
+def test_dense_feed_forward(T):
+    """The two products of a dense layer as they are used: gate and up with SwiGLU, then down into the residual
+    stream, in place."""
+    rng = np.random.default_rng(T)
+    H, I = 256, 320
+    q1, s1, c1, d1 = _weights(rng, 2 * I, H, 4, 32)
+    q2, s2, c2, d2 = _weights(rng, H, I, 8, 0)
+    h, h64 = _x(rng, T, H, "f32")
+    up = moe.LinearConfig(2 * I, H, 4, 32, moe.MOE_ACT_SWIGLU)
+    down = moe.LinearConfig(H, I, 8)
+    a = torch.empty((T, I), device=DEV)
+    ws = torch.empty(max(moe.moe_linear_workspace_bytes(c, T) for c in (up, down)), dtype=torch.uint8, device=DEV)
+    moe.moe_linear(up, c1, d1, h, a, ws)
+    moe.moe_linear(down, c2, d2, a, h, ws, residual=h)
+    r1, e1 = R.linear(q1, s1, h64, "swiglu")
+    r2, e2 = R.linear(q2, s2, r1, res=h64)
+    e2 = e2 + e1 @ np.abs(q2 * s2).T * (1 + 1e-3)
+    assert np.all(np.abs(h.double().cpu().numpy() - r2) <= e2 + 2.0 ** -24 * np.abs(r2))
+
+
+@pytest.mark.parametrize("T,N,K", [(2, 256, 512), (40, 256, 2048), (150, 192, 96)])
+def test_streams_and_graph_replays(T, N, K):
+    """On a side stream, and captured: every replay equals the eager call, with eager work and synchronizations
+    between the replays; equal calls give equal bits."""
+    rng = np.random.default_rng(T)
+    _, _, codes, scales = _weights(rng, N, K, 4, 32)
+    cfg = moe.LinearConfig(N, K, 4, 32, moe.MOE_ACT_SILU)
+    x, _ = _x(rng, T, K, "bf16")
+    inputs = [_x(rng, T, K, "bf16")[0] for _ in range(4)]
+    ya, yb = (torch.empty((T, N), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    wa, wb = (torch.empty(moe.moe_linear_workspace_bytes(cfg, T), dtype=torch.uint8, device=DEV) for _ in range(2))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    moe.moe_linear(cfg, codes, scales, x, ya, wa, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    moe.moe_linear(cfg, codes, scales, x, yb, wb)
+    torch.cuda.synchronize()
+    assert torch.equal(ya, yb)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.moe_linear(cfg, codes, scales, x, ya, wa)
+    for xx in inputs:
+        x.copy_(xx)
+        moe.moe_linear(cfg, codes, scales, xx, yb, wb)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(ya, yb)
