@@ -30,9 +30,9 @@ if not os.path.exists(LIB_PATH):
 # library must bind to the runtime torch uses (tensors and streams come from
 # torch), so torch is loaded first whenever it is installed.
 try:
-    import torch  # noqa: F401
+    import torch
 except ImportError:
-    pass
+    torch = None
 _lib = ctypes.CDLL(LIB_PATH)
 
 P, I32, I64, SZ, F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
@@ -438,47 +438,65 @@ def moe_layer_forward_noalloc(cfg: Config, weights: moe_layer_weights, x, y, tap
                                                  ctypes.byref(tap) if tap else None, _stream(stream)))
 
 
+_FLOAT_DT = {}
+
+
+def _float_types():
+    """{torch dtype: MOE_DTYPE_*} of the tensors that may be fp32, bf16 or fp16."""
+    _FLOAT_DT.update({torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16})
+    return _FLOAT_DT
+
+
 def _matrix(t, name, cols):
-    """A [rows][cols] device tensor of one of the three float types, rows possibly strided: (dtype code, stride)."""
-    import torch
-    codes = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
+    """A [rows][cols] device tensor of one of the three float types, rows possibly strided: (dtype code, rows,
+    elements between rows)."""
     if t is None or not getattr(t, "is_cuda", False):
         raise ArgError(f"{name}: must be a GPU tensor")
-    if t.dtype not in codes:
+    dt = (_FLOAT_DT or _float_types()).get(t.dtype)
+    if dt is None:
         raise ArgError(f"{name}: dtype {t.dtype}, expected float32, bfloat16 or float16")
-    if t.dim() != 2 or t.shape[1] != cols or t.shape[0] < 1:
-        raise ArgError(f"{name}: shape {tuple(t.shape)}, expected [>= 1, {cols}]")
-    ld = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
-    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or shape[0] < 1:
+        raise ArgError(f"{name}: shape {tuple(shape)}, expected [>= 1, {cols}]")
+    rows, (ld, step) = shape[0], t.stride()
+    if rows == 1 and ld < cols:
+        ld = cols
+    if ld < cols or (step != 1 and cols > 1):
         raise ArgError(f"{name}: strides {t.stride()}, expected rows of adjacent elements")
-    return codes[t.dtype], ld
+    return dt, rows, ld
 
 
-def _same_device(*named):
-    """Tensors of one call: raw pointers of another GPU would be read through the wrong device."""
-    dev = None
-    for t, name in named:
-        if t is None:
-            continue
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ArgError(f"{name}: on {t.device}, the other tensors on {dev}")
-    return dev
+def _dev_ptr(t, name, dtype, numel, dev):
+    """Address of a device tensor after _need's checks, which this repeats only for the message; the tensors of one
+    call share a device, since the library would read another GPU's pointer through the wrong one."""
+    if (getattr(t, "is_cuda", False) and t.numel() >= numel and t.is_contiguous()
+            and (dtype is None or t.dtype == (_DT.get(dtype) or _dtype(dtype)))):
+        if t.get_device() != dev:
+            raise ArgError(f"{name}: on {t.device}, the other tensors on cuda:{dev}")
+        return t.data_ptr()
+    _need(t, name, dtype, numel)
 
 
-def _op_stream(stream, dev):
-    """The given stream, else the current stream of the tensors' device."""
-    if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
-    return _stream(stream)
+def _same_dev(t, name, dev):
+    if t.get_device() != dev:
+        raise ArgError(f"{name}: on {t.device}, the other tensors on cuda:{dev}")
+    return t.data_ptr()
 
 
-def _on(dev):
-    """Kernels launch on the current device: make it the tensors' for the call."""
-    import torch
-    return torch.cuda.device(dev)
+def _opt_ptr(t, name, dtype, numel, dev):
+    return None if t is None else _dev_ptr(t, name, dtype, numel, dev)
+
+
+def _launch(fn, dev, stream, *args):
+    """Calls C entry fn with the tensors' device current (kernels launch on the current device) on the given
+    stream, else on that device's current stream."""
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _launch(fn, dev, stream, *args)
+    # the handle itself: building a torch Stream object around it takes 1 us of an 8 us call
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    rc = fn(*args, st)
+    return rc if rc == MOE_OK else _check(fn.__name__, rc)
 
 
 def moe_layer_forward_routed(cfg: Config, weights: moe_layer_weights, x, ids, w, y, ws, tap: moe_taps | None = None,
@@ -487,14 +505,11 @@ def moe_layer_forward_routed(cfg: Config, weights: moe_layer_weights, x, ids, w,
     c = cfg.c()
     T = x.shape[0] if T is None else T
     _check_forward_args(cfg, x, y, T, ws, tap)
-    _need(ids, "ids", "i32", max(T, 0) * max(cfg.top_k, 0))
-    _need(w, "w", "f32", max(T, 0) * max(cfg.top_k, 0))
-    dev = _same_device((x, "x"), (ids, "ids"), (w, "w"), (y, "y"), (ws, "ws"))
-    with _on(dev):
-        return _check("moe_layer_forward_routed",
-                      _lib.moe_layer_forward_routed(ctypes.byref(c), ctypes.byref(weights), _ptr(x), T, _ptr(ids),
-                                                    _ptr(w), _ptr(y), _ptr(ws), ws.numel() * ws.element_size(),
-                                                    ctypes.byref(tap) if tap else None, _op_stream(stream, dev)))
+    dev, n = x.get_device(), max(T, 0) * max(cfg.top_k, 0)
+    return _launch(_lib.moe_layer_forward_routed, dev, stream, ctypes.byref(c), ctypes.byref(weights), x.data_ptr(), T,
+                   _dev_ptr(ids, "ids", "i32", n, dev), _dev_ptr(w, "w", "f32", n, dev),
+                   _dev_ptr(y, "y", None, 0, dev), _dev_ptr(ws, "ws", None, 0, dev), ws.numel() * ws.element_size(),
+                   ctypes.byref(tap) if tap else None)
 
 
 @dataclass
@@ -523,60 +538,41 @@ def moe_route(cfg: RouteConfig, logits, ids, w, bias=None, valid=None, load=None
               stream=None):
     """Top-K routing of logits [T][E] (fp32, bf16 or fp16; rows may be strided) into ids and w [T][K]. load [E] int32
     and importance [E] fp32 need the workspace ws of moe_route_workspace_bytes."""
-    c = cfg.c()
-    dt, ld = _matrix(logits, "logits", cfg.n_experts)
-    T, E, K = logits.shape[0], cfg.n_experts, max(cfg.top_k, 0)
-    _need(ids, "ids", "i32", T * K)
-    _need(w, "w", "f32", T * K)
-    _opt(bias, "bias", "f32", E)
-    _opt(valid, "valid", "u8", T)
-    _opt(load, "load", "i32", E)
-    _opt(importance, "importance", "f32", E)
-    _opt(ws, "ws", None, 0)
-    dev = _same_device((logits, "logits"), (ids, "ids"), (w, "w"), (bias, "bias"), (valid, "valid"), (load, "load"),
-                       (importance, "importance"), (ws, "ws"))
-    with _on(dev):
-        return _check("moe_route", _lib.moe_route(ctypes.byref(c), _ptr(logits), dt, ld, T, _ptr(bias), _ptr(valid),
-                                                  _ptr(ids), _ptr(w), _ptr(load), _ptr(importance), _ptr(ws),
-                                                  0 if ws is None else ws.numel() * ws.element_size(),
-                                                  _op_stream(stream, dev)))
+    E, K = cfg.n_experts, max(cfg.top_k, 0)
+    dt, T, ld = _matrix(logits, "logits", E)
+    dev = logits.get_device()
+    return _launch(_lib.moe_route, dev, stream, ctypes.byref(cfg.c()), logits.data_ptr(), dt, ld, T,
+                   _opt_ptr(bias, "bias", "f32", E, dev), _opt_ptr(valid, "valid", "u8", T, dev),
+                   _dev_ptr(ids, "ids", "i32", T * K, dev), _dev_ptr(w, "w", "f32", T * K, dev),
+                   _opt_ptr(load, "load", "i32", E, dev), _opt_ptr(importance, "importance", "f32", E, dev),
+                   _opt_ptr(ws, "ws", None, 0, dev), 0 if ws is None else ws.numel() * ws.element_size())
 
 
 def moe_route_backward(cfg: RouteConfig, logits, ids, d_logits, d_w=None, d_importance=None, valid=None, stream=None):
     """Gradient of the logits from those of moe_route's weights and importance sums (one of the two may be None)."""
-    c = cfg.c()
-    dt, ld = _matrix(logits, "logits", cfg.n_experts)
-    dt_d, ld_d = _matrix(d_logits, "d_logits", cfg.n_experts)
-    T, E, K = logits.shape[0], cfg.n_experts, max(cfg.top_k, 0)
-    if dt_d != dt or d_logits.shape[0] < T:
+    E, K = cfg.n_experts, max(cfg.top_k, 0)
+    dt, T, ld = _matrix(logits, "logits", E)
+    dt_d, T_d, ld_d = _matrix(d_logits, "d_logits", E)
+    if dt_d != dt or T_d < T:
         raise ArgError(f"d_logits: {d_logits.dtype} {tuple(d_logits.shape)}, expected {logits.dtype} [>= {T}, {E}]")
-    _need(ids, "ids", "i32", T * K)
-    _opt(d_w, "d_w", "f32", T * K)
-    _opt(d_importance, "d_importance", "f32", E)
-    _opt(valid, "valid", "u8", T)
-    dev = _same_device((logits, "logits"), (d_logits, "d_logits"), (ids, "ids"), (d_w, "d_w"),
-                       (d_importance, "d_importance"), (valid, "valid"))
-    with _on(dev):
-        return _check("moe_route_backward",
-                      _lib.moe_route_backward(ctypes.byref(c), _ptr(logits), dt, ld, T, _ptr(valid), _ptr(ids),
-                                              _ptr(d_w), _ptr(d_importance), _ptr(d_logits), ld_d,
-                                              _op_stream(stream, dev)))
+    dev = logits.get_device()
+    return _launch(_lib.moe_route_backward, dev, stream, ctypes.byref(cfg.c()), logits.data_ptr(), dt, ld, T,
+                   _opt_ptr(valid, "valid", "u8", T, dev), _dev_ptr(ids, "ids", "i32", T * K, dev),
+                   _opt_ptr(d_w, "d_w", "f32", T * K, dev), _opt_ptr(d_importance, "d_importance", "f32", E, dev),
+                   _same_dev(d_logits, "d_logits", dev), ld_d)
 
 
 def moe_slot_weight_grad(e_out, ids, dy, d_w, stream=None):
     """d_w [T][K] = <dy[t], e_out[t*K + k]>, 0 for dropped slots; e_out is the layer's tap (its first T*K rows)."""
     _need(ids, "ids", "i32")
     _need(dy, "dy", "f32")
-    _need(e_out, "e_out", "f32")
     if ids.dim() != 2 or dy.dim() != 2 or dy.shape[0] < ids.shape[0]:
         raise ArgError(f"ids {tuple(ids.shape)}, dy {tuple(dy.shape)}: expected [T, K] and [>= T, H]")
     (T, K), H = ids.shape, dy.shape[1]
     _need(e_out, "e_out", "f32", rows=T * K, cols=H)
-    _need(d_w, "d_w", "f32", T * K)
-    dev = _same_device((e_out, "e_out"), (ids, "ids"), (dy, "dy"), (d_w, "d_w"))
-    with _on(dev):
-        return _check("moe_slot_weight_grad", _lib.moe_slot_weight_grad(_ptr(e_out), _ptr(ids), _ptr(dy), T, K, H,
-                                                                        _ptr(d_w), _op_stream(stream, dev)))
+    dev = e_out.get_device()
+    return _launch(_lib.moe_slot_weight_grad, dev, stream, e_out.data_ptr(), _same_dev(ids, "ids", dev),
+                   _same_dev(dy, "dy", dev), T, K, H, _dev_ptr(d_w, "d_w", "f32", T * K, dev))
 
 
 @dataclass
@@ -600,30 +596,26 @@ def moe_linear_workspace_bytes(cfg: LinearConfig, max_tokens: int) -> int:
 def moe_linear(cfg: LinearConfig, codes, scales, x, y, ws, bias=None, residual=None, stream=None):
     """y [T][N] = act(W x + bias) + residual (N = rows / 2 with MOE_ACT_SWIGLU) over row-tiled codes; x, y and
     residual of one type (fp32, bf16 or fp16), rows possibly strided. residual may be y."""
-    c = cfg.c()
-    dt, ldx = _matrix(x, "x", cfg.cols)
-    out = cfg.rows // 2 if cfg.act == MOE_ACT_SWIGLU else cfg.rows
-    dt_y, ldy = _matrix(y, "y", out)
-    T, ldr = x.shape[0], 0
-    if dt_y != dt or y.shape[0] < T:
+    rows, cols, G = cfg.rows, cfg.cols, cfg.group_size
+    out = rows // 2 if cfg.act == MOE_ACT_SWIGLU else rows
+    dt, T, ldx = _matrix(x, "x", cols)
+    dt_y, T_y, ldy = _matrix(y, "y", out)
+    if dt_y != dt or T_y < T:
         raise ArgError(f"y: {y.dtype} {tuple(y.shape)}, expected {x.dtype} [>= {T}, {out}]")
+    dev = x.get_device()
+    res, ldr = None, 0
     if residual is not None:
-        dt_r, ldr = _matrix(residual, "residual", out)
-        if dt_r != dt or residual.shape[0] < T:
+        dt_r, T_r, ldr = _matrix(residual, "residual", out)
+        if dt_r != dt or T_r < T:
             raise ArgError(f"residual: {residual.dtype} {tuple(residual.shape)}, expected {x.dtype} [>= {T}, {out}]")
-    _need(ws, "ws")
-    if _lib.moe_linear_workspace_bytes(ctypes.byref(c), 1) > 0:  # an invalid configuration is the library's to reject
-        bits = 8 if cfg.weight_bits == 8 else 4
-        groups = cfg.cols // cfg.group_size if cfg.group_size > 0 else 1
-        _need(codes, "codes", "u8", cfg.rows * cfg.cols * bits // 8)
-        _need(scales, "scales", "f32", cfg.rows * groups)
-        _opt(bias, "bias", "f32", cfg.rows)
-    dev = _same_device((x, "x"), (y, "y"), (codes, "codes"), (scales, "scales"), (bias, "bias"),
-                       (residual, "residual"), (ws, "ws"))
-    with _on(dev):
-        return _check("moe_linear", _lib.moe_linear(ctypes.byref(c), _ptr(codes), _ptr(scales), _ptr(bias), _ptr(x),
-                                                    ldx, T, dt, _ptr(residual), ldr, _ptr(y), ldy, _ptr(ws),
-                                                    ws.numel() * ws.element_size(), _op_stream(stream, dev)))
+        res = _same_dev(residual, "residual", dev)
+    # an invalid configuration is the library's to reject, before it looks at the data: sizes as if it were valid
+    n_codes = rows * cols * (8 if cfg.weight_bits == 8 else 4) // 8
+    n_scales = rows * (cols // G) if G > 0 else rows
+    return _launch(_lib.moe_linear, dev, stream, ctypes.byref(cfg.c()), _dev_ptr(codes, "codes", "u8", n_codes, dev),
+                   _dev_ptr(scales, "scales", "f32", n_scales, dev), _opt_ptr(bias, "bias", "f32", rows, dev),
+                   x.data_ptr(), ldx, T, dt, res, ldr, _same_dev(y, "y", dev), ldy, _dev_ptr(ws, "ws", None, 0, dev),
+                   ws.numel() * ws.element_size())
 
 
 def moe_prof_enable(max_calls: int, stages=None):

@@ -3,6 +3,7 @@
 //
 // One wavefront works on one token: lane l holds the NE consecutive experts l*NE .. l*NE + NE-1, so the lowest
 // lane and, in it, the lowest register that hold a value hold its lowest expert, which is the tie rule.
+#include <algorithm>
 #include <type_traits>
 
 #include "moe_float.h"
@@ -104,6 +105,7 @@ struct RouteArgs {
   int64_t ld;
   int32_t T, E, G, KG, K;
   int32_t group_max, renorm, vec;
+  int32_t glog;  // log2 of the lanes of a group, -1 where groups are not whole lanes or not a power of two of them
   float scale;
   const float* bias;
   const uint8_t* valid;
@@ -115,62 +117,170 @@ struct RouteArgs {
   float* pimp;     // [blocks][E] partial sums of the workgroups
 };
 
-// Group limiting: which lanes' experts stay. g[i] is the value that the groups are scored by (kDead where masked).
-// The score is the sum of the two largest of a group (of the one, where it has one) or the largest; the KG best
-// groups stay, the lower index first on equal scores. Returns a bit per kept expert of the lane; *near is set where
-// two groups lie closer than thr + 1e-6 (|a| + |b|).
-template <int NE>
-__device__ __forceinline__ uint32_t keep_groups(const int (&g)[NE], int E, int G, int KG, bool gmax, int lane,
-                                                float* s_row, float thr, bool* near) {
-  const int n = E / G;
-  // lane group g of the first G lanes scans its group's run in LDS
-#pragma unroll
-  for (int i = 0; i < NE; ++i)
-    if (lane * NE + i < E) s_row[lane * NE + i] = unkey(g[i]);
+// Orders LDS writes of some lanes of a wavefront before later LDS reads of others (and those before later writes).
+__device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  float score = kNegInf;
-  if (lane < G) {
-    float a = kNegInf, b = kNegInf;
-    for (int j = 0; j < n; ++j) {
-      const float v = s_row[lane * n + j];
-      const bool on = v > kNegInf;
-      b = on ? fmaxf(b, fminf(a, v)) : b;
-      a = on ? fmaxf(a, v) : a;
-    }
-    score = gmax || !(b > kNegInf) ? a : __fadd_rn(a, b);
+}
+// lanes of the mask below this one
+__device__ __forceinline__ int lanes_below(uint64_t m) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+}
+
+// (a, b) two largest of one set, (c, d) of another -> of both
+__device__ __forceinline__ void merge_top2(int& a, int& b, int c, int d) {
+  b = max(max(b, d), min(a, c));
+  a = max(a, c);
+}
+template <int CTRL>
+__device__ __forceinline__ void merge_top2_dpp(int& a, int& b) {
+  merge_top2(a, b, dpp_i<CTRL, 0xF>(a, a), dpp_i<CTRL, 0xF>(b, b));
+}
+
+// Group limiting: which of the lane's experts stay. g[i] is the value that the groups are scored by (kDead where
+// masked). The score is the sum of the two largest of a group (of the one, where it has one) or the largest; the KG
+// best groups stay, the lower index first on equal scores. *near is set where the last kept and the first dropped
+// group lie within thr + 1e-6 (|a| + |b|).
+// glog >= 0: a group is 2^glog whole lanes, its two largest are merged across them in registers; else its run is
+// scanned in LDS by one lane. 32,768 tokens x 256 experts in 8 groups: 73 us for the kernel with the scan alone.
+template <int NE>
+__device__ __forceinline__ uint32_t keep_groups(const int (&g)[NE], int E, int G, int KG, int glog, bool gmax, int lane,
+                                                int* s_row, float thr, bool* near) {
+  int a = kDead, b = kDead, mine, step;
+  if (glog >= 0) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) merge_top2(a, b, g[i], kDead);
+    if (glog >= 1) merge_top2_dpp<0xB1>(a, b);   // quad_perm [1,0,3,2]
+    if (glog >= 2) merge_top2_dpp<0x4E>(a, b);   // quad_perm [2,3,0,1]
+    if (glog >= 3) merge_top2_dpp<0x141>(a, b);  // row_half_mirror
+    if (glog >= 4) merge_top2_dpp<0x140>(a, b);  // row_mirror
+    if (glog >= 5) merge_top2(a, b, __shfl_xor(a, 16), __shfl_xor(b, 16));
+    if (glog >= 6) merge_top2(a, b, __shfl_xor(a, 32), __shfl_xor(b, 32));
+    mine = lane >> glog;
+    step = 1 << glog;
+  } else {
+    const int n = E / G;
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (lane * NE + i < E) s_row[lane * NE + i] = g[i];
+    wave_sync();
+    if (lane < G)
+      for (int j = 0; j < n; ++j) merge_top2(a, b, s_row[lane * n + j], kDead);
+    wave_sync();
+    mine = lane;
+    step = 1;
   }
+  const bool is = mine < G;
+  const int score = !is ? kDead : gmax || b == kDead ? a : okey(__fadd_rn(unkey(a), unkey(b)) + 0.0f);
   int rank = 0;
-  bool close = false;
   for (int h = 0; h < G; ++h) {
-    const float o = readlane_f(score, h);
-    rank += (o > score) || (o == score && h < lane);
-    close |= h != lane && o > kNegInf && score > kNegInf && fabsf(o - score) <= thr + 1e-6f * (fabsf(o) + fabsf(score));
+    const int o = __builtin_amdgcn_readlane(score, h * step);
+    rank += o + (h < mine ? 1 : 0) > score;  // keys of numbers stay below INT32_MAX
   }
-  *near = __ballot(lane < G && close) != 0;
-  const uint64_t kept = __ballot(lane < G && rank < KG && score > kNegInf);
+  const bool kept = is && rank < KG && score != kDead;
+  const int lowest_kept = -wave_max_i(kept ? -score : kDead);  // a kept key is above kDead, so -score exists
+  const int best_dropped = wave_max_i(is && !kept ? score : kDead);
+  *near = false;
+  if (best_dropped != kDead) {
+    const float p = unkey(lowest_kept), q = unkey(best_dropped);
+    *near = p - q <= thr + 1e-6f * (fabsf(p) + fabsf(q));
+  }
+  const uint64_t m = __ballot(kept);
   uint32_t r = 0;
+  if (glog >= 0) {
+    r = kept ? (1u << NE) - 1 : 0;
+  } else {
+    const int n = E / G;
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (lane * NE + i < E && (m >> ((lane * NE + i) / n) & 1)) r |= 1u << i;
+  }
+  return r;
+}
+
+// The K largest keys of the wavefront (all, where there are fewer; the lower index first on equal keys), in no order:
+// their number, and lane j < number holds the key and the expert of one of them, in *key and *id. *next is the
+// largest key left out (kDead: none).
+// The K-th largest is found by bisection between keys: a step is NE comparisons whose ballots are counted in scalar
+// registers, and about ten steps separate the K-th from the next; K rounds of a largest key took 20 vector
+// instructions each and 6 dependent lane moves.
+template <int NE>
+__device__ __forceinline__ int top_keys(const int (&k)[NE], int K, int lane, int* s_key, int* s_id, int* key, int* id,
+                                        int* next) {
+  int lm = k[0];
+#pragma unroll
+  for (int i = 1; i < NE; ++i) lm = max(lm, k[i]);
+  const int top = wave_max_i(lm);
+  // every lane with a live key has one that is at least the smallest of their largest ones
+  const uint64_t lanes = __ballot(lm != kDead);
+  const int base = __popcll(lanes) >= K ? -wave_max_i(lm != kDead ? -lm : kDead) : kDead + 1;
+  auto count = [&](int v) {
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) c += __popcll(__ballot(k[i] >= v));
+    return c;
+  };
+  const int n_base = count(base);
+  int lo = base, n_lo = n_base, hi = top, n_hi = 0;  // count(lo) >= K > count(hi + 1), where there are K
+  if (n_lo > K) {
+    while (lo != hi) {  // lo < hi: smallest v > lo with count(v) <= K lies in (lo, hi + 1]
+      const int mid = (int)((uint32_t)lo + (((uint32_t)hi - (uint32_t)lo + 1u) >> 1));
+      const int c = count(mid);
+      if (c == K) {
+        lo = mid;
+        n_lo = c;
+        break;
+      }
+      if (c > K) {
+        lo = mid;
+        n_lo = c;
+      } else {
+        hi = mid - 1;
+        n_hi = c;
+      }
+    }
+  }
+  // n_lo > K: more than K keys are at least lo, n_hi of them above it; the first K - n_hi that equal lo fill up
+  int before = 0;
+  if (n_lo > K) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) before += lanes_below(__ballot(k[i] == lo));
+  }
+  int at = 0, rest = kDead, n = 0;
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
-    const int e = lane * NE + i;
-    if (e < E && (kept >> (e / n) & 1)) r |= 1u << i;
+    bool on = k[i] >= lo;
+    if (n_lo > K && k[i] == lo) on = before++ < K - n_hi;
+    const uint64_t m = __ballot(on);
+    if (on) {
+      const int p = at + lanes_below(m);
+      s_key[p] = k[i];
+      s_id[p] = lane * NE + i;
+    }
+    at += __popcll(m);
+    rest = max(rest, on ? kDead : k[i]);
   }
-  __builtin_amdgcn_wave_barrier();  // s_row is written again by the next call
-  return r;
+  n = at;
+  wave_sync();
+  *key = lane < n ? s_key[lane] : kDead;
+  *id = lane < n ? s_id[lane] : -1;
+  wave_sync();
+  *next = wave_max_i(rest);
+  return n;
 }
 
 // The definition compares fl32(score) + bias, the score taken in 64 bits, so that every implementation chooses the
 // same experts. Taking 256 exponentials a token in 64 bits is most of the work; so the choice is made once with
 // 32-bit scores, and if two neighbours in the order (or two groups) lie closer than twice the error of those, once
 // more with the definition's. The bound: see thr below.
-template <int NE, class TZ, bool SOFTMAX, bool STATS>
-__global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
-  __shared__ float s_row[kWaves][64 * NE];
+template <int NE, class TZ, bool SOFTMAX, bool STATS, int WV>
+__global__ __launch_bounds__(64 * WV) void k_route(RouteArgs a) {
+  __shared__ int s_row[WV][64 * NE];  // a wavefront's scratch
   __shared__ int s_load[STATS ? 64 * NE : 1];
-  __shared__ float s_imp[STATS ? kWaves : 1][STATS ? 64 * NE : 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int E = a.E, K = a.K;
+  int* scratch = s_row[wave];
   float bias[NE], imp[NE];
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
@@ -178,20 +288,21 @@ __global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
     imp[i] = 0.0f;
   }
   if (STATS) {
-    for (int e = threadIdx.x; e < 64 * NE; e += 64 * kWaves) s_load[e] = 0;
+    for (int e = threadIdx.x; e < 64 * NE; e += 64 * WV) s_load[e] = 0;
     __syncthreads();
   }
   const bool by_sum = a.G > 1 && !a.group_max;
   const bool scored = a.bias || by_sum;  // the choice compares scores, not logits
-  for (int t = blockIdx.x * kWaves + wave; t < a.T; t += gridDim.x * kWaves) {
+  for (int t = blockIdx.x * WV + wave; t < a.T; t += gridDim.x * WV) {
+    const TZ* row = static_cast<const TZ*>(a.logits) + (size_t)t * a.ld;
     float z[NE];
-    uint32_t live = load_row<NE, TZ>(static_cast<const TZ*>(a.logits) + (size_t)t * a.ld, E, a.vec, lane, z);
+    uint32_t live = load_row<NE, TZ>(row, E, a.vec, lane, z);
     if (a.valid && a.valid[t] == 0) {
       live = 0;
 #pragma unroll
       for (int i = 0; i < NE; ++i) z[i] = kNegInf;
     }
-    const float m = row_max<NE>(z);  // -inf: nothing to choose from
+    const float m = SOFTMAX || STATS ? row_max<NE>(z) : 0.0f;  // -inf: nothing to choose from
     float s[NE];
     float rs = 0.0f;  // softmax: 1 / sum
     if (SOFTMAX) {
@@ -230,26 +341,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
     // at most 1/2 and 1: below 4e-7, and 6e-8 for rounding the 64-bit score. Softmax: the sum of up to 1024 terms
     // (21 roundings along a path) 1.3e-6, the exponential, reciprocal and product 4e-7, of the largest score rs.
     const float thr = SOFTMAX ? 4.5e-6f * rs + 1e-7f : 1.0e-6f;
-    int my_id = -1;
-    float my_z = 0.0f;
-    int n_sel = 0;
-    for (int attempt = 0; attempt < 2; ++attempt) {
-      if (attempt == 1) {  // the definition's scores
-        double d[NE], sum = 0.0;
-#pragma unroll
-        for (int i = 0; i < NE; ++i) {
-          const bool on = live >> i & 1;
-          if (SOFTMAX) {
-            d[i] = on ? exp((double)z[i] - (double)m) : 0.0;
-            sum += d[i];
-          } else {
-            d[i] = on ? 1.0 / (1.0 + exp(-(double)z[i])) : 0.0;
-          }
-        }
-        if (SOFTMAX) sum = wave_sum_d(sum);
-#pragma unroll
-        for (int i = 0; i < NE; ++i) s[i] = (float)(SOFTMAX ? d[i] / sum : d[i]);
-      }
+    int n_sel, my_key, my_id, rank;
+    float my_z;
+    for (int attempt = 0;; ++attempt) {
       int key[NE], gk[NE];
       bool near = false;
 #pragma unroll
@@ -261,55 +355,50 @@ __global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
       }
       if (a.G > 1) {
         const uint32_t keep =
-            keep_groups<NE>(gk, E, a.G, a.KG, a.group_max, lane, s_row[wave], scored ? 2.0f * thr : -1.0f, &near);
+            keep_groups<NE>(gk, E, a.G, a.KG, a.glog, a.group_max, lane, scratch, 2.0f * thr, &near);
 #pragma unroll
         for (int i = 0; i < NE; ++i) key[i] = keep >> i & 1 ? key[i] : kDead;
-        near = near && scored;
       }
-      // K rounds of a largest key; lane k keeps slot k. Round K only finds the best expert left out.
-      int my_key = kDead;
-      n_sel = 0;
-      my_id = -1;
-      for (int k = 0; k <= K; ++k) {
-        int lm = key[0];
+      int next;
+      n_sel = top_keys<NE>(key, K, lane, scratch, scratch + 32, &my_key, &my_id, &next);
+      my_z = kNegInf;  // read again: the logit of a chosen expert
+      if (lane < n_sel) my_z = fminf(to_f32<TZ>(row[my_id]), 3.402823466e38f) + 0.0f;
+      // the chosen in order: rank = how many come before; gap to the nearest of them
+      rank = 0;
+      float gap = INFINITY;
+      const float mine = unkey(my_key);
+      for (int j = 0; j < n_sel; ++j) {
+        const int ok = __builtin_amdgcn_readlane(my_key, j), oi = __builtin_amdgcn_readlane(my_id, j);
+        const bool ahead = ok > my_key || (ok == my_key && oi < my_id);
+        rank += ahead;
+        if (ahead) gap = fminf(gap, unkey(ok) - mine);
+      }
+      if (!scored || attempt == 1) break;
+      if (a.bias) {
+        // scores off by thr / 2 each; the rounding of the two additions is below 1e-6 of the values
+        if (next != kDead) gap = fminf(gap, mine - unkey(next));
+        const bool close = lane < n_sel && gap < INFINITY && gap <= thr + 1e-6f * (fabsf(mine) + gap);
+        near |= __ballot(close) != 0;
+      }
+      if (!near) break;
+      // the definition's scores
+      double d[NE], sum = 0.0;
 #pragma unroll
-        for (int i = 1; i < NE; ++i) lm = max(lm, key[i]);
-        const int mk = wave_max_i(lm);
-        if (mk == kDead) break;
-        if (lane == k) my_key = mk;
-        if (k == K) break;
-        const int win = __ffsll((unsigned long long)__ballot(lm == mk)) - 1;
-        int pos = 0;
-        float zs = 0.0f;
-        bool open = lane == win;
+      for (int i = 0; i < NE; ++i) {
+        const bool on = live >> i & 1;
+        float zi = z[i];
+        asm volatile("" : "+v"(zi));  // keeps this rare work inside the branch (it was hoisted above the loop)
+        if (SOFTMAX) {
+          d[i] = on ? exp((double)zi - (double)m) : 0.0;
+          sum += d[i];
+        } else {
+          d[i] = on ? 1.0 / (1.0 + exp(-(double)zi)) : 0.0;
+        }
+      }
+      if (SOFTMAX) sum = wave_sum_d(sum);
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-          const bool hit = open && key[i] == mk;
-          pos = hit ? i : pos;
-          zs = hit ? z[i] : zs;
-          key[i] = hit ? kDead : key[i];
-          open = open && !hit;
-        }
-        const int e = win * NE + __builtin_amdgcn_readlane(pos, win);
-        const float ze = readlane_f(zs, win);
-        if (lane == k) {
-          my_id = e;
-          my_z = ze;
-        }
-        ++n_sel;
-      }
-      if (!a.bias || attempt == 1) {
-        if (!near || attempt == 1) break;
-        continue;
-      }
-      // neighbours in the order: lane k against lane k + 1
-      const int nk = __shfl_down(my_key, 1);
-      const float c0 = unkey(my_key), c1 = unkey(nk);
-      const bool close = lane < K && my_key != kDead && nk != kDead &&
-                         c0 - c1 <= thr + 5e-7f * (fabsf(c0) + fabsf(c1));
-      if (!near && __ballot(close) == 0) break;
+      for (int i = 0; i < NE; ++i) s[i] = (float)(SOFTMAX ? d[i] / sum : d[i]);
     }
-    // weights, lane k slot k
     const bool on = lane < n_sel;
     float r;
     if (a.renorm) {
@@ -323,50 +412,57 @@ __global__ __launch_bounds__(64 * kWaves) void k_route(RouteArgs a) {
       float miss;
       sigmoid2(my_z, r, miss);
     }
-    if (lane < K) {
-      a.ids[(size_t)t * K + lane] = on ? my_id : -1;
-      a.w[(size_t)t * K + lane] = on ? r * a.scale : 0.0f;
+    if (lane < K) {  // the chosen by their rank, the empty slots behind them
+      const int k = on ? rank : lane;
+      a.ids[(size_t)t * K + k] = on ? my_id : -1;
+      a.w[(size_t)t * K + k] = on ? r * a.scale : 0.0f;
       if (STATS && on) atomicAdd(&s_load[my_id], 1);
     }
   }
   if (STATS) {
-#pragma unroll
-    for (int i = 0; i < NE; ++i) s_imp[wave][lane * NE + i] = imp[i];
+    float* s_imp = reinterpret_cast<float*>(s_row[0]);  // [WV][64 * NE]
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += 64 * kWaves) {
-      float v = s_imp[0][e];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) v += s_imp[w][e];
+    for (int i = 0; i < NE; ++i) s_imp[wave * 64 * NE + lane * NE + i] = imp[i];
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += 64 * WV) {
+      float v = s_imp[e];
+#pragma unroll
+      for (int w = 1; w < WV; ++w) v += s_imp[w * 64 * NE + e];
       a.pload[(size_t)blockIdx.x * E + e] = s_load[e];
       a.pimp[(size_t)blockIdx.x * E + e] = v;
     }
   }
 }
 
-// Sums the workgroups' partial statistics in a fixed order: 16 experts a workgroup, 16 lanes of rows each.
-__global__ __launch_bounds__(256) void k_route_stats(const int32_t* __restrict__ pload, const float* __restrict__ pimp,
-                                                     int blocks, int E, int32_t* __restrict__ load,
-                                                     float* __restrict__ imp) {
-  __shared__ int s_l[256];
-  __shared__ double s_i[256];
+// Sums the workgroups' partial statistics in a fixed order: 16 experts a workgroup, 64 lanes of rows each.
+__global__ __launch_bounds__(1024) void k_route_stats(const int32_t* __restrict__ pload, const float* __restrict__ pimp,
+                                                      int blocks, int E, int32_t* __restrict__ load,
+                                                      float* __restrict__ imp) {
+  __shared__ int s_l[1024];
+  __shared__ double s_i[1024];
   const int c = threadIdx.x & 15, r = threadIdx.x >> 4, e = blockIdx.x * 16 + c;
   int l = 0;
   double v = 0.0;
-  if (e < E)
-    for (int b = r; b < blocks; b += 16) {
+  if (e < E) {
+#pragma unroll 4
+    for (int b = r; b < blocks; b += 64) {
       l += pload[(size_t)b * E + e];
       v += (double)pimp[(size_t)b * E + e];
     }
+  }
   s_l[threadIdx.x] = l;
   s_i[threadIdx.x] = v;
-  __syncthreads();
-  if (r == 0 && e < E) {
-    for (int q = 1; q < 16; ++q) {
-      l += s_l[q * 16 + c];
-      v += s_i[q * 16 + c];
+  for (int h = 512; h >= 16; h >>= 1) {
+    __syncthreads();
+    if ((int)threadIdx.x < h) {
+      s_l[threadIdx.x] += s_l[threadIdx.x + h];
+      s_i[threadIdx.x] += s_i[threadIdx.x + h];
     }
-    if (load) load[e] = l;
-    if (imp) imp[e] = (float)v;
+  }
+  if (r == 0 && e < E) {
+    if (load) load[e] = s_l[threadIdx.x];
+    if (imp) imp[e] = (float)s_i[threadIdx.x];
   }
 }
 
@@ -535,14 +631,24 @@ __global__ __launch_bounds__(256) void k_slot_grad(const float* __restrict__ eou
 }  // namespace
 
 // ------------------------------------------------------------ launches
-constexpr int kRouteMaxBlocks = 2048;  // persistent grid: 8 workgroups per compute unit
+constexpr int kRouteMaxWaves = 8192;  // persistent grid: 8 wavefronts per SIMD
+// With statistics a workgroup leaves one row of partial sums; from this many tokens on it has 16 wavefronts, so that
+// there are at most 512 rows to add up.
+constexpr int kRouteWideT = 2048;
+constexpr int kWideWaves = 16;
 
-static int route_blocks(int T) {
-  const int need = (T + kWaves - 1) / kWaves;
-  return need < kRouteMaxBlocks ? need : kRouteMaxBlocks;
+static int route_blocks(int T, int waves = kWaves) {
+  const int need = (T + waves - 1) / waves, most = kRouteMaxWaves / waves;
+  return need < most ? need : most;
 }
+static int stats_waves(int T) { return T >= kRouteWideT ? kWideWaves : kWaves; }
 
-size_t route_ws_bytes(int E, int T) { return (size_t)route_blocks(T) * E * 8; }
+// for any number of tokens up to T: a batch just below the wide form leaves the most rows
+size_t route_ws_bytes(int E, int T) {
+  const int narrow = route_blocks(T < kRouteWideT ? T : kRouteWideT - 1);
+  const int rows = T < kRouteWideT ? narrow : std::max(narrow, route_blocks(T, kWideWaves));
+  return (size_t)rows * E * 8;
+}
 
 static int elems_per_lane(int E) { return E <= 64 ? 1 : E <= 128 ? 2 : E <= 256 ? 4 : E <= 512 ? 8 : 16; }
 
@@ -593,8 +699,12 @@ hipError_t launch_moe_route(const moe_route_config& c, const void* logits, int d
   a.valid = valid;
   a.ids = ids;
   a.w = w;
-  const int blocks = route_blocks(T);
+  a.glog = -1;
+  const int gl = a.E / a.G / elems_per_lane(a.E);  // lanes of a group
+  if (gl * elems_per_lane(a.E) * a.G == a.E && gl > 0 && (gl & (gl - 1)) == 0)
+    for (a.glog = 0; (1 << a.glog) < gl;) ++a.glog;
   const bool stats = load || imp;
+  const int waves = stats ? stats_waves(T) : kWaves, blocks = route_blocks(T, waves);
   if (stats) {
     a.pload = static_cast<int32_t*>(ws);
     a.pimp = reinterpret_cast<float*>(a.pload + (size_t)blocks * a.E);
@@ -603,10 +713,11 @@ hipError_t launch_moe_route(const moe_route_config& c, const void* logits, int d
     constexpr int NE = decltype(ne)::value;
     using TZ = decltype(tz);
     constexpr bool SM = decltype(sm)::value;
-    if (stats) k_route<NE, TZ, SM, true><<<blocks, 64 * kWaves, 0, st>>>(a);
-    else k_route<NE, TZ, SM, false><<<blocks, 64 * kWaves, 0, st>>>(a);
+    if (!stats) k_route<NE, TZ, SM, false, kWaves><<<blocks, 64 * kWaves, 0, st>>>(a);
+    else if (waves == kWaves) k_route<NE, TZ, SM, true, kWaves><<<blocks, 64 * kWaves, 0, st>>>(a);
+    else k_route<NE, TZ, SM, true, kWideWaves><<<blocks, 64 * kWideWaves, 0, st>>>(a);
   });
-  if (stats) k_route_stats<<<(a.E + 15) / 16, 256, 0, st>>>(a.pload, a.pimp, blocks, a.E, load, imp);
+  if (stats) k_route_stats<<<(a.E + 15) / 16, 1024, 0, st>>>(a.pload, a.pimp, blocks, a.E, load, imp);
   return hipGetLastError();
 }
 

@@ -83,6 +83,7 @@ __device__ __forceinline__ float sigmoid_rel(float z, float ref) {
   const float d = __builtin_amdgcn_rcpf(1.0f + exp_neg(-fabsf(z)));
   return z >= 0.0f ? d : exp_neg(z - ref) * d;
 }
-__device__ __forceinline__ float safe_rcp(float v) { return v > 0.0f ? 1.0f / v : 0.0f; }
+// 1 / v to 1 unit in the last place, 0 for an empty sum
+__device__ __forceinline__ float safe_rcp(float v) { return v > 0.0f ? __builtin_amdgcn_rcpf(v) : 0.0f; }
 
 }  // namespace moe
