@@ -12,6 +12,7 @@
 // Unpacking a word of eight nibbles: the nibble, moved to 0..15 by flipping its top bit, is put into the low (or
 // next) mantissa bits of 1024.0; a packed subtraction (or multiply-add by 1/16) leaves the code. That gives the
 // element order 0 4 1 5 2 6 3 7, in which the activations are stored too.
+#include <algorithm>
 #include <type_traits>
 
 #include "moe_float.h"
@@ -30,6 +31,7 @@ typedef uint32_t u4v __attribute__((ext_vector_type(4)));
 struct LinearArgs {
   int32_t T, N, K, nb, nbp;  // tokens, weight rows, columns, 32-blocks of a row, blocks padded to a multiple of 2
   int32_t half;              // rows of the gate part (SwiGLU), else 0
+  int32_t vec_x;             // rows of x start on 16-byte boundaries
   int32_t act, gshift;       // gshift: log2(group / 32), -1 for one scale a row
   const uint8_t* codes;
   const float* scales;
@@ -42,6 +44,98 @@ struct LinearArgs {
   _Float16* xl;  // their rest (fp32 activations only), same order
   int32_t* sh;   // [T] power of two that token t was multiplied by
 };
+
+// ------------------------------------------------------------ activations to fp16
+// A granule: eight neighbouring elements of a token as they lie in memory.
+template <class TX>
+struct Granule {
+  uint32_t w[2 * sizeof(TX)];
+};
+// vec: the rows of x start on 16-byte boundaries
+template <class TX>
+__device__ __forceinline__ void load8(const TX* p, bool vec, Granule<TX>& d) {
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(TX) / 2; ++i) {
+      const u4v v = reinterpret_cast<const u4v*>(p)[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d.w[4 * i + j] = v[j];
+    }
+  } else {
+    TX v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = p[i];
+    __builtin_memcpy(&d, v, sizeof(d));
+  }
+}
+typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+// Largest magnitudes: the bits without the sign, compared as integers (infinity and NaN come out on top). bf16: two in
+// one word.
+template <class TX>
+__device__ __forceinline__ void amax8(const Granule<TX>& d, uint32_t& m) {
+#pragma unroll
+  for (int i = 0; i < (int)(2 * sizeof(TX)); ++i) {
+    if (sizeof(TX) == 4) {
+      m = max(m, d.w[i] & 0x7FFFFFFFu);
+    } else {
+      const us2 v = __builtin_bit_cast(us2, d.w[i] & 0x7FFF7FFFu);
+      m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2, m), v));
+    }
+  }
+}
+template <class TX>
+__device__ __forceinline__ uint32_t amax_bits(uint32_t m) {
+  return sizeof(TX) == 4 ? m : max(m << 16, m & 0xFFFF0000u);
+}
+// power of two for the largest magnitude: 0 where it is zero, infinite or NaN
+__device__ __forceinline__ int scale_shift(uint32_t amax) {
+  return amax > 0 && amax < 0x7F800000u ? 14 - ((int)(amax >> 23) - 127) : 0;
+}
+// Element pairs (0 4) (1 5) (2 6) (3 7) as fp16. finite: the token holds neither infinity nor NaN; otherwise its
+// finite values are only kept finite.
+template <class TX>
+__device__ __forceinline__ void convert8(const Granule<TX>& d, int sh, bool finite, h8& hi, h8& lo) {
+  if constexpr (std::is_same<TX, _Float16>::value) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      o[2 * i] = __builtin_amdgcn_perm(d.w[i + 2], d.w[i], 0x05040100u);
+      o[2 * i + 1] = __builtin_amdgcn_perm(d.w[i + 2], d.w[i], 0x07060302u);
+    }
+    __builtin_memcpy(&hi, o, 16);
+  } else {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = (i >> 1) + 4 * (i & 1);
+      uint32_t u;
+      if (sizeof(TX) == 4) u = d.w[e & (2 * sizeof(TX) - 1)];
+      else u = e & 1 ? d.w[e >> 1] & 0xFFFF0000u : d.w[e >> 1] << 16;
+      v[i] = ldexpf(__uint_as_float(u), sh);
+    }
+    if (!finite)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (fabsf(v[i]) < INFINITY) v[i] = fminf(fmaxf(v[i], -65504.0f), 65504.0f);
+    if constexpr (sizeof(TX) == 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        hi[i] = (_Float16)v[i];
+        lo[i] = (_Float16)(v[i] - (float)hi[i]);
+      }
+      if (!finite)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (!(fabsf(v[i]) < INFINITY)) lo[i] = (_Float16)0.0f;
+    } else {  // a bf16 value fits, or is far below the largest: rounding toward zero serves
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        o[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(v[2 * i], v[2 * i + 1]));
+      __builtin_memcpy(&hi, o, 16);
+    }
+  }
+}
 
 // ------------------------------------------------------------ activations to fp16 in tile order
 // One workgroup takes 8 tokens: thread = (token tid % 8, granule of 8 elements tid / 8), so 8 neighbouring threads
@@ -60,29 +154,26 @@ __global__ __launch_bounds__(256) void k_linear_x(LinearArgs a) {
   if (kScaled) {
     uint32_t m = 0;
     if (in)
-      for (int g = g0; g < ng; g += 32)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(to_f32<TX>(row[g * 8 + i])) & 0x7FFFFFFFu);
+      for (int g = g0; g < ng; g += 32) {
+        Granule<TX> v;
+        load8(row + g * 8, a.vec_x, v);
+        amax8<TX>(v, m);
+      }
+    m = amax_bits<TX>(m);
     s_max[g0][tk] = m;
     __syncthreads();
     for (int i = 0; i < 32; ++i) m = max(m, s_max[i][tk]);
     finite = m < 0x7F800000u;
-    sh = finite && m > 0 ? 14 - ((int)(m >> 23) - 127) : 0;
+    sh = scale_shift(m);
   }
   if (in && g0 == 0) a.sh[t] = sh;
   const size_t base = (size_t)(t >> 5) * a.nbp * 1024 + (size_t)(t & 31) * 8;
   for (int g = g0; g < a.nbp * 4; g += 32) {
-    h8 hi, lo;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = (i >> 1) + 4 * (i & 1);  // element order 0 4 1 5 2 6 3 7
-      float v = in && g < ng ? to_f32<TX>(row[g * 8 + e]) : 0.0f;
-      if (kScaled) {
-        v = ldexpf(v, sh);
-        if (!finite && fabsf(v) < INFINITY) v = fminf(fmaxf(v, -65504.0f), 65504.0f);
-      }
-      hi[i] = (_Float16)v;
-      lo[i] = (_Float16)(fabsf(v) < INFINITY ? v - (float)hi[i] : 0.0f);
+    h8 hi = {}, lo = {};
+    if (in && g < ng) {
+      Granule<TX> v;
+      load8(row + g * 8, a.vec_x, v);
+      convert8<TX>(v, sh, finite, hi, lo);
     }
     const size_t at = base + (size_t)g * 256;  // g = block * 4 + slice
     *reinterpret_cast<h8*>(a.xh + at) = hi;
@@ -260,7 +351,436 @@ __global__ __launch_bounds__(256) void k_linear_tile(LinearArgs a) {
     }
 }
 
+// ------------------------------------------------------------ few tokens: product
+// Reading the codes is what counts: all of them are in flight at once. v_mfma_f32_16x16x32_f16 multiplies 16 tokens by
+// fragments of 16 weight rows, F of them in a wavefront (with SwiGLU 16 gate rows and the 16 up rows that go with
+// them).
+// Codes: lane (row r = l % 16, g = l / 16) loads the 16 bytes (int8: 32) of its row in block 4q + g. With one scale a
+// row, instruction i then takes slice i of the four blocks; with group scales a 4 x 4 transposition over the lane
+// groups leaves the lane slice g of each block, so that one instruction covers one block and scales are applied
+// between blocks.
+// Activations are converted in LDS, order [blocks][4 slices][tokens][8], each token multiplied by a power of two of its
+// own. Their loads are issued ahead of the codes' (loads return in order) and stay in registers while the largest is
+// found.
+typedef float f4v __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ void transpose4(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  auto s = __builtin_amdgcn_permlane32_swap(a, c, false, false);
+  a = s[0], c = s[1];
+  s = __builtin_amdgcn_permlane32_swap(b, d, false, false);
+  b = s[0], d = s[1];
+  s = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = s[0], b = s[1];
+  s = __builtin_amdgcn_permlane16_swap(c, d, false, false);
+  c = s[0], d = s[1];
+}
+
+// One quad of blocks of a fragment: codes and scales. GSH: -1 one scale a row, else log2(group / 32), at most 2 (a
+// larger group has one scale for the quad too).
+template <int W, int GSH>
+struct Quad {
+  static constexpr int kScales = GSH < 0 ? 1 : 4 >> GSH;
+  uint32_t w[W];
+  float s[kScales];
+};
+
+// A wavefront's weight rows.
+template <int W, int GSH, int F>
+struct Rows {
+  int row[F];
+  const uint8_t* src[F];
+  const float* scale[F];
+  int g, nb, gshift;
+
+  // output columns out0 .. of the F fragments
+  __device__ __forceinline__ Rows(const LinearArgs& a, int out0, int lane) : g(lane >> 4), nb(a.nb), gshift(a.gshift) {
+    const int r = lane & 15, groups = GSH >= 0 ? a.nb >> a.gshift : 0;
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      row[f] = a.half ? f * a.half + min(out0 + r, a.half - 1) : min(out0 + 16 * f + r, a.N - 1);
+      src[f] = a.codes + tbw_off<W>(row[f] / 64, 0, a.nb) + (size_t)(row[f] % 64) * (4 * W);
+      scale[f] = a.scales + (GSH >= 0 ? (size_t)(row[f] / 64) * groups * 64 + row[f] % 64 : (size_t)row[f]);
+    }
+  }
+  // blocks b .. b + 3; past the last block the activations are zero, so any codes will do
+  __device__ __forceinline__ void load(Quad<W, GSH> (&d)[F], int b) const {
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      const u4v* p = reinterpret_cast<const u4v*>(src[f] + (size_t)min(b + g, nb - 1) * kTileBlock<W>);
+#pragma unroll
+      for (int i = 0; i < W / 4; ++i) {
+        const u4v v = __builtin_nontemporal_load(p + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[f].w[4 * i + j] = v[j];
+      }
+      if constexpr (GSH >= 0)
+#pragma unroll
+        for (int i = 0; i < Quad<W, GSH>::kScales; ++i)
+          d[f].s[i] = scale[f][(size_t)(min(b + (i << GSH), nb - 1) >> gshift) * 64];
+    }
+  }
+};
+
+// acc += quad times activations. x: LDS of the quad's first block; token fragment n and half v start at
+// (v * NT + n) * stride halfs; a block has 4 slices of TOK tokens of 8 halfs; rt the lane's token.
+template <int NX, int NT, int TOK, int W, int GSH, int F>
+__device__ __forceinline__ void multiply_quad(Quad<W, GSH> (&d)[F], const _Float16* x, int stride, int rt, int g,
+                                              f4v (&acc)[NT][F]) {
+  if constexpr (GSH >= 0)
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      if constexpr (W == 4) {
+        transpose4(d[f].w[0], d[f].w[1], d[f].w[2], d[f].w[3]);
+      } else {  // slice j: words 2j and 2j + 1
+        transpose4(d[f].w[0], d[f].w[2], d[f].w[4], d[f].w[6]);
+        transpose4(d[f].w[1], d[f].w[3], d[f].w[5], d[f].w[7]);
+      }
+    }
+  f4v c[NT][F];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool first = GSH == 0 || (GSH == 1 && (i & 1) == 0) || i == 0;
+    const bool last = GSH == 0 || (GSH == 1 && (i & 1) == 1) || i == 3;
+    h8 wf[F];
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      if constexpr (W == 4) wf[f] = codes_h8(d[f].w[i]);
+      else wf[f] = codes_h8(d[f].w[2 * i], d[f].w[2 * i + 1]);
+    }
+    const int slice = GSH < 0 ? g * 4 + i : i * 4 + g;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int v = 0; v < NX; ++v) {
+        const h8 xf = *reinterpret_cast<const h8*>(x + (v * NT + n) * stride + (slice * TOK + rt) * 8);
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          if (GSH < 0) {
+            acc[n][f] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xf, wf[f], acc[n][f], 0, 0, 0);
+          } else {
+            const f4v zero = {0.0f, 0.0f, 0.0f, 0.0f};
+            c[n][f] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xf, wf[f], first && v == 0 ? zero : c[n][f], 0, 0, 0);
+          }
+        }
+      }
+    if (GSH >= 0 && last) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc[n][f][j] = fmaf(c[n][f][j], d[f].s[(i >> (GSH < 0 ? 0 : GSH)) & (Quad<W, GSH>::kScales - 1)], acc[n][f][j]);
+    }
+  }
+}
+
+// Orders a wavefront's LDS writes before its later reads of other lanes' data.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Up to 4 tokens (TOK 1 or 4): a workgroup finishes 16*F rows in one launch. Its wavefronts share the columns; each
+// converts its own columns of the tokens, with a power of two of its own, and waits for no other before the sum.
+constexpr int kTinyWaves = 8;
+constexpr int tiny_rounds(size_t size) { return size == 4 ? 4 : 8; }  // granules of 32 bytes or 16 that a lane converts
+
+template <class TX, int TOK, int W, int GSH, int F>
+__global__ __launch_bounds__(64 * kTinyWaves, 4) void k_linear_tiny(LinearArgs a) {
+  constexpr int NX = std::is_same<TX, float>::value ? 2 : 1;
+  constexpr int kRing = W == 8 || F == 2 ? 3 : 4;  // quads of codes in flight
+  extern __shared__ __align__(16) _Float16 xs[];   // per wavefront [NX][its blocks][4][TOK][8]
+  __shared__ float s_sum[kTinyWaves][F][TOK][16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, rt = min(lane & 15, TOK - 1);
+  const int nq = (a.nb + 3) / 4, per = (nq + kTinyWaves - 1) / kTinyWaves;
+  const int qa = min(wave * per, nq), qb = min(qa + per, nq);
+  const int ng = (min(4 * qb, a.nb) - min(4 * qa, a.nb)) * 4;  // granules of a token in the wavefront's columns
+  const int tk = lane % TOK, g0 = lane / TOK;
+  constexpr int kPer = 64 / TOK, kRounds = tiny_rounds(sizeof(TX));
+  Granule<TX> raw[kRounds];
+  const TX* xrow = static_cast<const TX*>(a.x) + (size_t)min(tk, a.T - 1) * a.ldx + (size_t)qa * 128;
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k)
+    if (g0 + k * kPer < ng) load8(xrow + (g0 + k * kPer) * 8, a.vec_x, raw[k]);
+  __builtin_amdgcn_sched_barrier(0);
+  const int out0 = blockIdx.x * (a.half ? 16 : 16 * F);
+  const Rows<W, GSH, F> rows(a, out0, lane);
+  Quad<W, GSH> ring[kRing][F];
+#pragma unroll
+  for (int k = 0; k < kRing; ++k)
+    if (qa + k < qb) rows.load(ring[k], 4 * (qa + k));
+  __builtin_amdgcn_sched_barrier(0);
+  bool finite = true;
+  int sh = 0;
+  if constexpr (!std::is_same<TX, _Float16>::value) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k)
+      if (g0 + k * kPer < ng) amax8<TX>(raw[k], m);
+    m = amax_bits<TX>(m);
+#pragma unroll
+    for (int o = TOK; o < 64; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
+    finite = m < 0x7F800000u;
+    sh = scale_shift(m);
+  }
+  _Float16* x = xs + (size_t)wave * NX * per * 128 * TOK;
+  const int stride = per * 128 * TOK;
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {
+    const int gr = g0 + k * kPer;
+    if (gr < (qb - qa) * 16) {
+      h8 hi = {}, lo = {};
+      if (gr < ng) convert8<TX>(raw[k], sh, finite, hi, lo);
+      *reinterpret_cast<h8*>(x + (gr * TOK + tk) * 8) = hi;
+      if (NX == 2) *reinterpret_cast<h8*>(x + stride + (gr * TOK + tk) * 8) = lo;
+    }
+  }
+  wave_sync();
+  f4v acc[1][F];
+#pragma unroll
+  for (int f = 0; f < F; ++f) acc[0][f] = f4v{0.0f, 0.0f, 0.0f, 0.0f};
+  auto multiply = [&](Quad<W, GSH> (&d)[F], int q) __attribute__((always_inline)) {
+    multiply_quad<NX, 1, TOK, W, GSH, F>(d, x + (q - qa) * 128 * TOK, stride, rt, g, acc);
+  };
+  int q0 = qa;
+  for (; q0 + kRing < qb; q0 += kRing) {
+#pragma unroll
+    for (int k = 0; k < kRing; ++k) {
+      multiply(ring[k], q0 + k);
+      rows.load(ring[k], 4 * min(q0 + k + kRing, qb - 1));
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kRing; ++k)
+    if (q0 + k < qb) multiply(ring[k], q0 + k);
+  // lane group 0 holds the real tokens: row r, token j; token j's power of two is in lane j
+#pragma unroll
+  for (int j = 0; j < TOK; ++j) {
+    const int back = -__builtin_amdgcn_readlane(sh, j);
+    if (g == 0)
+#pragma unroll
+      for (int f = 0; f < F; ++f) s_sum[wave][f][j][lane] = ldexpf(acc[0][f][j], back);
+  }
+  __syncthreads();
+  if (threadIdx.x >= 16 * TOK) return;
+  const int j = threadIdx.x >> 4, r = threadIdx.x & 15;
+  if (j >= a.T) return;
+  float v[F];
+#pragma unroll
+  for (int f = 0; f < F; ++f) {
+    v[f] = s_sum[0][f][j][r];
+#pragma unroll
+    for (int w = 1; w < kTinyWaves; ++w) v[f] += s_sum[w][f][j][r];  // columns in ascending order
+    const int row = a.half ? f * a.half + out0 + r : out0 + 16 * f + r;
+    if (GSH < 0) v[f] *= a.scales[row];
+  }
+  if (a.half) {
+    finish<TX>(a, j, out0 + r, v[0], v[F - 1]);
+  } else {
+#pragma unroll
+    for (int f = 0; f < F; ++f) finish<TX>(a, j, out0 + 16 * f + r, v[f], 0.0f);
+  }
+}
+
+// Up to 64 tokens: a workgroup takes 128 rows (64 gate and 64 up) over a part of the columns, because every workgroup
+// reads and converts the activations of its columns; four wavefronts of 32 rows for each half of them. Parts are added
+// by k_linear_join.
+constexpr int kSlimRowWaves = 4, kSlimColWaves = 2, kSlimLanes = 64 * kSlimRowWaves * kSlimColWaves;
+constexpr int kSlimRounds = 8;  // granules that a lane converts, over all token fragments
+
+template <class TX, int NT, int W, int GSH>
+__global__ __launch_bounds__(kSlimLanes, 2) void k_linear_slim(LinearArgs a, int kblocks, float* __restrict__ part) {
+  constexpr int NX = std::is_same<TX, float>::value ? 2 : 1, F = 2, RW = kSlimRowWaves;
+  constexpr int kPer = kSlimLanes / 16, kRounds = kSlimRounds / NT, kRing = 3;
+  extern __shared__ __align__(16) _Float16 xs[];  // [NX][NT][nq * 4 blocks][4][16][8]; later the second half's sums
+  __shared__ uint32_t s_max[kSlimLanes / 64][NT * 16];
+  __shared__ int s_sh[NT * 16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+  const int rw = wave % RW, kw = wave / RW;
+  const int b0 = blockIdx.y * kblocks, nblk = min(kblocks, a.nb - b0), nq = (nblk + 3) / 4;
+
+  const int tk = threadIdx.x & 15, g0 = threadIdx.x >> 4, ng = nblk * 4;
+  Granule<TX> raw[NT][kRounds];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const TX* row = static_cast<const TX*>(a.x) + (size_t)min(16 * n + tk, a.T - 1) * a.ldx + (size_t)b0 * 32;
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k)
+      if (g0 + k * kPer < ng) load8(row + (g0 + k * kPer) * 8, a.vec_x, raw[n][k]);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  const int out0 = (blockIdx.x * RW + rw) * (a.half ? 16 : 32);
+  const bool any = out0 < (a.half ? a.half : a.N);
+  const Rows<W, GSH, F> rows(a, out0, lane);
+  const int per = (nq + kSlimColWaves - 1) / kSlimColWaves;
+  const int qa = min(kw * per, nq), qb = min(qa + per, nq);  // this wavefront's quads
+  Quad<W, GSH> ring[kRing][F];
+#pragma unroll
+  for (int k = 0; k < kRing; ++k)
+    if (qa + k < qb) rows.load(ring[k], b0 + 4 * (qa + k));
+  __builtin_amdgcn_sched_barrier(0);
+
+  bool finite[NT];
+  int sh[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) finite[n] = true, sh[n] = 0;
+  if constexpr (!std::is_same<TX, _Float16>::value) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int k = 0; k < kRounds; ++k)
+        if (g0 + k * kPer < ng) amax8<TX>(raw[n][k], m);
+      m = amax_bits<TX>(m);
+      m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+      m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+      if (lane < 16) s_max[wave][n * 16 + tk] = m;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int w = 0; w < kSlimLanes / 64; ++w) m = max(m, s_max[w][n * 16 + tk]);
+      finite[n] = m < 0x7F800000u;
+      sh[n] = scale_shift(m);
+    }
+  }
+  if (g0 == 0)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) s_sh[n * 16 + tk] = sh[n];
+  const int stride = nq * 2048;  // halfs of a token fragment
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+      const int gr = g0 + k * kPer;
+      if (gr < nq * 16) {
+        h8 hi = {}, lo = {};
+        if (gr < ng) convert8<TX>(raw[n][k], sh[n], finite[n], hi, lo);
+        *reinterpret_cast<h8*>(xs + n * stride + (gr * 16 + tk) * 8) = hi;
+        if (NX == 2) *reinterpret_cast<h8*>(xs + (NT + n) * stride + (gr * 16 + tk) * 8) = lo;
+      }
+    }
+  __syncthreads();
+
+  f4v acc[NT][F];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int f = 0; f < F; ++f) acc[n][f] = f4v{0.0f, 0.0f, 0.0f, 0.0f};
+  auto multiply = [&](Quad<W, GSH> (&d)[F], int q) __attribute__((always_inline)) {
+    multiply_quad<NX, NT, 16, W, GSH, F>(d, xs + q * 2048, stride, r, g, acc);
+  };
+  int q0 = qa;
+  for (; q0 + kRing < qb; q0 += kRing) {
+#pragma unroll
+    for (int k = 0; k < kRing; ++k) {
+      multiply(ring[k], q0 + k);
+      rows.load(ring[k], b0 + 4 * min(q0 + k + kRing, qb - 1));
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kRing; ++k)
+    if (q0 + k < qb) multiply(ring[k], q0 + k);
+
+  // first half of the columns plus second
+  f4v* sums = reinterpret_cast<f4v*>(xs);  // [RW][NT][F][64 lanes]
+  __syncthreads();
+  if (kw > 0) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int f = 0; f < F; ++f) sums[((rw * NT + n) * F + f) * 64 + lane] = acc[n][f];
+  }
+  __syncthreads();
+  if (kw > 0 || !any) return;
+  float rs[F];
+#pragma unroll
+  for (int f = 0; f < F; ++f) rs[f] = GSH < 0 ? *rows.scale[f] : 1.0f;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int f = 0; f < F; ++f) acc[n][f] += sums[((rw * NT + n) * F + f) * 64 + lane];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = 16 * n + 4 * g + j;
+      if (t >= a.T) continue;
+      const int back = -s_sh[t];
+      float v[F];
+#pragma unroll
+      for (int f = 0; f < F; ++f) v[f] = ldexpf(acc[n][f][j] * rs[f], back);
+      if (part) {
+#pragma unroll
+        for (int f = 0; f < F; ++f) part[((size_t)blockIdx.y * a.T + t) * a.N + rows.row[f]] = v[f];
+      } else if (a.half) {
+        finish<TX>(a, t, rows.row[0], v[0], v[1]);
+      } else {
+#pragma unroll
+        for (int f = 0; f < F; ++f) finish<TX>(a, t, rows.row[f], v[f], 0.0f);
+      }
+    }
+  }
+}
+
+// Adds the parts in ascending order and finishes; one output a lane, kJoinLoads parts read at once.
+constexpr int kJoinLoads = 16;
+template <class TX>
+__global__ __launch_bounds__(256) void k_linear_join(LinearArgs a, const float* __restrict__ part, int parts) {
+  const int out = a.half ? a.half : a.N;
+  const int col = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
+  if (col >= out) return;
+  const size_t step = (size_t)a.T * a.N;
+  const float* p = part + (size_t)t * a.N + col;
+  float v = 0.0f, u = 0.0f;
+  for (int k0 = 0; k0 < parts; k0 += kJoinLoads) {
+    float b[kJoinLoads], c[kJoinLoads];
+#pragma unroll
+    for (int k = 0; k < kJoinLoads; ++k) {
+      const size_t at = (size_t)min(k0 + k, parts - 1) * step;
+      b[k] = p[at];
+      if (a.half) c[k] = p[at + a.half];
+    }
+#pragma unroll
+    for (int k = 0; k < kJoinLoads; ++k)
+      if (k0 + k < parts) {
+        v += b[k];
+        if (a.half) u += c[k];
+      }
+  }
+  finish<TX>(a, t, col, v, u);
+}
+
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// Up to this many tokens the codes' way through memory counts more than the products.
+constexpr int kSlimTokens = 64;
+constexpr int kTinyTokens = 4;
+constexpr int kSlimGroups = 256;  // workgroups wanted: one per compute unit
+
+// up to 4 tokens whose columns fit the lanes' rounds, and the activations 64 KB; size: bytes of an activation
+bool tiny_fits(int64_t T, int K, int size) {
+  const int tok = T == 1 ? 1 : kTinyTokens, quads = (K / 32 + 3) / 4, per = (quads + kTinyWaves - 1) / kTinyWaves;
+  return T <= kTinyTokens && per * 16 * tok <= tiny_rounds(size) * 64 &&
+         kTinyWaves * per * 256 * tok * (size == 4 ? 2 : 1) <= 64 << 10;
+}
+int slim_frags(int64_t T) { return T <= 16 ? 1 : T <= 32 ? 2 : 4; }
+
+// Columns are cut so that about kSlimGroups workgroups run, in parts of whole quads of blocks that the lanes' rounds
+// cover.
+struct SlimPlan {
+  int kblocks, parts;
+};
+SlimPlan slim_plan(int N, int nb, int nt) {
+  const int groups = (N + 127) / 128, quads = (nb + 3) / 4;
+  const int most = kSlimRounds / nt * (kSlimLanes / 16) / 16;
+  int parts = std::max(1, std::min(quads, kSlimGroups / groups));
+  const int per = std::min((quads + parts - 1) / parts, most);
+  parts = (quads + per - 1) / per;
+  return {per * 4, parts};
+}
 
 struct LinearPlan {
   size_t xh, xl, sh, total;
@@ -275,9 +795,59 @@ LinearPlan linear_plan(int K, int64_t T) {
   p.total = p.sh + up256((size_t)T * 4);
   return p;
 }
+size_t slim_bytes(int N, int K, int64_t T) {
+  const SlimPlan s = slim_plan(N, K / 32, slim_frags(T));
+  return s.parts > 1 ? (size_t)s.parts * T * N * 4 : 0;
+}
+
+template <class TX, int TOK, int F, int W, int GSH>
+void tiny_launch(const LinearArgs& a, hipStream_t st) {
+  constexpr int NX = std::is_same<TX, float>::value ? 2 : 1;
+  const int quads = (a.nb + 3) / 4, per = (quads + kTinyWaves - 1) / kTinyWaves;
+  const int rows = a.half ? a.half / 16 : a.N / (16 * F);
+  k_linear_tiny<TX, TOK, W, GSH, F><<<rows, 64 * kTinyWaves, (size_t)kTinyWaves * per * 256 * TOK * NX, st>>>(a);
+}
+template <class TX, int NT, int W, int GSH>
+void slim_launch(const LinearArgs& a, float* ws, hipStream_t st) {
+  constexpr int NX = std::is_same<TX, float>::value ? 2 : 1;
+  const SlimPlan s = slim_plan(a.N, a.nb, NT);
+  const int nq = std::min(s.kblocks / 4, (a.nb + 3) / 4);
+  const size_t lds = std::max((size_t)NX * NT * nq * 4096, (size_t)kSlimRowWaves * NT * 2 * 64 * 16);
+  const int out = a.half ? a.half : a.N, per = a.half ? 64 : 128;
+  float* part = s.parts > 1 ? ws : nullptr;
+  k_linear_slim<TX, NT, W, GSH><<<dim3((out + per - 1) / per, s.parts), kSlimLanes, lds, st>>>(a, s.kblocks, part);
+  if (part) k_linear_join<TX><<<dim3((out + 255) / 256, a.T), 256, 0, st>>>(a, part, s.parts);
+}
+template <class TX, int W, int GSH>
+void few_tokens(const LinearArgs& a, float* ws, hipStream_t st) {
+  if (tiny_fits(a.T, a.K, sizeof(TX))) {
+    if (a.T == 1) {
+      if (a.half) tiny_launch<TX, 1, 2, W, GSH>(a, st);
+      else tiny_launch<TX, 1, 1, W, GSH>(a, st);
+    } else {
+      if (a.half) tiny_launch<TX, kTinyTokens, 2, W, GSH>(a, st);
+      else tiny_launch<TX, kTinyTokens, 1, W, GSH>(a, st);
+    }
+  } else if (a.T <= 16) {
+    slim_launch<TX, 1, W, GSH>(a, ws, st);
+  } else if (a.T <= 32) {
+    slim_launch<TX, 2, W, GSH>(a, ws, st);
+  } else {
+    slim_launch<TX, 4, W, GSH>(a, ws, st);
+  }
+}
 
 template <class TX>
-void linear_launch(const LinearArgs& a, int bits, hipStream_t st) {
+void linear_launch(const LinearArgs& a, int bits, void* ws, hipStream_t st) {
+  if (a.T <= kSlimTokens) {
+    float* p = static_cast<float*>(ws);
+    if (bits == 8) few_tokens<TX, 8, -1>(a, p, st);
+    else if (a.gshift < 0) few_tokens<TX, 4, -1>(a, p, st);
+    else if (a.gshift == 0) few_tokens<TX, 4, 0>(a, p, st);
+    else if (a.gshift == 1) few_tokens<TX, 4, 1>(a, p, st);
+    else few_tokens<TX, 4, 2>(a, p, st);
+    return;
+  }
   k_linear_x<TX><<<(a.T + 31) / 32 * 4, 256, 0, st>>>(a);
   const int cols = a.half ? a.half / 32 : a.N / 64;
   const dim3 grid((cols + 3) / 4, (a.T + 31) / 32);
@@ -288,7 +858,12 @@ void linear_launch(const LinearArgs& a, int bits, hipStream_t st) {
 
 }  // namespace
 
-size_t linear_ws_bytes(const moe_linear_config& c, int64_t T) { return linear_plan(c.cols, T).total; }
+// for any number of tokens up to T
+size_t linear_ws_bytes(const moe_linear_config& c, int64_t T) {
+  size_t b = T > kSlimTokens ? linear_plan(c.cols, T).total : 256;
+  for (int64_t t : {(int64_t)16, (int64_t)32, (int64_t)kSlimTokens}) b = std::max(b, slim_bytes(c.rows, c.cols, std::min(t, T)));
+  return b;
+}
 
 hipError_t launch_linear(const moe_linear_config& c, const uint8_t* codes, const float* scales, const float* bias,
                          const void* x, int64_t ldx, int T, int dtype, const void* res, int64_t ldr, void* y,
@@ -301,6 +876,8 @@ hipError_t launch_linear(const moe_linear_config& c, const uint8_t* codes, const
   a.nbp = (a.nb + 1) & ~1;
   a.half = c.act == MOE_ACT_SWIGLU ? c.rows / 2 : 0;
   a.act = c.act;
+  const size_t elem = dtype == MOE_DTYPE_F32 ? 4 : 2;
+  a.vec_x = aligned16(x) && (size_t)ldx * elem % 16 == 0;
   a.gshift = -1;
   if (c.group_size > 0)
     for (a.gshift = 0; (32 << a.gshift) < c.group_size;) ++a.gshift;
@@ -319,9 +896,9 @@ hipError_t launch_linear(const moe_linear_config& c, const uint8_t* codes, const
   a.xl = reinterpret_cast<_Float16*>(w + p.xl);
   a.sh = reinterpret_cast<int32_t*>(w + p.sh);
   const int bits = c.weight_bits == 8 ? 8 : 4;
-  if (dtype == MOE_DTYPE_F32) linear_launch<float>(a, bits, st);
-  else if (dtype == MOE_DTYPE_BF16) linear_launch<bf16_t>(a, bits, st);
-  else linear_launch<_Float16>(a, bits, st);
+  if (dtype == MOE_DTYPE_F32) linear_launch<float>(a, bits, ws, st);
+  else if (dtype == MOE_DTYPE_BF16) linear_launch<bf16_t>(a, bits, ws, st);
+  else linear_launch<_Float16>(a, bits, ws, st);
   return hipGetLastError();
 }
 
