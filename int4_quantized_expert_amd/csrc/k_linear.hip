@@ -32,6 +32,7 @@ struct LinearArgs {
   int32_t T, N, K, nb, nbp;  // tokens, weight rows, columns, 32-blocks of a row, blocks padded to a multiple of 2
   int32_t half;              // rows of the gate part (SwiGLU), else 0
   int32_t vec_x;             // rows of x start on 16-byte boundaries
+  int32_t vec_r, vec_y;      // rows of the residual and of y on boundaries of four elements
   int32_t act, gshift;       // gshift: log2(group / 32), -1 for one scale a row
   const uint8_t* codes;
   const float* scales;
@@ -139,45 +140,59 @@ __device__ __forceinline__ void convert8(const Granule<TX>& d, int sh, bool fini
 
 // ------------------------------------------------------------ activations to fp16 in tile order
 // One workgroup takes 8 tokens: thread = (token tid % 8, granule of 8 elements tid / 8), so 8 neighbouring threads
-// write 128 contiguous bytes and each token is read in runs of 32 granules.
+// write 128 contiguous bytes and each token is read in runs of 128 granules. Up to 8 granules a thread (8192 columns)
+// stay in registers between the search for the largest and the conversion; of longer rows the rest is read twice.
+constexpr int kPrepLanes = 128, kPrepRounds = 8;
 template <class TX>
-__global__ __launch_bounds__(256) void k_linear_x(LinearArgs a) {
-  __shared__ uint32_t s_max[32][8];
+__global__ __launch_bounds__(8 * kPrepLanes) void k_linear_x(LinearArgs a) {
+  __shared__ uint32_t s_max[16][8];
   const int tk = threadIdx.x & 7, g0 = threadIdx.x >> 3;
   const int t = blockIdx.x * 8 + tk;
   const bool in = t < a.T;
   const TX* row = static_cast<const TX*>(a.x) + (size_t)(in ? t : 0) * a.ldx;
-  const int ng = a.K / 8;
-  constexpr bool kScaled = !std::is_same<TX, _Float16>::value;
+  const int ng = in ? a.K / 8 : 0;
+  Granule<TX> raw[kPrepRounds];
+#pragma unroll
+  for (int k = 0; k < kPrepRounds; ++k)
+    if (g0 + k * kPrepLanes < ng) load8(row + (g0 + k * kPrepLanes) * 8, a.vec_x, raw[k]);
   int sh = 0;
   bool finite = true;
-  if (kScaled) {
+  if constexpr (!std::is_same<TX, _Float16>::value) {
     uint32_t m = 0;
-    if (in)
-      for (int g = g0; g < ng; g += 32) {
-        Granule<TX> v;
-        load8(row + g * 8, a.vec_x, v);
-        amax8<TX>(v, m);
-      }
+#pragma unroll
+    for (int k = 0; k < kPrepRounds; ++k)
+      if (g0 + k * kPrepLanes < ng) amax8<TX>(raw[k], m);
+    for (int g = g0 + kPrepRounds * kPrepLanes; g < ng; g += kPrepLanes) {
+      Granule<TX> v;
+      load8(row + g * 8, a.vec_x, v);
+      amax8<TX>(v, m);
+    }
     m = amax_bits<TX>(m);
-    s_max[g0][tk] = m;
+#pragma unroll
+    for (int o = 8; o < 64; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
+    if ((threadIdx.x & 63) < 8) s_max[threadIdx.x >> 6][tk] = m;
     __syncthreads();
-    for (int i = 0; i < 32; ++i) m = max(m, s_max[i][tk]);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, s_max[i][tk]);
     finite = m < 0x7F800000u;
     sh = scale_shift(m);
   }
   if (in && g0 == 0) a.sh[t] = sh;
   const size_t base = (size_t)(t >> 5) * a.nbp * 1024 + (size_t)(t & 31) * 8;
-  for (int g = g0; g < a.nbp * 4; g += 32) {
+  auto store = [&](int g, const Granule<TX>& v) __attribute__((always_inline)) {
     h8 hi = {}, lo = {};
-    if (in && g < ng) {
-      Granule<TX> v;
-      load8(row + g * 8, a.vec_x, v);
-      convert8<TX>(v, sh, finite, hi, lo);
-    }
+    if (g < ng) convert8<TX>(v, sh, finite, hi, lo);
     const size_t at = base + (size_t)g * 256;  // g = block * 4 + slice
     *reinterpret_cast<h8*>(a.xh + at) = hi;
     if (std::is_same<TX, float>::value) *reinterpret_cast<h8*>(a.xl + at) = lo;
+  };
+#pragma unroll
+  for (int k = 0; k < kPrepRounds; ++k)
+    if (g0 + k * kPrepLanes < a.nbp * 4) store(g0 + k * kPrepLanes, raw[k]);
+  for (int g = g0 + kPrepRounds * kPrepLanes; g < a.nbp * 4; g += kPrepLanes) {
+    Granule<TX> v = {};
+    if (g < ng) load8(row + g * 8, a.vec_x, v);
+    store(g, v);
   }
 }
 
@@ -231,29 +246,123 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int t, int col, floa
   static_cast<TX*>(a.y)[(size_t)t * a.ldy + col] = from_f32<TX>(v);
 }
 
+// Four neighbouring outputs of token t, already converted back by 2^back.
+template <class TX>
+__device__ __forceinline__ void finish4(const LinearArgs& a, int t, int col, int back, const float* gate, const float* up) {
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = ldexpf(gate[i], back);
+  if (a.bias)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += a.bias[col + i];
+  if (a.act == MOE_ACT_SWIGLU) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float s, miss, u = ldexpf(up[i], back);
+      if (a.bias) u += a.bias[a.half + col + i];
+      sigmoid2(v[i], s, miss);
+      v[i] = v[i] * s * u;
+    }
+  } else if (a.act != MOE_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = activate(v[i], a.act);
+  }
+  struct alignas(4 * sizeof(TX)) Four {
+    TX v[4];
+  };
+  if (a.res) {
+    const TX* p = static_cast<const TX*>(a.res) + (size_t)t * a.ldr + col;
+    Four r;
+    if (a.vec_r) r = *reinterpret_cast<const Four*>(p);
+    else
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.v[i] = p[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += to_f32<TX>(r.v[i]);
+  }
+  TX* p = static_cast<TX*>(a.y) + (size_t)t * a.ldy + col;
+  Four o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o.v[i] = from_f32<TX>(v[i]);
+  if (a.vec_y) *reinterpret_cast<Four*>(p) = o;
+  else
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = o.v[i];
+}
+
 // ------------------------------------------------------------ product
 // A wavefront multiplies 32*TT tokens by two fragments of 32 weight rows (64 consecutive rows; with SwiGLU 32 gate
-// rows and the 32 up rows that go with them) with v_mfma_f32_32x32x16_f16. Four wavefronts of a workgroup share the
-// tokens, whose activations pass through LDS; each reads its own codes from memory into registers.
+// rows and the 32 up rows that go with them) with v_mfma_f32_32x32x16_f16; four wavefronts of a workgroup take the same
+// tokens. A code fragment costs 10 vector instructions to unpack and serves TT matrix instructions of 8 passes, so
+// with TT = 4 the unpacking hides behind them.
+// The activations of a step (two blocks of columns) pass through LDS in two buffers: the next step's are loaded to
+// registers while this one is multiplied. Each wavefront reads its own codes from memory into registers, also a step
+// ahead.
 // Lane l: token / weight row l % 32, half g = l / 32 of a block. Result: weight row l % 32, tokens
-// 8*(i/4) + 4*g + i%4.
-template <class TX, int TT, int W, bool GS>
-__global__ __launch_bounds__(256) void k_linear_tile(LinearArgs a) {
+// 8*(i/4) + 4*g + i%4. GSH: -1 one scale a row, 0 groups of one block, 1 groups of two blocks or more.
+constexpr int kOutRow = 260;  // floats of a token's row of results in LDS: 256 and a shift of four banks
+template <class TX, int TT>
+constexpr size_t tile_lds() {
+  return std::max<size_t>(2 * TT * (std::is_same<TX, float>::value ? 2 : 1) * 4096, 16 * kOutRow * 4);
+}
+
+template <class TX, int TT, int W, int GSH>
+__device__ __forceinline__ void tile_run(const LinearArgs& a, int row_tile, int t0, int p0, int p1, char* s_mem,
+                                         float* __restrict__ part) {
   constexpr int NX = std::is_same<TX, float>::value ? 2 : 1;
-  constexpr int kStep = TT * NX * 2 * 1024;  // halfs of a block pair: [NX][TT][2 blocks][4 slices][32][8]
-  __shared__ __align__(16) _Float16 s_x[kStep];
+  constexpr int kStep = NX * TT * 2048;  // halfs of a step: [NX][TT][2 blocks][4 slices][32][8]
+  auto s_x = reinterpret_cast<_Float16(*)[kStep]>(s_mem);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 31, g = lane >> 5;
   const int cols = a.half ? a.half / 32 : a.N / 64;  // wavefront tiles over the outputs
-  const int wt = blockIdx.x * 4 + wave;
-  const int t0 = blockIdx.y * 32 * TT;
-  const int wtc = min(wt, cols - 1);
+  const int wt = row_tile * 4 + wave, wtc = min(wt, cols - 1);
   int row[2];
   row[0] = a.half ? wtc * 32 + r : wtc * 64 + r;
   row[1] = a.half ? a.half + wtc * 32 + r : wtc * 64 + 32 + r;
   const uint8_t* src[2];
+  const float* ssrc[2];
+  const int groups = GSH >= 0 ? a.nb >> a.gshift : 0;
 #pragma unroll
-  for (int f = 0; f < 2; ++f)
+  for (int f = 0; f < 2; ++f) {
     src[f] = a.codes + tbw_off<W>(row[f] / 64, 0, a.nb) + (size_t)(row[f] % 64) * (4 * W);
+    ssrc[f] = a.scales + (GSH >= 0 ? (size_t)(row[f] / 64) * groups * 64 + row[f] % 64 : (size_t)row[f]);
+  }
+  // this lane's 16 bytes of each [2 blocks][4 slices][32][8] chunk
+  const _Float16* xsrc[TT];
+#pragma unroll
+  for (int tt = 0; tt < TT; ++tt)
+    xsrc[tt] = a.xh + (size_t)min(t0 / 32 + tt, (a.T - 1) / 32) * a.nbp * 1024 + threadIdx.x * 8;
+  const size_t low = a.xl - a.xh;
+  constexpr int kScales = GSH == 0 ? 2 : 1;
+  u4v xn[NX][TT];  // the next step's
+  uint32_t wn[2][W];
+  float sn[2][kScales];
+  auto fetch = [&](int p) __attribute__((always_inline)) {
+#pragma unroll
+    for (int n = 0; n < NX; ++n)
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt)
+        xn[n][tt] = *reinterpret_cast<const u4v*>(xsrc[tt] + n * low + (size_t)p * 2048);
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      const u4v* q = reinterpret_cast<const u4v*>(src[f] + (size_t)min(2 * p + g, a.nb - 1) * kTileBlock<W>);
+#pragma unroll
+      for (int i = 0; i < W / 4; ++i) {
+        const u4v v = q[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) wn[f][4 * i + j] = v[j];
+      }
+      if constexpr (GSH >= 0)
+#pragma unroll
+        for (int i = 0; i < kScales; ++i) sn[f][i] = ssrc[f][(size_t)(min(2 * p + i, a.nb - 1) >> a.gshift) * 64];
+    }
+  };
+  auto put = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int n = 0; n < NX; ++n)
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt)
+        *reinterpret_cast<u4v*>(&s_x[buf][((n * TT + tt) * 256 + threadIdx.x) * 8]) = xn[n][tt];
+  };
   f16v acc[TT][2];
 #pragma unroll
   for (int tt = 0; tt < TT; ++tt)
@@ -261,94 +370,148 @@ __global__ __launch_bounds__(256) void k_linear_tile(LinearArgs a) {
     for (int f = 0; f < 2; ++f)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[tt][f][i] = 0.0f;
-  const int groups = GS ? a.nb >> a.gshift : 0;
-  for (int b = 0; b < a.nbp; b += 2) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kStep / 8; i += 256) {
-      const int n = i / (TT * 256), tt = i / 256 % TT, rest = i % 256;
-      const int tg = min(t0 / 32 + tt, (a.T - 1) / 32);
-      const _Float16* p = (n ? a.xl : a.xh) + ((size_t)tg * a.nbp + b) * 1024 + (size_t)rest * 8;
-      *reinterpret_cast<h8*>(s_x + (size_t)i * 8) = *reinterpret_cast<const h8*>(p);
-    }
-    __syncthreads();
-    u4v w[2][W / 4];
+  fetch(p0);
+  put(0);
+  __syncthreads();
+  for (int p = p0; p < p1; ++p) {
+    const _Float16* x = s_x[(p - p0) & 1];
+    uint32_t w[2][W];
+    float sc[2][kScales];
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
-      const u4v* p = reinterpret_cast<const u4v*>(src[f] + (size_t)min(b + g, a.nb - 1) * kTileBlock<W>);
 #pragma unroll
-      for (int i = 0; i < W / 4; ++i) w[f][i] = p[i];
-      // half g of both blocks instead of all of block b + g
+      for (int i = 0; i < W; ++i) w[f][i] = wn[f][i];
+      if constexpr (GSH >= 0)
+#pragma unroll
+        for (int i = 0; i < kScales; ++i) sc[f][i] = sn[f][i];
+      // half g of both blocks instead of all of block 2p + g
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) {
-        constexpr int hv = W / 4 - 1, ho = W == 4 ? 2 : 0;
-        const auto sw = __builtin_amdgcn_permlane32_swap(w[f][0][i], w[f][hv][i + ho], false, false);
-        w[f][0][i] = sw[0];
-        w[f][hv][i + ho] = sw[1];
+        const auto sw = __builtin_amdgcn_permlane32_swap(w[f][i], w[f][i + W / 2], false, false);
+        w[f][i] = sw[0];
+        w[f][i + W / 2] = sw[1];
       }
     }
+    const bool more = p + 1 < p1;
+    if (more) fetch(p + 1);
+    h8 wf[2][2][2];  // [block][m][fragment]
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {  // block b + h
-      h8 wf[2][2];
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int f = 0; f < 2; ++f)
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-          wf[f][m] = W == 4 ? codes_h8(w[f][0][2 * h + m]) : codes_h8(w[f][h & (W / 4 - 1)][2 * m], w[f][h & (W / 4 - 1)][2 * m + 1]);
-      float sc[2];
-      if (GS) {
-        const int gi = min(b + h, a.nb - 1) >> a.gshift;
-#pragma unroll
-        for (int f = 0; f < 2; ++f) sc[f] = a.scales[((size_t)(row[f] / 64) * groups + gi) * 64 + row[f] % 64];
-      }
-#pragma unroll
-      for (int tt = 0; tt < TT; ++tt)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-          f16v c;
-          if (GS) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) c[i] = 0.0f;
-          } else {
-            c = acc[tt][f];
-          }
-#pragma unroll
-          for (int n = 0; n < NX; ++n)
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              const h8 xf = *reinterpret_cast<const h8*>(
-                  s_x + ((size_t)((n * TT + tt) * 2 + h) * 4 + 2 * g + m) * 256 + r * 8);
-              c = __builtin_amdgcn_mfma_f32_32x32x16_f16(xf, wf[f][m], c, 0, 0, 0);
-            }
-          if (GS) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[tt][f][i] = fmaf(c[i], sc[f], acc[tt][f][i]);
-          } else {
-            acc[tt][f] = c;
-          }
+          if constexpr (W == 4) wf[h][m][f] = codes_h8(w[f][2 * h + m]);
+          else wf[h][m][f] = codes_h8(w[f][4 * h + 2 * m], w[f][4 * h + 2 * m + 1]);
         }
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) {
+      f16v c[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int n = 0; n < NX; ++n) {
+            const h8 xf = *reinterpret_cast<const h8*>(x + (((n * TT + tt) * 2 + h) * 4 + 2 * g + m) * 256 + r * 8);
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              if constexpr (GSH < 0) {
+                acc[tt][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xf, wf[h][m][f], acc[tt][f], 0, 0, 0);
+              } else {
+                const bool first = m == 0 && n == 0 && (GSH == 0 || h == 0);
+                f16v zero;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) zero[i] = 0.0f;
+                c[f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xf, wf[h][m][f], first ? zero : c[f], 0, 0, 0);
+              }
+            }
+          }
+        if constexpr (GSH >= 0)
+          if (GSH == 0 || h == 1)
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) acc[tt][f][i] = fmaf(c[f][i], sc[f][h & (kScales - 1)], acc[tt][f][i]);
+      }
     }
+    if (more) put((p + 1 - p0) & 1);
+    __syncthreads();
   }
-  if (wt >= cols) return;
   float rs[2] = {1.0f, 1.0f};
-  if (!GS) {
-    rs[0] = a.scales[row[0]];
-    rs[1] = a.scales[row[1]];
+  if (GSH < 0) rs[0] = *ssrc[0], rs[1] = *ssrc[1];
+  if (part) {
+    if (wt >= cols) return;
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int t = t0 + 32 * tt + 8 * (i >> 2) + 4 * g + (i & 3);
+        if (t >= a.T) continue;
+        const int back = -a.sh[t];
+        float* q = part + (size_t)t * a.N;
+        q[row[0]] = ldexpf(acc[tt][0][i] * rs[0], back);
+        q[row[1]] = ldexpf(acc[tt][1][i] * rs[1], back);
+      }
+    return;
   }
+  // results through LDS, 16 tokens at a time, so that they are finished and stored four neighbours a lane
+  float* s_out = reinterpret_cast<float*>(s_mem);
+  const int at0 = a.half ? wave * 32 + r : wave * 64 + r, at1 = a.half ? 128 + at0 : 32 + at0;
+  const int quads = a.half ? 32 : 64, col0 = row_tile * quads * 4, out = a.half ? a.half : a.N;
 #pragma unroll
   for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int t = t0 + 32 * tt + 8 * (i >> 2) + 4 * g + (i & 3);
-      if (t >= a.T) continue;
-      const int sh = -a.sh[t];
-      const float v0 = ldexpf(acc[tt][0][i] * rs[0], sh), v1 = ldexpf(acc[tt][1][i] * rs[1], sh);
-      if (a.half) {
-        finish<TX>(a, t, wt * 32 + r, v0, v1);
-      } else {
-        finish<TX>(a, t, row[0], v0, 0.0f);
-        finish<TX>(a, t, row[1], v1, 0.0f);
+    for (int hh = 0; hh < 2; ++hh) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int tk = 8 * (i >> 2) + 4 * g + (i & 3);
+        s_out[tk * kOutRow + at0] = acc[tt][0][8 * hh + i] * rs[0];
+        s_out[tk * kOutRow + at1] = acc[tt][1][8 * hh + i] * rs[1];
+      }
+      __syncthreads();
+      for (int k = threadIdx.x; k < 16 * quads; k += 256) {
+        const int tk = k / quads, c = k % quads * 4, t = t0 + 32 * tt + 16 * hh + tk;
+        if (t < a.T && col0 + c < out)
+          finish4<TX>(a, t, col0 + c, -a.sh[t], s_out + tk * kOutRow + c, s_out + tk * kOutRow + 128 + c);
       }
     }
+}
+
+// Tiles of 32*TT tokens by 256 rows. The first `whole` of them take a workgroup each; the others, which would leave
+// part of the card idle in the last turn, are done in halves of 16*TT tokens by two workgroups.
+// Workgroups go to the eight dies in turn: die d takes the d-th eighth of the tiles, in an order that walks 8 row
+// tiles by all token tiles, so that what a die works on at a time shares its cache.
+constexpr int kTileRowGroup = 8, kDies = 8;
+__device__ __forceinline__ int die_order(int id, int n) {
+  const int d = id % kDies, q = n / kDies, m = n % kDies;
+  return d * q + min(d, m) + id / kDies;
+}
+
+template <class TX, int TT, int W, int GSH>
+__global__ __launch_bounds__(256, 2) void k_linear_tile(LinearArgs a, int row_tiles, int tok_tiles, int whole, int pairs,
+                                                        float* __restrict__ part) {
+  __shared__ __align__(16) char s_mem[tile_lds<TX, TT>()];
+  const int tiles = row_tiles * tok_tiles, bid = blockIdx.x;
+  int id, half = -1;
+  if (bid < whole) {
+    id = die_order(bid, whole);
+  } else {
+    const int k = die_order(bid - whole, 2 * (tiles - whole));
+    id = whole + (k >> 1);
+    half = k & 1;
+  }
+  const int group = id / (kTileRowGroup * tok_tiles), in_group = id - group * kTileRowGroup * tok_tiles;
+  const int rows_in = min(kTileRowGroup, row_tiles - group * kTileRowGroup);
+  const int row_tile = group * kTileRowGroup + in_group % rows_in, t0 = in_group / rows_in * 32 * TT;
+  const int p0 = blockIdx.y * pairs, p1 = min(p0 + pairs, a.nbp / 2);
+  if (part) part += (size_t)blockIdx.y * a.T * a.N;
+  if (half < 0) {
+    tile_run<TX, TT, W, GSH>(a, row_tile, t0, p0, p1, s_mem, part);
+  } else if (TT > 1 && t0 + half * 16 * TT < a.T) {
+    tile_run<TX, (TT > 1 ? TT / 2 : 1), W, GSH>(a, row_tile, t0 + half * 16 * TT, p0, p1, s_mem, part);
+  }
 }
 
 // ------------------------------------------------------------ few tokens: product
@@ -782,6 +945,30 @@ SlimPlan slim_plan(int N, int nb, int nt) {
   return {per * 4, parts};
 }
 
+// More tokens: tiles of 32*tt tokens by 256 rows, two workgroups on a compute unit at a time (three where registers
+// allow). tt: 4, or 2 where a tile
+// of 128 tokens needs too many registers (fp32 activations: two halves of each; group scales: a second set of sums).
+// The tiles that do not fill a whole turn of the card are halved if the halves do not need more than a turn.
+template <class TX, int GSH>
+constexpr int tile_frags() {
+  return std::is_same<TX, float>::value || GSH >= 0 ? 2 : 4;
+}
+template <class TX, int GSH>
+constexpr int tile_slots() {
+  return std::is_same<TX, float>::value && GSH < 0 ? 768 : 512;
+}
+struct TilePlan {
+  int row_tiles, tok_tiles, whole;
+};
+TilePlan tile_plan(int N, int tt, int slots, int64_t T) {
+  TilePlan p;
+  p.row_tiles = (N + 255) / 256;
+  p.tok_tiles = (int)((T + 32 * tt - 1) / (32 * tt));
+  const int tiles = p.row_tiles * p.tok_tiles, rest = tiles % slots;
+  p.whole = tt > 1 && rest <= slots / 2 ? tiles - rest : tiles;
+  return p;
+}
+
 struct LinearPlan {
   size_t xh, xl, sh, total;
 };
@@ -837,6 +1024,14 @@ void few_tokens(const LinearArgs& a, float* ws, hipStream_t st) {
   }
 }
 
+template <class TX, int W, int GSH>
+void tile_launch(const LinearArgs& a, hipStream_t st) {
+  constexpr int TT = tile_frags<TX, GSH>();
+  const TilePlan p = tile_plan(a.N, TT, tile_slots<TX, GSH>(), a.T);
+  const int blocks = p.whole + 2 * (p.row_tiles * p.tok_tiles - p.whole);
+  k_linear_tile<TX, TT, W, GSH><<<blocks, 256, 0, st>>>(a, p.row_tiles, p.tok_tiles, p.whole, a.nbp / 2, nullptr);
+}
+
 template <class TX>
 void linear_launch(const LinearArgs& a, int bits, void* ws, hipStream_t st) {
   if (a.T <= kSlimTokens) {
@@ -848,12 +1043,11 @@ void linear_launch(const LinearArgs& a, int bits, void* ws, hipStream_t st) {
     else few_tokens<TX, 4, 2>(a, p, st);
     return;
   }
-  k_linear_x<TX><<<(a.T + 31) / 32 * 4, 256, 0, st>>>(a);
-  const int cols = a.half ? a.half / 32 : a.N / 64;
-  const dim3 grid((cols + 3) / 4, (a.T + 31) / 32);
-  if (bits == 8) k_linear_tile<TX, 1, 8, false><<<grid, 256, 0, st>>>(a);
-  else if (a.gshift >= 0) k_linear_tile<TX, 1, 4, true><<<grid, 256, 0, st>>>(a);
-  else k_linear_tile<TX, 1, 4, false><<<grid, 256, 0, st>>>(a);
+  k_linear_x<TX><<<(a.T + 31) / 32 * 4, 8 * kPrepLanes, 0, st>>>(a);
+  if (bits == 8) tile_launch<TX, 8, -1>(a, st);
+  else if (a.gshift < 0) tile_launch<TX, 4, -1>(a, st);
+  else if (a.gshift == 0) tile_launch<TX, 4, 0>(a, st);
+  else tile_launch<TX, 4, 1>(a, st);
 }
 
 }  // namespace
@@ -878,6 +1072,8 @@ hipError_t launch_linear(const moe_linear_config& c, const uint8_t* codes, const
   a.act = c.act;
   const size_t elem = dtype == MOE_DTYPE_F32 ? 4 : 2;
   a.vec_x = aligned16(x) && (size_t)ldx * elem % 16 == 0;
+  a.vec_r = reinterpret_cast<uintptr_t>(res) % (4 * elem) == 0 && ldr % 4 == 0;
+  a.vec_y = reinterpret_cast<uintptr_t>(y) % (4 * elem) == 0 && ldy % 4 == 0;
   a.gshift = -1;
   if (c.group_size > 0)
     for (a.gshift = 0; (32 << a.gshift) < c.group_size;) ++a.gshift;
