@@ -301,50 +301,60 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, int t, int col, int
 // Lane l: token / weight row l % 32, half g = l / 32 of a block. Result: weight row l % 32, tokens
 // 8*(i/4) + 4*g + i%4. GSH: -1 one scale a row, 0 groups of one block, 1 groups of two blocks or more.
 constexpr int kOutRow = 260;  // floats of a token's row of results in LDS: 256 and a shift of four banks
-template <class TX, int TT>
+template <class TX, int TT, int KW>
 constexpr size_t tile_lds() {
-  return std::max<size_t>(2 * TT * (std::is_same<TX, float>::value ? 2 : 1) * 4096, 16 * kOutRow * 4);
+  return std::max<size_t>({(size_t)KW * 2 * TT * (std::is_same<TX, float>::value ? 2 : 1) * 4096,
+                           (size_t)(KW / 2) * 32 * 1024, (size_t)16 * kOutRow * 4});
 }
 
-template <class TX, int TT, int W, int GSH>
-__device__ __forceinline__ void tile_run(const LinearArgs& a, int row_tile, int t0, int p0, int p1, char* s_mem,
-                                         float* __restrict__ part) {
+// KW: groups of four wavefronts that share the columns.
+template <class TX, int TT, int W, int GSH, int KW>
+__device__ __forceinline__ void tile_run(const LinearArgs& a, int row_tile, int t0, char* s_mem) {
   constexpr int NX = std::is_same<TX, float>::value ? 2 : 1;
   constexpr int kStep = NX * TT * 2048;  // halfs of a step: [NX][TT][2 blocks][4 slices][32][8]
-  auto s_x = reinterpret_cast<_Float16(*)[kStep]>(s_mem);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 31, g = lane >> 5;
+  // values that are equal in a wavefront are made so for the compiler: addresses are then a scalar base and a lane's
+  // constant offset, without vector arithmetic in the loop
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, wave = wv & 3, r = lane & 31, g = lane >> 5;
+  const int kw = wv >> 2, tid = threadIdx.x & 255;
+  auto s_x = reinterpret_cast<_Float16(*)[kStep]>(s_mem) + kw * 2;
+  const int steps = (a.nbp / 2 + KW - 1) / KW, p0 = min(kw * steps, a.nbp / 2), p1 = min(p0 + steps, a.nbp / 2);
   const int cols = a.half ? a.half / 32 : a.N / 64;  // wavefront tiles over the outputs
-  const int wt = row_tile * 4 + wave, wtc = min(wt, cols - 1);
-  int row[2];
-  row[0] = a.half ? wtc * 32 + r : wtc * 64 + r;
-  row[1] = a.half ? a.half + wtc * 32 + r : wtc * 64 + 32 + r;
+  const int wtc = min(row_tile * 4 + wave, cols - 1);
+  int first[2];  // first weight row of a fragment
+  first[0] = a.half ? wtc * 32 : wtc * 64;
+  first[1] = a.half ? a.half + wtc * 32 : wtc * 64 + 32;
   const uint8_t* src[2];
   const float* ssrc[2];
   const int groups = GSH >= 0 ? a.nb >> a.gshift : 0;
 #pragma unroll
   for (int f = 0; f < 2; ++f) {
-    src[f] = a.codes + tbw_off<W>(row[f] / 64, 0, a.nb) + (size_t)(row[f] % 64) * (4 * W);
-    ssrc[f] = a.scales + (GSH >= 0 ? (size_t)(row[f] / 64) * groups * 64 + row[f] % 64 : (size_t)row[f]);
+    src[f] = a.codes + tbw_off<W>(first[f] / 64, 0, a.nb) + (size_t)(first[f] % 64) * (4 * W);
+    ssrc[f] = a.scales + (GSH >= 0 ? (size_t)(first[f] / 64) * groups * 64 + first[f] % 64 : (size_t)first[f]);
   }
-  // this lane's 16 bytes of each [2 blocks][4 slices][32][8] chunk
+  const uint32_t off0 = r * (4 * W), off1 = off0 + g * (uint32_t)kTileBlock<W>;
+  // this workgroup's [2 blocks][4 slices][32][8] chunks, 16 bytes a lane
   const _Float16* xsrc[TT];
 #pragma unroll
-  for (int tt = 0; tt < TT; ++tt)
-    xsrc[tt] = a.xh + (size_t)min(t0 / 32 + tt, (a.T - 1) / 32) * a.nbp * 1024 + threadIdx.x * 8;
+  for (int tt = 0; tt < TT; ++tt) xsrc[tt] = a.xh + (size_t)min(t0 / 32 + tt, (a.T - 1) / 32) * a.nbp * 1024;
   const size_t low = a.xl - a.xh;
   constexpr int kScales = GSH == 0 ? 2 : 1;
-  u4v xn[NX][TT];  // the next step's
-  uint32_t wn[2][W];
-  float sn[2][kScales];
-  auto fetch = [&](int p) __attribute__((always_inline)) {
+  u4v xn[NX][TT];   // activations and
+  uint32_t wn[2][W];  // codes of the next step
+  float sn[2][kScales], sc[2][kScales];
+  h8 wf[2][2][2];  // this step's fragments: [block][m][fragment]
+  auto fetch_x = [&](int p) __attribute__((always_inline)) {
 #pragma unroll
     for (int n = 0; n < NX; ++n)
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt)
-        xn[n][tt] = *reinterpret_cast<const u4v*>(xsrc[tt] + n * low + (size_t)p * 2048);
+        xn[n][tt] = *reinterpret_cast<const u4v*>(xsrc[tt] + n * low + (size_t)p * 2048 + (uint32_t)(tid * 8));
+  };
+  auto fetch_w = [&](int p) __attribute__((always_inline)) {
+    const uint32_t off = 2 * p + 1 < a.nb ? off1 : off0;  // past the last block the activations are zero
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
-      const u4v* q = reinterpret_cast<const u4v*>(src[f] + (size_t)min(2 * p + g, a.nb - 1) * kTileBlock<W>);
+      const u4v* q = reinterpret_cast<const u4v*>(src[f] + (size_t)p * (2 * kTileBlock<W>) + off);
 #pragma unroll
       for (int i = 0; i < W / 4; ++i) {
         const u4v v = q[i];
@@ -353,7 +363,33 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int row_tile, int 
       }
       if constexpr (GSH >= 0)
 #pragma unroll
-        for (int i = 0; i < kScales; ++i) sn[f][i] = ssrc[f][(size_t)(min(2 * p + i, a.nb - 1) >> a.gshift) * 64];
+        for (int i = 0; i < kScales; ++i)
+          sn[f][i] = ssrc[f][(size_t)(min(2 * p + i, a.nb - 1) >> a.gshift) * 64 + (uint32_t)r];
+    }
+  };
+  auto unpack = [&](h8 (&d)[2][2][2], float (&ds)[2][kScales]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      if constexpr (GSH >= 0)
+#pragma unroll
+        for (int j = 0; j < kScales; ++j) ds[f][j] = sn[f][j];
+      uint32_t w[W];
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j] = wn[f][j];
+      // half g of both blocks instead of all of block 2p + g
+#pragma unroll
+      for (int j = 0; j < W / 2; ++j) {
+        const auto sw = __builtin_amdgcn_permlane32_swap(w[j], w[j + W / 2], false, false);
+        w[j] = sw[0];
+        w[j + W / 2] = sw[1];
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          if constexpr (W == 4) d[h][m][f] = codes_h8(w[2 * h + m]);
+          else d[h][m][f] = codes_h8(w[4 * h + 2 * m], w[4 * h + 2 * m + 1]);
+        }
     }
   };
   auto put = [&](int buf) __attribute__((always_inline)) {
@@ -361,7 +397,7 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int row_tile, int 
     for (int n = 0; n < NX; ++n)
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt)
-        *reinterpret_cast<u4v*>(&s_x[buf][((n * TT + tt) * 256 + threadIdx.x) * 8]) = xn[n][tt];
+        *reinterpret_cast<u4v*>(&s_x[buf][((n * TT + tt) * 256 + tid) * 8]) = xn[n][tt];
   };
   f16v acc[TT][2];
 #pragma unroll
@@ -370,40 +406,7 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int row_tile, int 
     for (int f = 0; f < 2; ++f)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[tt][f][i] = 0.0f;
-  fetch(p0);
-  put(0);
-  __syncthreads();
-  for (int p = p0; p < p1; ++p) {
-    const _Float16* x = s_x[(p - p0) & 1];
-    uint32_t w[2][W];
-    float sc[2][kScales];
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-#pragma unroll
-      for (int i = 0; i < W; ++i) w[f][i] = wn[f][i];
-      if constexpr (GSH >= 0)
-#pragma unroll
-        for (int i = 0; i < kScales; ++i) sc[f][i] = sn[f][i];
-      // half g of both blocks instead of all of block 2p + g
-#pragma unroll
-      for (int i = 0; i < W / 2; ++i) {
-        const auto sw = __builtin_amdgcn_permlane32_swap(w[f][i], w[f][i + W / 2], false, false);
-        w[f][i] = sw[0];
-        w[f][i + W / 2] = sw[1];
-      }
-    }
-    const bool more = p + 1 < p1;
-    if (more) fetch(p + 1);
-    h8 wf[2][2][2];  // [block][m][fragment]
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          if constexpr (W == 4) wf[h][m][f] = codes_h8(w[f][2 * h + m]);
-          else wf[h][m][f] = codes_h8(w[f][4 * h + 2 * m], w[f][4 * h + 2 * m + 1]);
-        }
+  auto multiply = [&](const _Float16* x) __attribute__((always_inline)) {
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) {
       f16v c[2];
@@ -422,7 +425,7 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int row_tile, int 
                 const bool first = m == 0 && n == 0 && (GSH == 0 || h == 0);
                 f16v zero;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) zero[i] = 0.0f;
+                for (int j = 0; j < 16; ++j) zero[j] = 0.0f;
                 c[f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xf, wf[h][m][f], first ? zero : c[f], 0, 0, 0);
               }
             }
@@ -432,29 +435,73 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int row_tile, int 
 #pragma unroll
             for (int f = 0; f < 2; ++f)
 #pragma unroll
-              for (int i = 0; i < 16; ++i) acc[tt][f][i] = fmaf(c[f][i], sc[f][h & (kScales - 1)], acc[tt][f][i]);
+              for (int j = 0; j < 16; ++j) acc[tt][f][j] = fmaf(c[f][j], sc[f][h & (kScales - 1)], acc[tt][f][j]);
       }
     }
-    if (more) put((p + 1 - p0) & 1);
+  };
+  if (p0 < p1) {
+    fetch_x(p0);
+    fetch_w(p0);
+    put(0);
+  }
+  if constexpr (TT == 4) {
+    // The next step's codes are unpacked between this step's matrix instructions. Past the last step the fetches repeat
+    // it and their results are not used: the body has no branch, which would keep the two apart. 8,192 tokens
+    // 12288 x 6144: 1,002 us with the unpacking in front, 968 so; with fewer matrix instructions a step it was slower.
+    unpack(wf, sc);
+    fetch_x(min(p0 + 1, p1 - 1));
+    fetch_w(min(p0 + 1, p1 - 1));
     __syncthreads();
+    for (int i = 0; i < steps; ++i, __syncthreads()) {
+      const int p = p0 + i;
+      if (KW > 1 && p >= p1) continue;  // a group with fewer columns
+      h8 wl[2][2][2];
+      float sl[2][kScales];
+      unpack(wl, sl);
+      fetch_w(min(p + 2, p1 - 1));
+      put((i + 1) & 1);
+      fetch_x(min(p + 2, p1 - 1));
+      multiply(s_x[i & 1]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) wf[h][m][f] = wl[h][m][f];
+    }
+  } else {
+    __syncthreads();
+    for (int i = 0; i < steps; ++i, __syncthreads()) {
+      const int p = p0 + i;
+      if (KW > 1 && p >= p1) continue;
+      unpack(wf, sc);
+      const bool more = p + 1 < p1;
+      if (more) {
+        fetch_x(p + 1);
+        fetch_w(p + 1);
+      }
+      multiply(s_x[i & 1]);
+      if (more) put((i + 1) & 1);
+    }
+  }
+  // the groups' sums: the upper half to the lower until one is left, 32 tokens at a time
+#pragma unroll
+  for (int k = KW / 2; k > 0; k >>= 1) {
+    float* s = reinterpret_cast<float*>(s_mem);  // [group][32][256]
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) {
+      if (kw >= k && kw < 2 * k)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[((kw - k) * 32 + i) * 256 + tid] = acc[tt][i >> 4][i & 15];
+      __syncthreads();
+      if (kw < k)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[tt][i >> 4][i & 15] += s[(kw * 32 + i) * 256 + tid];
+      __syncthreads();
+    }
   }
   float rs[2] = {1.0f, 1.0f};
-  if (GSH < 0) rs[0] = *ssrc[0], rs[1] = *ssrc[1];
-  if (part) {
-    if (wt >= cols) return;
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int t = t0 + 32 * tt + 8 * (i >> 2) + 4 * g + (i & 3);
-        if (t >= a.T) continue;
-        const int back = -a.sh[t];
-        float* q = part + (size_t)t * a.N;
-        q[row[0]] = ldexpf(acc[tt][0][i] * rs[0], back);
-        q[row[1]] = ldexpf(acc[tt][1][i] * rs[1], back);
-      }
-    return;
-  }
+  if (GSH < 0) rs[0] = ssrc[0][r], rs[1] = ssrc[1][r];
   // results through LDS, 16 tokens at a time, so that they are finished and stored four neighbours a lane
   float* s_out = reinterpret_cast<float*>(s_mem);
   const int at0 = a.half ? wave * 32 + r : wave * 64 + r, at1 = a.half ? 128 + at0 : 32 + at0;
@@ -464,14 +511,15 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int row_tile, int 
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
       __syncthreads();
+      if (kw == 0)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int tk = 8 * (i >> 2) + 4 * g + (i & 3);
-        s_out[tk * kOutRow + at0] = acc[tt][0][8 * hh + i] * rs[0];
-        s_out[tk * kOutRow + at1] = acc[tt][1][8 * hh + i] * rs[1];
-      }
+        for (int i = 0; i < 8; ++i) {
+          const int tk = 8 * (i >> 2) + 4 * g + (i & 3);
+          s_out[tk * kOutRow + at0] = acc[tt][0][8 * hh + i] * rs[0];
+          s_out[tk * kOutRow + at1] = acc[tt][1][8 * hh + i] * rs[1];
+        }
       __syncthreads();
-      for (int k = threadIdx.x; k < 16 * quads; k += 256) {
+      for (int k = threadIdx.x; k < 16 * quads; k += 256 * KW) {
         const int tk = k / quads, c = k % quads * 4, t = t0 + 32 * tt + 16 * hh + tk;
         if (t < a.T && col0 + c < out)
           finish4<TX>(a, t, col0 + c, -a.sh[t], s_out + tk * kOutRow + c, s_out + tk * kOutRow + 128 + c);
@@ -479,39 +527,26 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int row_tile, int 
     }
 }
 
-// Tiles of 32*TT tokens by 256 rows. The first `whole` of them take a workgroup each; the others, which would leave
-// part of the card idle in the last turn, are done in halves of 16*TT tokens by two workgroups.
-// Workgroups go to the eight dies in turn: die d takes the d-th eighth of the tiles, in an order that walks 8 row
-// tiles by all token tiles, so that what a die works on at a time shares its cache.
+// Tiles of 32*BT tokens by 256 rows, numbered so that 8 row tiles are walked by all token tiles; a launch takes `count`
+// of them from `first` on, each cut into BT / TT workgroups of 32*TT tokens. Workgroups go to the eight dies in turn:
+// die d takes the d-th eighth of a launch, so that what a die works on at a time shares its cache.
 constexpr int kTileRowGroup = 8, kDies = 8;
-__device__ __forceinline__ int die_order(int id, int n) {
-  const int d = id % kDies, q = n / kDies, m = n % kDies;
-  return d * q + min(d, m) + id / kDies;
+template <class TX, int GSH>
+constexpr int base_frags() {  // 128 tokens need too many registers with two halves of them or a second set of sums
+  return std::is_same<TX, float>::value || GSH >= 0 ? 2 : 4;
 }
 
-template <class TX, int TT, int W, int GSH>
-__global__ __launch_bounds__(256, 2) void k_linear_tile(LinearArgs a, int row_tiles, int tok_tiles, int whole, int pairs,
-                                                        float* __restrict__ part) {
-  __shared__ __align__(16) char s_mem[tile_lds<TX, TT>()];
-  const int tiles = row_tiles * tok_tiles, bid = blockIdx.x;
-  int id, half = -1;
-  if (bid < whole) {
-    id = die_order(bid, whole);
-  } else {
-    const int k = die_order(bid - whole, 2 * (tiles - whole));
-    id = whole + (k >> 1);
-    half = k & 1;
-  }
+template <class TX, int TT, int W, int GSH, int KW>
+__global__ __launch_bounds__(256 * KW, KW == 4 ? 4 : 2) void k_linear_tile(LinearArgs a, int row_tiles, int tok_tiles,
+                                                                          int first, int count) {
+  constexpr int BT = base_frags<TX, GSH>(), kCut = BT / TT;
+  __shared__ __align__(16) char s_mem[tile_lds<TX, TT, KW>()];
+  const int n = count * kCut, d = blockIdx.x % kDies, q = n / kDies, m = n % kDies;
+  const int k = d * q + min(d, m) + blockIdx.x / kDies, id = first + k / kCut;
   const int group = id / (kTileRowGroup * tok_tiles), in_group = id - group * kTileRowGroup * tok_tiles;
   const int rows_in = min(kTileRowGroup, row_tiles - group * kTileRowGroup);
-  const int row_tile = group * kTileRowGroup + in_group % rows_in, t0 = in_group / rows_in * 32 * TT;
-  const int p0 = blockIdx.y * pairs, p1 = min(p0 + pairs, a.nbp / 2);
-  if (part) part += (size_t)blockIdx.y * a.T * a.N;
-  if (half < 0) {
-    tile_run<TX, TT, W, GSH>(a, row_tile, t0, p0, p1, s_mem, part);
-  } else if (TT > 1 && t0 + half * 16 * TT < a.T) {
-    tile_run<TX, (TT > 1 ? TT / 2 : 1), W, GSH>(a, row_tile, t0 + half * 16 * TT, p0, p1, s_mem, part);
-  }
+  const int t0 = in_group / rows_in * 32 * BT + k % kCut * 32 * TT;
+  if (t0 < a.T) tile_run<TX, TT, W, GSH, KW>(a, group * kTileRowGroup + in_group % rows_in, t0, s_mem);
 }
 
 // ------------------------------------------------------------ few tokens: product
@@ -945,30 +980,6 @@ SlimPlan slim_plan(int N, int nb, int nt) {
   return {per * 4, parts};
 }
 
-// More tokens: tiles of 32*tt tokens by 256 rows, two workgroups on a compute unit at a time (three where registers
-// allow). tt: 4, or 2 where a tile
-// of 128 tokens needs too many registers (fp32 activations: two halves of each; group scales: a second set of sums).
-// The tiles that do not fill a whole turn of the card are halved if the halves do not need more than a turn.
-template <class TX, int GSH>
-constexpr int tile_frags() {
-  return std::is_same<TX, float>::value || GSH >= 0 ? 2 : 4;
-}
-template <class TX, int GSH>
-constexpr int tile_slots() {
-  return std::is_same<TX, float>::value && GSH < 0 ? 768 : 512;
-}
-struct TilePlan {
-  int row_tiles, tok_tiles, whole;
-};
-TilePlan tile_plan(int N, int tt, int slots, int64_t T) {
-  TilePlan p;
-  p.row_tiles = (N + 255) / 256;
-  p.tok_tiles = (int)((T + 32 * tt - 1) / (32 * tt));
-  const int tiles = p.row_tiles * p.tok_tiles, rest = tiles % slots;
-  p.whole = tt > 1 && rest <= slots / 2 ? tiles - rest : tiles;
-  return p;
-}
-
 struct LinearPlan {
   size_t xh, xl, sh, total;
 };
@@ -1024,12 +1035,39 @@ void few_tokens(const LinearArgs& a, float* ws, hipStream_t st) {
   }
 }
 
+// More tokens. What fills the card twice over (two workgroups on each of 256 compute units) runs in whole tiles of four
+// wavefronts; of what is left, up to 256 tiles run one a compute unit, with eight wavefronts that share the columns, and
+// fewer than that are cut into halves or quarters first.
+constexpr int kUnits = 256;
 template <class TX, int W, int GSH>
 void tile_launch(const LinearArgs& a, hipStream_t st) {
-  constexpr int TT = tile_frags<TX, GSH>();
-  const TilePlan p = tile_plan(a.N, TT, tile_slots<TX, GSH>(), a.T);
-  const int blocks = p.whole + 2 * (p.row_tiles * p.tok_tiles - p.whole);
-  k_linear_tile<TX, TT, W, GSH><<<blocks, 256, 0, st>>>(a, p.row_tiles, p.tok_tiles, p.whole, a.nbp / 2, nullptr);
+  constexpr int BT = base_frags<TX, GSH>(), KQ = GSH >= 0 ? 2 : 4;
+  const int row_tiles = (a.N + 255) / 256, tok_tiles = (a.T + 32 * BT - 1) / (32 * BT);
+  const int tiles = row_tiles * tok_tiles;
+  for (int at = 0, left; (left = tiles - at) > 0;) {
+    if constexpr (BT == 4) {
+      if (left >= 2 * kUnits) {
+        const int n = left / (2 * kUnits) * (2 * kUnits);
+        k_linear_tile<TX, 4, W, GSH, 1><<<n, 256, 0, st>>>(a, row_tiles, tok_tiles, at, n);
+        at += n;
+      } else if (left > kUnits / 2) {
+        const int n = std::min(left, kUnits);
+        k_linear_tile<TX, 4, W, GSH, 2><<<n, 512, 0, st>>>(a, row_tiles, tok_tiles, at, n);
+        at += n;
+      } else if (left > kUnits / 4) {
+        k_linear_tile<TX, 2, W, GSH, 2><<<2 * left, 512, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+        at += left;
+      } else {
+        k_linear_tile<TX, 1, W, GSH, KQ><<<4 * left, 256 * KQ, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+        at += left;
+      }
+    } else {
+      if (left > kUnits) k_linear_tile<TX, 2, W, GSH, 1><<<left, 256, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+      else if (left > kUnits / 2) k_linear_tile<TX, 2, W, GSH, 2><<<left, 512, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+      else k_linear_tile<TX, 1, W, GSH, KQ><<<2 * left, 256 * KQ, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+      at += left;
+    }
+  }
 }
 
 template <class TX>
