@@ -301,26 +301,28 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, int t, int col, int
 // Lane l: token / weight row l % 32, half g = l / 32 of a block. Result: weight row l % 32, tokens
 // 8*(i/4) + 4*g + i%4. GSH: -1 one scale a row, 0 groups of one block, 1 groups of two blocks or more.
 constexpr int kOutRow = 260;  // floats of a token's row of results in LDS: 256 and a shift of four banks
-template <class TX, int TT, int KW>
+template <class TX, int TT, int RW, int KW>
 constexpr size_t tile_lds() {
   return std::max<size_t>({(size_t)KW * 2 * TT * (std::is_same<TX, float>::value ? 2 : 1) * 4096,
-                           (size_t)(KW / 2) * 32 * 1024, (size_t)16 * kOutRow * 4});
+                           (size_t)(KW / 2) * RW * 8 * 1024, (size_t)16 * kOutRow * 4});
 }
 
-// KW: groups of four wavefronts that share the columns.
-template <class TX, int TT, int W, int GSH, int KW>
-__device__ __forceinline__ void tile_run(const LinearArgs& a, int row_tile, int t0, char* s_mem) {
+// KW groups of RW wavefronts: a group's wavefronts take 64 rows each, from wavefront tile wt0 on, the groups share the
+// columns.
+template <class TX, int TT, int W, int GSH, int RW, int KW>
+__device__ __forceinline__ void tile_run(const LinearArgs& a, int wt0, int t0, char* s_mem) {
   constexpr int NX = std::is_same<TX, float>::value ? 2 : 1;
   constexpr int kStep = NX * TT * 2048;  // halfs of a step: [NX][TT][2 blocks][4 slices][32][8]
   // values that are equal in a wavefront are made so for the compiler: addresses are then a scalar base and a lane's
   // constant offset, without vector arithmetic in the loop
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63, wave = wv & 3, r = lane & 31, g = lane >> 5;
-  const int kw = wv >> 2, tid = threadIdx.x & 255;
+  constexpr int kLanes = 64 * RW;  // of a group
+  const int lane = threadIdx.x & 63, wave = wv % RW, r = lane & 31, g = lane >> 5;
+  const int kw = wv / RW, tid = threadIdx.x % kLanes;
   auto s_x = reinterpret_cast<_Float16(*)[kStep]>(s_mem) + kw * 2;
   const int steps = (a.nbp / 2 + KW - 1) / KW, p0 = min(kw * steps, a.nbp / 2), p1 = min(p0 + steps, a.nbp / 2);
   const int cols = a.half ? a.half / 32 : a.N / 64;  // wavefront tiles over the outputs
-  const int wtc = min(row_tile * 4 + wave, cols - 1);
+  const int wtc = min(wt0 + wave, cols - 1);
   int first[2];  // first weight row of a fragment
   first[0] = a.half ? wtc * 32 : wtc * 64;
   first[1] = a.half ? a.half + wtc * 32 : wtc * 64 + 32;
@@ -339,7 +341,8 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int row_tile, int 
   for (int tt = 0; tt < TT; ++tt) xsrc[tt] = a.xh + (size_t)min(t0 / 32 + tt, (a.T - 1) / 32) * a.nbp * 1024;
   const size_t low = a.xl - a.xh;
   constexpr int kScales = GSH == 0 ? 2 : 1;
-  u4v xn[NX][TT];   // activations and
+  constexpr int kXs = 4 / RW;  // 16-byte loads of a lane and chunk
+  u4v xn[NX][TT][kXs];  // activations and
   uint32_t wn[2][W];  // codes of the next step
   float sn[2][kScales], sc[2][kScales];
   h8 wf[2][2][2];  // this step's fragments: [block][m][fragment]
@@ -348,7 +351,10 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int row_tile, int 
     for (int n = 0; n < NX; ++n)
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt)
-        xn[n][tt] = *reinterpret_cast<const u4v*>(xsrc[tt] + n * low + (size_t)p * 2048 + (uint32_t)(tid * 8));
+#pragma unroll
+        for (int j = 0; j < kXs; ++j)
+          xn[n][tt][j] =
+              *reinterpret_cast<const u4v*>(xsrc[tt] + n * low + (size_t)p * 2048 + (uint32_t)((j * kLanes + tid) * 8));
   };
   auto fetch_w = [&](int p) __attribute__((always_inline)) {
     const uint32_t off = 2 * p + 1 < a.nb ? off1 : off0;  // past the last block the activations are zero
@@ -397,7 +403,9 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int row_tile, int 
     for (int n = 0; n < NX; ++n)
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt)
-        *reinterpret_cast<u4v*>(&s_x[buf][((n * TT + tt) * 256 + tid) * 8]) = xn[n][tt];
+#pragma unroll
+        for (int j = 0; j < kXs; ++j)
+          *reinterpret_cast<u4v*>(&s_x[buf][((n * TT + tt) * 256 + j * kLanes + tid) * 8]) = xn[n][tt][j];
   };
   f16v acc[TT][2];
 #pragma unroll
@@ -487,16 +495,16 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int row_tile, int 
   // the groups' sums: the upper half to the lower until one is left, 32 tokens at a time
 #pragma unroll
   for (int k = KW / 2; k > 0; k >>= 1) {
-    float* s = reinterpret_cast<float*>(s_mem);  // [group][32][256]
+    float* s = reinterpret_cast<float*>(s_mem);  // [group][32][kLanes]
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) {
       if (kw >= k && kw < 2 * k)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s[((kw - k) * 32 + i) * 256 + tid] = acc[tt][i >> 4][i & 15];
+        for (int i = 0; i < 32; ++i) s[((kw - k) * 32 + i) * kLanes + tid] = acc[tt][i >> 4][i & 15];
       __syncthreads();
       if (kw < k)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) acc[tt][i >> 4][i & 15] += s[(kw * 32 + i) * 256 + tid];
+        for (int i = 0; i < 32; ++i) acc[tt][i >> 4][i & 15] += s[(kw * 32 + i) * kLanes + tid];
       __syncthreads();
     }
   }
@@ -504,8 +512,8 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int row_tile, int 
   if (GSH < 0) rs[0] = ssrc[0][r], rs[1] = ssrc[1][r];
   // results through LDS, 16 tokens at a time, so that they are finished and stored four neighbours a lane
   float* s_out = reinterpret_cast<float*>(s_mem);
-  const int at0 = a.half ? wave * 32 + r : wave * 64 + r, at1 = a.half ? 128 + at0 : 32 + at0;
-  const int quads = a.half ? 32 : 64, col0 = row_tile * quads * 4, out = a.half ? a.half : a.N;
+  const int at0 = a.half ? wave * 32 + r : wave * 64 + r, at1 = 32 * (a.half ? RW : 1) + at0;
+  const int quads = (a.half ? 8 : 16) * RW, col0 = wt0 * (a.half ? 32 : 64), out = a.half ? a.half : a.N;
 #pragma unroll
   for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
@@ -519,16 +527,17 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int row_tile, int 
           s_out[tk * kOutRow + at1] = acc[tt][1][8 * hh + i] * rs[1];
         }
       __syncthreads();
-      for (int k = threadIdx.x; k < 16 * quads; k += 256 * KW) {
+      for (int k = threadIdx.x; k < 16 * quads; k += kLanes * KW) {
         const int tk = k / quads, c = k % quads * 4, t = t0 + 32 * tt + 16 * hh + tk;
         if (t < a.T && col0 + c < out)
-          finish4<TX>(a, t, col0 + c, -a.sh[t], s_out + tk * kOutRow + c, s_out + tk * kOutRow + 128 + c);
+          finish4<TX>(a, t, col0 + c, -a.sh[t], s_out + tk * kOutRow + c,
+                      s_out + tk * kOutRow + 32 * RW + c);
       }
     }
 }
 
 // Tiles of 32*BT tokens by 256 rows, numbered so that 8 row tiles are walked by all token tiles; a launch takes `count`
-// of them from `first` on, each cut into BT / TT workgroups of 32*TT tokens. Workgroups go to the eight dies in turn:
+// of them from `first` on, each cut into BT / TT by 4 / RW workgroups of 32*TT tokens and 64*RW rows. Workgroups go to the eight dies in turn:
 // die d takes the d-th eighth of a launch, so that what a die works on at a time shares its cache.
 constexpr int kTileRowGroup = 8, kDies = 8;
 template <class TX, int GSH>
@@ -536,17 +545,19 @@ constexpr int base_frags() {  // 128 tokens need too many registers with two hal
   return std::is_same<TX, float>::value || GSH >= 0 ? 2 : 4;
 }
 
-template <class TX, int TT, int W, int GSH, int KW>
-__global__ __launch_bounds__(256 * KW, KW == 4 ? 4 : 2) void k_linear_tile(LinearArgs a, int row_tiles, int tok_tiles,
-                                                                          int first, int count) {
-  constexpr int BT = base_frags<TX, GSH>(), kCut = BT / TT;
-  __shared__ __align__(16) char s_mem[tile_lds<TX, TT, KW>()];
-  const int n = count * kCut, d = blockIdx.x % kDies, q = n / kDies, m = n % kDies;
-  const int k = d * q + min(d, m) + blockIdx.x / kDies, id = first + k / kCut;
+template <class TX, int TT, int W, int GSH, int RW, int KW>
+__global__ __launch_bounds__(64 * RW * KW, RW * KW == 16 ? 4 : 2) void k_linear_tile(LinearArgs a, int row_tiles,
+                                                                                     int tok_tiles, int first,
+                                                                                     int count) {
+  constexpr int BT = base_frags<TX, GSH>(), kToks = BT / TT, kRows = 4 / RW;  // the cut of a tile
+  __shared__ __align__(16) char s_mem[tile_lds<TX, TT, RW, KW>()];
+  const int n = count * kToks * kRows, d = blockIdx.x % kDies, q = n / kDies, m = n % kDies;
+  const int k = d * q + min(d, m) + blockIdx.x / kDies, id = first + k / (kToks * kRows);
   const int group = id / (kTileRowGroup * tok_tiles), in_group = id - group * kTileRowGroup * tok_tiles;
   const int rows_in = min(kTileRowGroup, row_tiles - group * kTileRowGroup);
-  const int t0 = in_group / rows_in * 32 * BT + k % kCut * 32 * TT;
-  if (t0 < a.T) tile_run<TX, TT, W, GSH, KW>(a, group * kTileRowGroup + in_group % rows_in, t0, s_mem);
+  const int t0 = in_group / rows_in * 32 * BT + k % kToks * 32 * TT;
+  const int wt0 = (group * kTileRowGroup + in_group % rows_in) * 4 + k / kToks % kRows * RW;
+  if (t0 < a.T && wt0 * (a.half ? 32 : 64) < (a.half ? a.half : a.N)) tile_run<TX, TT, W, GSH, RW, KW>(a, wt0, t0, s_mem);
 }
 
 // ------------------------------------------------------------ few tokens: product
@@ -782,9 +793,9 @@ __global__ __launch_bounds__(64 * kTinyWaves, 4) void k_linear_tiny(LinearArgs a
   }
 }
 
-// Up to 64 tokens: a workgroup takes 128 rows (64 gate and 64 up) over a part of the columns, because every workgroup
-// reads and converts the activations of its columns; four wavefronts of 32 rows for each half of them. Parts are added
-// by k_linear_join.
+// More: a workgroup takes 128 rows (64 gate and 64 up) by 16*NT tokens over a part of the columns, because every
+// workgroup reads and converts the activations of its columns; four wavefronts of 32 rows for each half of them. Parts
+// are added by k_linear_join.
 constexpr int kSlimRowWaves = 4, kSlimColWaves = 2, kSlimLanes = 64 * kSlimRowWaves * kSlimColWaves;
 constexpr int kSlimRounds = 8;  // granules that a lane converts, over all token fragments
 
@@ -799,11 +810,13 @@ __global__ __launch_bounds__(kSlimLanes, 2) void k_linear_slim(LinearArgs a, int
   const int rw = wave % RW, kw = wave / RW;
   const int b0 = blockIdx.y * kblocks, nblk = min(kblocks, a.nb - b0), nq = (nblk + 3) / 4;
 
+  const int t0 = blockIdx.z * 16 * NT;
+
   const int tk = threadIdx.x & 15, g0 = threadIdx.x >> 4, ng = nblk * 4;
   Granule<TX> raw[NT][kRounds];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const TX* row = static_cast<const TX*>(a.x) + (size_t)min(16 * n + tk, a.T - 1) * a.ldx + (size_t)b0 * 32;
+    const TX* row = static_cast<const TX*>(a.x) + (size_t)min(t0 + 16 * n + tk, a.T - 1) * a.ldx + (size_t)b0 * 32;
 #pragma unroll
     for (int k = 0; k < kRounds; ++k)
       if (g0 + k * kPer < ng) load8(row + (g0 + k * kPer) * 8, a.vec_x, raw[n][k]);
@@ -904,9 +917,9 @@ __global__ __launch_bounds__(kSlimLanes, 2) void k_linear_slim(LinearArgs a, int
     for (int f = 0; f < F; ++f) acc[n][f] += sums[((rw * NT + n) * F + f) * 64 + lane];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int t = 16 * n + 4 * g + j;
+      const int tt = 16 * n + 4 * g + j, t = t0 + tt;
       if (t >= a.T) continue;
-      const int back = -s_sh[t];
+      const int back = -s_sh[tt];
       float v[F];
 #pragma unroll
       for (int f = 0; f < F; ++f) v[f] = ldexpf(acc[n][f][j] * rs[f], back);
@@ -953,10 +966,14 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearArgs a, const float* 
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// Up to this many tokens the codes' way through memory counts more than the products.
-constexpr int kSlimTokens = 64;
+// Where the codes' way through memory, and having enough workgroups, counts more than the products: up to 32 tokens, and
+// up to kSlimWork tokens times rows, at which the tiles below take as long (64 tokens x 6144 rows: 16 us over 2048
+// columns either way, 32 and 29 over 6144; 192 x 2048: 16 either way, 30 and 30).
+constexpr int kSlimTokens = 32;
+constexpr int64_t kSlimWork = 3 << 17;
 constexpr int kTinyTokens = 4;
 constexpr int kSlimGroups = 256;  // workgroups wanted: one per compute unit
+bool is_slim(int64_t T, int N) { return T <= kSlimTokens || T * N <= kSlimWork; }
 
 // up to 4 tokens whose columns fit the lanes' rounds, and the activations 64 KB; size: bytes of an activation
 bool tiny_fits(int64_t T, int K, int size) {
@@ -964,15 +981,15 @@ bool tiny_fits(int64_t T, int K, int size) {
   return T <= kTinyTokens && per * 16 * tok <= tiny_rounds(size) * 64 &&
          kTinyWaves * per * 256 * tok * (size == 4 ? 2 : 1) <= 64 << 10;
 }
-int slim_frags(int64_t T) { return T <= 16 ? 1 : T <= 32 ? 2 : 4; }
+int slim_frags(int64_t T) { return T <= 16 ? 1 : 2; }
 
 // Columns are cut so that about kSlimGroups workgroups run, in parts of whole quads of blocks that the lanes' rounds
 // cover.
 struct SlimPlan {
   int kblocks, parts;
 };
-SlimPlan slim_plan(int N, int nb, int nt) {
-  const int groups = (N + 127) / 128, quads = (nb + 3) / 4;
+SlimPlan slim_plan(int N, int nb, int nt, int64_t T) {
+  const int groups = (N + 127) / 128 * (int)((T + 16 * nt - 1) / (16 * nt)), quads = (nb + 3) / 4;
   const int most = kSlimRounds / nt * (kSlimLanes / 16) / 16;
   int parts = std::max(1, std::min(quads, kSlimGroups / groups));
   const int per = std::min((quads + parts - 1) / parts, most);
@@ -994,7 +1011,7 @@ LinearPlan linear_plan(int K, int64_t T) {
   return p;
 }
 size_t slim_bytes(int N, int K, int64_t T) {
-  const SlimPlan s = slim_plan(N, K / 32, slim_frags(T));
+  const SlimPlan s = slim_plan(N, K / 32, slim_frags(T), T);
   return s.parts > 1 ? (size_t)s.parts * T * N * 4 : 0;
 }
 
@@ -1008,12 +1025,12 @@ void tiny_launch(const LinearArgs& a, hipStream_t st) {
 template <class TX, int NT, int W, int GSH>
 void slim_launch(const LinearArgs& a, float* ws, hipStream_t st) {
   constexpr int NX = std::is_same<TX, float>::value ? 2 : 1;
-  const SlimPlan s = slim_plan(a.N, a.nb, NT);
+  const SlimPlan s = slim_plan(a.N, a.nb, NT, a.T);
   const int nq = std::min(s.kblocks / 4, (a.nb + 3) / 4);
   const size_t lds = std::max((size_t)NX * NT * nq * 4096, (size_t)kSlimRowWaves * NT * 2 * 64 * 16);
   const int out = a.half ? a.half : a.N, per = a.half ? 64 : 128;
   float* part = s.parts > 1 ? ws : nullptr;
-  k_linear_slim<TX, NT, W, GSH><<<dim3((out + per - 1) / per, s.parts), kSlimLanes, lds, st>>>(a, s.kblocks, part);
+  k_linear_slim<TX, NT, W, GSH><<<dim3((out + per - 1) / per, s.parts, (a.T + 16 * NT - 1) / (16 * NT)), kSlimLanes, lds, st>>>(a, s.kblocks, part);
   if (part) k_linear_join<TX><<<dim3((out + 255) / 256, a.T), 256, 0, st>>>(a, part, s.parts);
 }
 template <class TX, int W, int GSH>
@@ -1028,10 +1045,8 @@ void few_tokens(const LinearArgs& a, float* ws, hipStream_t st) {
     }
   } else if (a.T <= 16) {
     slim_launch<TX, 1, W, GSH>(a, ws, st);
-  } else if (a.T <= 32) {
-    slim_launch<TX, 2, W, GSH>(a, ws, st);
   } else {
-    slim_launch<TX, 4, W, GSH>(a, ws, st);
+    slim_launch<TX, 2, W, GSH>(a, ws, st);
   }
 }
 
@@ -1048,23 +1063,28 @@ void tile_launch(const LinearArgs& a, hipStream_t st) {
     if constexpr (BT == 4) {
       if (left >= 2 * kUnits) {
         const int n = left / (2 * kUnits) * (2 * kUnits);
-        k_linear_tile<TX, 4, W, GSH, 1><<<n, 256, 0, st>>>(a, row_tiles, tok_tiles, at, n);
+        k_linear_tile<TX, 4, W, GSH, 4, 1><<<n, 256, 0, st>>>(a, row_tiles, tok_tiles, at, n);
         at += n;
       } else if (left > kUnits / 2) {
         const int n = std::min(left, kUnits);
-        k_linear_tile<TX, 4, W, GSH, 2><<<n, 512, 0, st>>>(a, row_tiles, tok_tiles, at, n);
+        k_linear_tile<TX, 4, W, GSH, 4, 2><<<n, 512, 0, st>>>(a, row_tiles, tok_tiles, at, n);
         at += n;
       } else if (left > kUnits / 4) {
-        k_linear_tile<TX, 2, W, GSH, 2><<<2 * left, 512, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+        k_linear_tile<TX, 2, W, GSH, 4, 2><<<2 * left, 512, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+        at += left;
+      } else if (left > kUnits / 8) {
+        k_linear_tile<TX, 1, W, GSH, 4, 4><<<4 * left, 1024, 0, st>>>(a, row_tiles, tok_tiles, at, left);
         at += left;
       } else {
-        k_linear_tile<TX, 1, W, GSH, KQ><<<4 * left, 256 * KQ, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+        k_linear_tile<TX, 1, W, GSH, 2, 8><<<8 * left, 1024, 0, st>>>(a, row_tiles, tok_tiles, at, left);
         at += left;
       }
     } else {
-      if (left > kUnits) k_linear_tile<TX, 2, W, GSH, 1><<<left, 256, 0, st>>>(a, row_tiles, tok_tiles, at, left);
-      else if (left > kUnits / 2) k_linear_tile<TX, 2, W, GSH, 2><<<left, 512, 0, st>>>(a, row_tiles, tok_tiles, at, left);
-      else k_linear_tile<TX, 1, W, GSH, KQ><<<2 * left, 256 * KQ, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+      if (left >= 2 * kUnits) k_linear_tile<TX, 2, W, GSH, 4, 1><<<left, 256, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+      else if (left > kUnits) k_linear_tile<TX, 1, W, GSH, 4, 1><<<2 * left, 256, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+      else if (left > kUnits / 2) k_linear_tile<TX, 2, W, GSH, 4, 2><<<left, 512, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+      else if (left > kUnits / 4) k_linear_tile<TX, 1, W, GSH, 4, KQ><<<2 * left, 256 * KQ, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+      else k_linear_tile<TX, 1, W, GSH, 2, 2 * KQ><<<4 * left, 256 * KQ, 0, st>>>(a, row_tiles, tok_tiles, at, left);
       at += left;
     }
   }
@@ -1072,7 +1092,7 @@ void tile_launch(const LinearArgs& a, hipStream_t st) {
 
 template <class TX>
 void linear_launch(const LinearArgs& a, int bits, void* ws, hipStream_t st) {
-  if (a.T <= kSlimTokens) {
+  if (is_slim(a.T, a.N)) {
     float* p = static_cast<float*>(ws);
     if (bits == 8) few_tokens<TX, 8, -1>(a, p, st);
     else if (a.gshift < 0) few_tokens<TX, 4, -1>(a, p, st);
@@ -1092,8 +1112,10 @@ void linear_launch(const LinearArgs& a, int bits, void* ws, hipStream_t st) {
 
 // for any number of tokens up to T
 size_t linear_ws_bytes(const moe_linear_config& c, int64_t T) {
-  size_t b = T > kSlimTokens ? linear_plan(c.cols, T).total : 256;
-  for (int64_t t : {(int64_t)16, (int64_t)32, (int64_t)kSlimTokens}) b = std::max(b, slim_bytes(c.rows, c.cols, std::min(t, T)));
+  size_t b = is_slim(T, c.rows) ? 256 : linear_plan(c.cols, T).total;
+  const int64_t most = std::min(T, std::max<int64_t>(kSlimTokens, kSlimWork / c.rows));
+  b = std::max(b, slim_bytes(c.rows, c.cols, std::min<int64_t>(T, 16)));
+  for (int64_t t = 32; t < most + 32; t += 32) b = std::max(b, slim_bytes(c.rows, c.cols, std::min(t, most)));
   return b;
 }
 

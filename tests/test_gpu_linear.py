@@ -81,6 +81,44 @@ def test_whole_numbers_are_exact(T, N, K, bits, group, dtype):
     assert torch.equal(y.cpu(), torch.from_numpy(want.astype(np.float32)).to(DT[dtype]))
 
 
+# Enough tiles for each way in which larger batches are laid out over the card: whole turns of 512 tiles of 128 x 256, up
+# to 256 with wavefronts that share the columns, halves and quarters; with 64-token tiles (fp32, group scales) the same.
+BATCHES = [(1024, 16384, 64), (600, 8128, 96), (300, 8192, 160), (191, 6080, 352), (70, 6144, 1056), (520, 16320, 32),
+           (1700, 11072, 128), (193, 4160, 96), (33, 12352, 544)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("bits,group,act", [(4, 0, "none"), (8, 0, "none"), (4, 32, "none"), (4, 128, "none"), (4, 0, "relu")])
+@pytest.mark.parametrize("T,N,K", BATCHES)
+def test_whole_numbers_are_exact_in_large_batches(T, N, K, bits, group, act, dtype):
+    K = (K + group - 1) // group * group if group else K
+    rng = np.random.default_rng(T + N + K)
+    q, s, codes, scales = _weights(rng, N, K, bits, group, whole=True)
+    x, x64 = _x(rng, T, K, dtype, whole=True)
+    y = _call(moe.LinearConfig(N, K, bits, group, ACT[act]), codes, scales, x, N)
+    wt = torch.from_numpy(q * np.repeat(s, K // s.shape[1], axis=1)).to(DEV)
+    want = torch.mm(torch.from_numpy(x64).to(DEV), wt.t().contiguous())
+    want = want.clamp(min=0) if act == "relu" else want
+    assert torch.equal(y, want.float().to(DT[dtype]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,N,K,bits,group", [(1024, 16384, 64, 4, 0), (600, 8064, 96, 8, 0), (300, 8192, 160, 4, 0),
+                                              (191, 6080, 352, 4, 0), (520, 16320, 128, 4, 128), (33, 12352, 544, 4, 32)])
+def test_swiglu_in_large_batches(T, N, K, bits, group, dtype):
+    rng = np.random.default_rng(T + N + K)
+    q, s, codes, scales = _weights(rng, N, K, bits, group)
+    x, x64 = _x(rng, T, K, dtype)
+    b = rng.normal(0, 0.5, N).astype(np.float32)
+    res = torch.from_numpy(rng.normal(0, 1, (T, N // 2)).astype(np.float32)).to(DT[dtype])
+    y = _call(moe.LinearConfig(N, K, bits, group, ACT["swiglu"]), codes, scales, x, N // 2, torch.from_numpy(b).to(DEV),
+              res.to(DEV))
+    rows = rng.permutation(T)[:24]
+    ref, err = R.linear(q, s, x64[rows], "swiglu", b.astype(np.float64), res.double().numpy()[rows])
+    got = y.double().cpu().numpy()[rows]
+    assert np.all(np.abs(got - ref) <= err + R.HALF_STEP[dtype] * (np.abs(ref) + err) + 1e-37)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("act", list(ACT))
 @pytest.mark.parametrize("T,N,K,bits,group", [(1, 256, 544, 4, 0), (5, 64, 256, 4, 32), (16, 192, 96, 8, 0),
