@@ -18,34 +18,44 @@ constexpr int kWaves = 4;  // wavefronts per workgroup
 // ------------------------------------------------------------ wavefront reductions
 // A row of 16 lanes by quad permutes and mirrors, then the rows by the two row broadcasts; lane 63 holds the
 // result of all 64 lanes and readlane makes it uniform. No LDS round trip.
+// Every lane of these patterns has a source, so the move can be part of the instruction that uses it.
+template <int CTRL>
+__device__ __forceinline__ int dpp_i(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
+}
+// the same into the rows of the mask only; the others get `old`, which has no effect on the reduction
 template <int CTRL, int ROWS>
-__device__ __forceinline__ int dpp_i(int old, int v) {
+__device__ __forceinline__ int dpp_rows(int old, int v) {
   return __builtin_amdgcn_update_dpp(old, v, CTRL, ROWS, 0xF, false);
 }
 __device__ __forceinline__ int wave_max_i(int v) {
-  v = max(v, dpp_i<0xB1, 0xF>(v, v));   // quad_perm [1,0,3,2]
-  v = max(v, dpp_i<0x4E, 0xF>(v, v));   // quad_perm [2,3,0,1]
-  v = max(v, dpp_i<0x141, 0xF>(v, v));  // row_half_mirror
-  v = max(v, dpp_i<0x140, 0xF>(v, v));  // row_mirror
-  v = max(v, dpp_i<0x142, 0xA>(v, v));  // row_bcast15 into rows 1 and 3
-  v = max(v, dpp_i<0x143, 0xC>(v, v));  // row_bcast31 into rows 2 and 3
+  v = max(v, dpp_i<0xB1>(v));   // quad_perm [1,0,3,2]
+  v = max(v, dpp_i<0x4E>(v));   // quad_perm [2,3,0,1]
+  v = max(v, dpp_i<0x141>(v));  // row_half_mirror
+  v = max(v, dpp_i<0x140>(v));  // row_mirror
+  v = max(v, dpp_rows<0x142, 0xA>(INT32_MIN, v));  // row_bcast15 into rows 1 and 3
+  v = max(v, dpp_rows<0x143, 0xC>(INT32_MIN, v));  // row_bcast31 into rows 2 and 3
   return __builtin_amdgcn_readlane(v, 63);
 }
-template <int CTRL, int ROWS>
+template <int CTRL>
 __device__ __forceinline__ float dpp_add(float v) {
-  return v + __builtin_bit_cast(float, dpp_i<CTRL, ROWS>(0, __builtin_bit_cast(int, v)));
+  return v + __builtin_bit_cast(float, dpp_i<CTRL>(__builtin_bit_cast(int, v)));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add_rows(float v) {
+  return v + __builtin_bit_cast(float, dpp_rows<CTRL, ROWS>(0, __builtin_bit_cast(int, v)));
 }
 __device__ __forceinline__ float readlane_f(float v, int lane) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
 }
 // fixed order: pairs, quads, halves, rows
 __device__ __forceinline__ float wave_sum(float v) {
-  v = dpp_add<0xB1, 0xF>(v);
-  v = dpp_add<0x4E, 0xF>(v);
-  v = dpp_add<0x141, 0xF>(v);
-  v = dpp_add<0x140, 0xF>(v);
-  v = dpp_add<0x142, 0xA>(v);
-  v = dpp_add<0x143, 0xC>(v);
+  v = dpp_add<0xB1>(v);
+  v = dpp_add<0x4E>(v);
+  v = dpp_add<0x141>(v);
+  v = dpp_add<0x140>(v);
+  v = dpp_add_rows<0x142, 0xA>(v);
+  v = dpp_add_rows<0x143, 0xC>(v);
   return readlane_f(v, 63);
 }
 __device__ __forceinline__ double wave_sum_d(double v) {
@@ -72,20 +82,25 @@ struct alignas(NE * sizeof(TZ) < 16 ? NE * sizeof(TZ) : 16) Run {
 template <int NE, class TZ>
 __device__ __forceinline__ uint32_t load_row(const TZ* row, int E, bool vec, int lane, float (&z)[NE]) {
   const int e0 = lane * NE;
-  Run<NE, TZ> r;
-  if (vec) {
-    if (e0 < E) r = *reinterpret_cast<const Run<NE, TZ>*>(row + e0);
+  float f[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) f[i] = kNegInf;
+  if (vec) {  // E is a multiple of NE
+    if (e0 < E) {
+      const Run<NE, TZ> r = *reinterpret_cast<const Run<NE, TZ>*>(row + e0);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) f[i] = to_f32<TZ>(r.v[i]);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < NE; ++i)
-      if (e0 + i < E) r.v[i] = row[e0 + i];
+      if (e0 + i < E) f[i] = to_f32<TZ>(row[e0 + i]);
   }
   uint32_t live = 0;
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
-    float f = e0 + i < E ? to_f32<TZ>(r.v[i]) : kNegInf;
-    const bool on = f > lowest<TZ>();
-    z[i] = on ? fminf(f, 3.402823466e38f) + 0.0f : kNegInf;
+    const bool on = f[i] > lowest<TZ>();
+    z[i] = on ? __builtin_amdgcn_fmed3f(f[i], -3.402823466e38f, 3.402823466e38f) + 0.0f : kNegInf;
     live |= on ? 1u << i : 0u;
   }
   return live;
@@ -123,9 +138,9 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
-// lanes of the mask below this one
-__device__ __forceinline__ int lanes_below(uint64_t m) {
-  return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+// lanes of the mask below this one, and c
+__device__ __forceinline__ int lanes_below(uint64_t m, int c) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, c));
 }
 
 // (a, b) two largest of one set, (c, d) of another -> of both
@@ -135,7 +150,7 @@ __device__ __forceinline__ void merge_top2(int& a, int& b, int c, int d) {
 }
 template <int CTRL>
 __device__ __forceinline__ void merge_top2_dpp(int& a, int& b) {
-  merge_top2(a, b, dpp_i<CTRL, 0xF>(a, a), dpp_i<CTRL, 0xF>(b, b));
+  merge_top2(a, b, dpp_i<CTRL>(a), dpp_i<CTRL>(b));
 }
 
 // Group limiting: which of the lane's experts stay. g[i] is the value that the groups are scored by (kDead where
@@ -174,19 +189,27 @@ __device__ __forceinline__ uint32_t keep_groups(const int (&g)[NE], int E, int G
   const bool is = mine < G;
   const int score = !is ? kDead : gmax || b == kDead ? a : okey(__fadd_rn(unkey(a), unkey(b)) + 0.0f);
   int rank = 0;
-  for (int h = 0; h < G; ++h) {
-    const int o = __builtin_amdgcn_readlane(score, h * step);
-    rank += o + (h < mine ? 1 : 0) > score;  // keys of numbers stay below INT32_MAX
+  if (G <= 8) {  // all pairs at once: lane 8a + b compares group b with group a
+    const int pa = __shfl(score, (lane >> 3) * step), pb = __shfl(score, (lane & 7) * step);
+    const uint64_t ahead = __ballot((lane & 7) < G && pb + ((lane & 7) < lane >> 3 ? 1 : 0) > pa);
+    rank = __popc((uint32_t)(ahead >> (mine & 7) * 8) & 0xFFu);
+  } else {
+    for (int h = 0; h < G; ++h) {
+      const int o = __builtin_amdgcn_readlane(score, h * step);
+      rank += o + (h < mine ? 1 : 0) > score;  // keys of numbers stay below INT32_MAX
+    }
   }
   const bool kept = is && rank < KG && score != kDead;
-  const int lowest_kept = -wave_max_i(kept ? -score : kDead);  // a kept key is above kDead, so -score exists
-  const int best_dropped = wave_max_i(is && !kept ? score : kDead);
+  const uint64_t m = __ballot(kept), last = __ballot(is && rank == KG - 1), next = __ballot(is && rank == KG);
   *near = false;
-  if (best_dropped != kDead) {
-    const float p = unkey(lowest_kept), q = unkey(best_dropped);
-    *near = p - q <= thr + 1e-6f * (fabsf(p) + fabsf(q));
+  if (next) {  // the last group kept and the best one dropped
+    const int kp = __builtin_amdgcn_readlane(score, __ffsll((unsigned long long)last) - 1);
+    const int kq = __builtin_amdgcn_readlane(score, __ffsll((unsigned long long)next) - 1);
+    if (kp != kDead && kq != kDead) {
+      const float p = unkey(kp), q = unkey(kq);
+      *near = p - q <= thr + 1e-6f * (fabsf(p) + fabsf(q));
+    }
   }
-  const uint64_t m = __ballot(kept);
   uint32_t r = 0;
   if (glog >= 0) {
     r = kept ? (1u << NE) - 1 : 0;
@@ -206,8 +229,7 @@ __device__ __forceinline__ uint32_t keep_groups(const int (&g)[NE], int E, int G
 // registers, and about ten steps separate the K-th from the next; K rounds of a largest key took 20 vector
 // instructions each and 6 dependent lane moves.
 template <int NE>
-__device__ __forceinline__ int top_keys(const int (&k)[NE], int K, int lane, int* s_key, int* s_id, int* key, int* id,
-                                        int* next) {
+__device__ __forceinline__ int top_keys(const int (&k)[NE], int K, int lane, int* scratch, int* key, int* id, int* next) {
   int lm = k[0];
 #pragma unroll
   for (int i = 1; i < NE; ++i) lm = max(lm, k[i]);
@@ -221,64 +243,81 @@ __device__ __forceinline__ int top_keys(const int (&k)[NE], int K, int lane, int
     for (int i = 0; i < NE; ++i) c += __popcll(__ballot(k[i] >= v));
     return c;
   };
-  const int n_base = count(base);
-  int lo = base, n_lo = n_base, hi = top, n_hi = 0;  // count(lo) >= K > count(hi + 1), where there are K
-  if (n_lo > K) {
-    while (lo != hi) {  // lo < hi: smallest v > lo with count(v) <= K lies in (lo, hi + 1]
-      const int mid = (int)((uint32_t)lo + (((uint32_t)hi - (uint32_t)lo + 1u) >> 1));
-      const int c = count(mid);
-      if (c == K) {
-        lo = mid;
-        n_lo = c;
-        break;
-      }
-      if (c > K) {
-        lo = mid;
-        n_lo = c;
-      } else {
-        hi = mid - 1;
-        n_hi = c;
-      }
-    }
+  int lo = base, n_lo = count(base), hi = top, n_hi = 0;  // count(lo) >= K > count(hi + 1), where there are K
+  while (n_lo > K && lo != hi) {  // the smallest v > lo with count(v) <= K lies in (lo, hi + 1]
+    const int mid = (int)((uint32_t)lo + (((uint32_t)hi - (uint32_t)lo + 1u) >> 1));
+    const int c = count(mid);
+    const bool up = c >= K;
+    lo = up ? mid : lo;
+    n_lo = up ? c : n_lo;
+    hi = up ? hi : mid - 1;
+    n_hi = up ? n_hi : c;
   }
-  // n_lo > K: more than K keys are at least lo, n_hi of them above it; the first K - n_hi that equal lo fill up
-  int before = 0;
-  if (n_lo > K) {
+  int kk[NE];
 #pragma unroll
-    for (int i = 0; i < NE; ++i) before += lanes_below(__ballot(k[i] == lo));
+  for (int i = 0; i < NE; ++i) kk[i] = k[i];
+  int rest = kDead;
+  if (n_lo > K) {  // more than K keys are at least lo, n_hi of them above it: the first K - n_hi that equal lo fill up
+    int before = 0;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) before += lanes_below(__ballot(k[i] == lo), 0);
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (k[i] == lo && before++ >= K - n_hi) kk[i] = kDead;
+    rest = lo;
   }
-  int at = 0, rest = kDead, n = 0;
+  int at = 0;
+  uint2* slot = reinterpret_cast<uint2*>(scratch);
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
-    bool on = k[i] >= lo;
-    if (n_lo > K && k[i] == lo) on = before++ < K - n_hi;
+    const bool on = kk[i] >= lo;
     const uint64_t m = __ballot(on);
-    if (on) {
-      const int p = at + lanes_below(m);
-      s_key[p] = k[i];
-      s_id[p] = lane * NE + i;
-    }
+    if (on) slot[lanes_below(m, at)] = make_uint2((uint32_t)kk[i], (uint32_t)(lane * NE + i));
     at += __popcll(m);
-    rest = max(rest, on ? kDead : k[i]);
+    rest = max(rest, on ? kDead : kk[i]);
   }
-  n = at;
   wave_sync();
-  *key = lane < n ? s_key[lane] : kDead;
-  *id = lane < n ? s_id[lane] : -1;
+  const uint2 mine = lane < at ? slot[lane] : make_uint2((uint32_t)kDead, 0xFFFFFFFFu);
   wave_sync();
+  *key = (int)mine.x;
+  *id = (int)mine.y;
   *next = wave_max_i(rest);
-  return n;
+  return at;
+}
+
+// Rank of the lane's key among the first n lanes' (larger first, the lower id first on equal keys).
+__device__ __forceinline__ int rank_of(int key, int id, int n, int lane) {
+  int rank = 0;
+  if (n <= 8) {  // all pairs at once: lane 8a + b compares key b with key a
+    const int ka = __shfl(key, lane >> 3), kb = __shfl(key, lane & 7), ia = __shfl(id, lane >> 3), ib = __shfl(id, lane & 7);
+    const uint64_t ahead = __ballot((lane & 7) < n && (kb > ka || (kb == ka && ib < ia)));
+    rank = __popc((uint32_t)(ahead >> (lane & 7) * 8) & 0xFFu);
+  } else {
+    for (int j = 0; j < n; ++j) {
+      const int ok = __builtin_amdgcn_readlane(key, j), oi = __builtin_amdgcn_readlane(id, j);
+      rank += ok > key || (ok == key && oi < id);
+    }
+  }
+  return rank;
+}
+
+// e^x (x <= 0) and sigmoid for comparing scores: the argument of 2^x is rounded once, which for the scores, 1 / (1 +
+// e^-|z|) or e^(z - max) / sum, is below 4e-8 of the largest, however large |z| is.
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+__device__ __forceinline__ float sigmoid_fast(float z) {
+  const float a = exp_fast(-fabsf(z)), d = __builtin_amdgcn_rcpf(1.0f + a);
+  return z >= 0.0f ? d : a * d;
 }
 
 // The definition compares fl32(score) + bias, the score taken in 64 bits, so that every implementation chooses the
-// same experts. Taking 256 exponentials a token in 64 bits is most of the work; so the choice is made once with
-// 32-bit scores, and if two neighbours in the order (or two groups) lie closer than twice the error of those, once
-// more with the definition's. The bound: see thr below.
+// same experts. Taking 256 exponentials a token in 64 bits is most of the work; so the choice is made with 32-bit
+// scores, and a token where two neighbours in the order (or two groups) lie closer than twice the error of those (see
+// thr) is set aside and done once more with the definition's: 2 tokens in 1,000 of 256 biased sigmoid scores.
 template <int NE, class TZ, bool SOFTMAX, bool STATS, int WV>
-__global__ __launch_bounds__(64 * WV) void k_route(RouteArgs a) {
-  __shared__ int s_row[WV][64 * NE];  // a wavefront's scratch
+__global__ __launch_bounds__(64 * WV, NE <= 4 ? 6 : NE == 8 ? 4 : 2) void k_route(RouteArgs a) {
+  __shared__ __align__(8) int s_row[WV][64 * NE];  // a wavefront's scratch
   __shared__ int s_load[STATS ? 64 * NE : 1];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int E = a.E, K = a.K;
   int* scratch = s_row[wave];
   float bias[NE], imp[NE];
@@ -293,24 +332,28 @@ __global__ __launch_bounds__(64 * WV) void k_route(RouteArgs a) {
   }
   const bool by_sum = a.G > 1 && !a.group_max;
   const bool scored = a.bias || by_sum;  // the choice compares scores, not logits
-  for (int t = blockIdx.x * WV + wave; t < a.T; t += gridDim.x * WV) {
+
+  // one token; true where it has to be done with exact scores instead (then nothing is written)
+  auto token = [&](int t, auto exact_) __attribute__((always_inline)) -> bool {
+    constexpr bool EXACT = decltype(exact_)::value;
     const TZ* row = static_cast<const TZ*>(a.logits) + (size_t)t * a.ld;
-    float z[NE];
-    uint32_t live = load_row<NE, TZ>(row, E, a.vec, lane, z);
     if (a.valid && a.valid[t] == 0) {
-      live = 0;
-#pragma unroll
-      for (int i = 0; i < NE; ++i) z[i] = kNegInf;
+      if (lane < K) {
+        a.ids[(size_t)t * K + lane] = -1;
+        a.w[(size_t)t * K + lane] = 0.0f;
+      }
+      return false;
     }
-    const float m = SOFTMAX || STATS ? row_max<NE>(z) : 0.0f;  // -inf: nothing to choose from
-    float s[NE];
-    float rs = 0.0f;  // softmax: 1 / sum
-    if (SOFTMAX) {
+    float z[NE], s[NE];
+    const uint32_t live = load_row<NE, TZ>(row, E, a.vec, lane, z);
+    float m = 0.0f, rs = 0.0f;  // softmax: largest logit (-inf: nothing to choose from), 1 / sum
+    if constexpr (SOFTMAX) {
+      m = row_max<NE>(z);
       if (scored || STATS || !a.renorm) {
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-          s[i] = live >> i & 1 ? exp_neg(z[i] - m) : 0.0f;
+          s[i] = live >> i & 1 ? exp_fast(z[i] - m) : 0.0f;
           sum += s[i];
         }
         rs = safe_rcp(wave_sum(sum));
@@ -319,95 +362,102 @@ __global__ __launch_bounds__(64 * WV) void k_route(RouteArgs a) {
       }
     } else if (scored || STATS) {
 #pragma unroll
-      for (int i = 0; i < NE; ++i) {
-        float miss;
-        sigmoid2(z[i], s[i], miss);
-        s[i] = live >> i & 1 ? s[i] : 0.0f;
+      for (int i = 0; i < NE; ++i) s[i] = live >> i & 1 ? sigmoid_fast(z[i]) : 0.0f;
+    }
+    if constexpr (STATS && !EXACT) {
+      if constexpr (SOFTMAX) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) imp[i] += s[i];
+      } else {
+        float q[NE], sum = 0.0f, zm = z[0];
+#pragma unroll
+        for (int i = 1; i < NE; ++i) zm = fmaxf(zm, z[i]);
+        const bool low = __ballot(zm >= -40.0f) == 0;  // the sum would underflow: relative to the largest logit
+        const float ref = low ? row_max<NE>(z) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+          q[i] = s[i];
+          if (low) q[i] = live >> i & 1 ? sigmoid_rel(z[i], ref) : 0.0f;
+          sum += q[i];
+        }
+        const float r = safe_rcp(wave_sum(sum));
+#pragma unroll
+        for (int i = 0; i < NE; ++i) imp[i] = fmaf(q[i], r, imp[i]);
       }
     }
-    if (STATS) {
-      float q[NE], sum = 0.0f;
+    if constexpr (EXACT) {  // through LDS, one expert of the lane at a time: rare, and it should not cost registers
+      float* f = reinterpret_cast<float*>(scratch) + lane * NE;
 #pragma unroll
-      for (int i = 0; i < NE; ++i) {
-        q[i] = s[i];
-        if (!SOFTMAX && m < -40.0f) q[i] = live >> i & 1 ? sigmoid_rel(z[i], m) : 0.0f;
-        sum += q[i];
+      for (int i = 0; i < NE; ++i) f[i] = z[i];
+      double sum = 0.0;
+      if (SOFTMAX) {
+#pragma unroll 1
+        for (int i = 0; i < NE; ++i)
+          if (f[i] > kNegInf) sum += exp((double)f[i] - (double)m);
+        sum = wave_sum_d(sum);
       }
-      const float r = SOFTMAX ? 1.0f : safe_rcp(wave_sum(sum));
+#pragma unroll 1
+      for (int i = 0; i < NE; ++i) {
+        const double zi = f[i];
+        f[i] = !(f[i] > kNegInf) ? 0.0f
+                                 : (float)(SOFTMAX ? exp(zi - (double)m) / sum : 1.0 / (1.0 + exp(-zi)));
+      }
 #pragma unroll
-      for (int i = 0; i < NE; ++i) imp[i] = fmaf(q[i], r, imp[i]);
+      for (int i = 0; i < NE; ++i) s[i] = f[i];
+      wave_sync();
     }
-    // Twice the error of a 32-bit score. Sigmoid: e^-|z| 2e-7, the sum, reciprocal and product 2.5e-7, weighted by
-    // at most 1/2 and 1: below 4e-7, and 6e-8 for rounding the 64-bit score. Softmax: the sum of up to 1024 terms
+    // Twice the error of a 32-bit score. Sigmoid: e^-|z| 2.1e-7, the sum, reciprocal and product 2.4e-7, weighted by at
+    // most 1/4 and 1: below 3e-7, and 6e-8 for rounding the 64-bit score. Softmax: the sum of up to 1024 terms
     // (21 roundings along a path) 1.3e-6, the exponential, reciprocal and product 4e-7, of the largest score rs.
     const float thr = SOFTMAX ? 4.5e-6f * rs + 1e-7f : 1.0e-6f;
-    int n_sel, my_key, my_id, rank;
-    float my_z;
-    for (int attempt = 0;; ++attempt) {
-      int key[NE], gk[NE];
-      bool near = false;
+    int key[NE];
+    bool near = false;
 #pragma unroll
-      for (int i = 0; i < NE; ++i) {
-        const bool on = live >> i & 1;
-        const float c = a.bias ? __fadd_rn(s[i], bias[i]) + 0.0f : z[i];
-        key[i] = on && c > kNegInf ? okey(c) : kDead;
-        gk[i] = on && by_sum && !a.bias ? okey(s[i]) : key[i];
-      }
-      if (a.G > 1) {
-        const uint32_t keep =
-            keep_groups<NE>(gk, E, a.G, a.KG, a.glog, a.group_max, lane, scratch, 2.0f * thr, &near);
-#pragma unroll
-        for (int i = 0; i < NE; ++i) key[i] = keep >> i & 1 ? key[i] : kDead;
-      }
-      int next;
-      n_sel = top_keys<NE>(key, K, lane, scratch, scratch + 32, &my_key, &my_id, &next);
-      my_z = kNegInf;  // read again: the logit of a chosen expert
-      if (lane < n_sel) my_z = fminf(to_f32<TZ>(row[my_id]), 3.402823466e38f) + 0.0f;
-      // the chosen in order: rank = how many come before; gap to the nearest of them
-      rank = 0;
-      float gap = INFINITY;
-      const float mine = unkey(my_key);
-      for (int j = 0; j < n_sel; ++j) {
-        const int ok = __builtin_amdgcn_readlane(my_key, j), oi = __builtin_amdgcn_readlane(my_id, j);
-        const bool ahead = ok > my_key || (ok == my_key && oi < my_id);
-        rank += ahead;
-        if (ahead) gap = fminf(gap, unkey(ok) - mine);
-      }
-      if (!scored || attempt == 1) break;
-      if (a.bias) {
-        // scores off by thr / 2 each; the rounding of the two additions is below 1e-6 of the values
-        if (next != kDead) gap = fminf(gap, mine - unkey(next));
-        const bool close = lane < n_sel && gap < INFINITY && gap <= thr + 1e-6f * (fabsf(mine) + gap);
-        near |= __ballot(close) != 0;
-      }
-      if (!near) break;
-      // the definition's scores
-      double d[NE], sum = 0.0;
-#pragma unroll
-      for (int i = 0; i < NE; ++i) {
-        const bool on = live >> i & 1;
-        float zi = z[i];
-        asm volatile("" : "+v"(zi));  // keeps this rare work inside the branch (it was hoisted above the loop)
-        if (SOFTMAX) {
-          d[i] = on ? exp((double)zi - (double)m) : 0.0;
-          sum += d[i];
-        } else {
-          d[i] = on ? 1.0 / (1.0 + exp(-(double)zi)) : 0.0;
-        }
-      }
-      if (SOFTMAX) sum = wave_sum_d(sum);
-#pragma unroll
-      for (int i = 0; i < NE; ++i) s[i] = (float)(SOFTMAX ? d[i] / sum : d[i]);
+    for (int i = 0; i < NE; ++i) {
+      const float c = a.bias ? __fadd_rn(s[i], bias[i]) + 0.0f : z[i];
+      key[i] = (live >> i & 1) && c > kNegInf ? okey(c) : kDead;
     }
+    if (a.G > 1) {
+      int gk[NE];
+#pragma unroll
+      for (int i = 0; i < NE; ++i) gk[i] = by_sum && !a.bias ? (live >> i & 1 ? okey(s[i]) : kDead) : key[i];
+      const uint32_t keep = keep_groups<NE>(gk, E, a.G, a.KG, a.glog, a.group_max, lane, scratch, 2.0f * thr, &near);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) key[i] = keep >> i & 1 ? key[i] : kDead;
+    }
+    int my_key, my_id, next;
+    const int n_sel = top_keys<NE>(key, K, lane, scratch, &my_key, &my_id, &next);
     const bool on = lane < n_sel;
+    float my_z = kNegInf;  // read again: the logit of a chosen expert
+    if (on) my_z = fminf(to_f32<TZ>(row[my_id]), 3.402823466e38f) + 0.0f;
+    const int rank = rank_of(my_key, my_id, n_sel, lane);
+    if (!EXACT && scored) {
+      if (a.bias) {  // the chosen in order, and the best one left out
+        if (on) scratch[rank] = my_key;
+        if (lane == 0) scratch[n_sel] = next;
+        wave_sync();
+        const int nk = on ? scratch[rank + 1] : kDead;
+        wave_sync();
+        const float p = unkey(my_key), gap = p - unkey(nk);
+        // the rounding of the two additions is below 1e-6 of the values
+        near |= __ballot(on && nk != kDead && gap <= thr + 1e-6f * (fabsf(p) + gap)) != 0;
+      }
+      if (near) return true;
+    }
     float r;
     if (a.renorm) {
-      const float ref = unkey(wave_max_i(on ? okey(my_z) : kDead));
-      float q = 0.0f;
-      if (on) q = SOFTMAX ? exp_neg(my_z - ref) : sigmoid_rel(my_z, fminf(ref, 0.0f));
+      float q;
+      if (!SOFTMAX && __ballot(on && my_z < -40.0f) == 0) {
+        float miss;
+        sigmoid2(my_z, q, miss);
+        q = on ? q : 0.0f;
+      } else {
+        const float ref = unkey(wave_max_i(on ? okey(my_z) : kDead));
+        q = !on ? 0.0f : SOFTMAX ? exp_neg(my_z - ref) : sigmoid_rel(my_z, fminf(ref, 0.0f));
+      }
       r = q * safe_rcp(wave_sum(q));
     } else if (SOFTMAX) {
-      r = on ? exp_neg(my_z - m) * rs : 0.0f;
+      r = exp_neg(my_z - m) * rs;
     } else {
       float miss;
       sigmoid2(my_z, r, miss);
@@ -417,6 +467,19 @@ __global__ __launch_bounds__(64 * WV) void k_route(RouteArgs a) {
       a.ids[(size_t)t * K + k] = on ? my_id : -1;
       a.w[(size_t)t * K + k] = on ? r * a.scale : 0.0f;
       if (STATS && on) atomicAdd(&s_load[my_id], 1);
+    }
+    return false;
+  };
+
+  const int step = gridDim.x * WV;
+  for (int t0 = blockIdx.x * WV + wave; t0 < a.T; t0 += 64 * step) {
+    uint64_t again = 0;
+    for (int i = 0; i < 64 && t0 + i * step < a.T; ++i)
+      if (token(t0 + i * step, std::false_type{})) again |= 1ull << i;
+    while (again) {
+      const int i = __ffsll((unsigned long long)again) - 1;
+      again &= again - 1;
+      token(t0 + i * step, std::true_type{});
     }
   }
   if (STATS) {
@@ -607,35 +670,52 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_grad(RouteGradArgs a) {
 }
 
 // ------------------------------------------------------------ gradient of the routing weights
-// dw[t][k] = sum_h dy[t][h] e_out[t*K + k][h]. Reads every slot's row once: HBM-bound. One wavefront takes one
-// slot; the K slots of a token sit next to each other, so dy comes from the caches after the first.
+// dw[t][k] = sum_h dy[t][h] e_out[t*K + k][h]. Reads every slot's row once: HBM-bound. One wavefront takes one slot,
+// eight 16-byte loads of its row in flight (not kept in the caches); the K slots of a token sit next to each other, so
+// dy comes from the caches after the first.
+constexpr int kSlotLoads = 8;
+typedef float f4v __attribute__((ext_vector_type(4)));
 __global__ __launch_bounds__(256) void k_slot_grad(const float* __restrict__ eout, const int32_t* __restrict__ ids,
                                                    const float* __restrict__ dy, int64_t slots, int K, int H,
                                                    float* __restrict__ dw) {
   const int lane = threadIdx.x & 63;
   const int64_t j = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (j >= slots) return;
-  float v = 0.0f;
+  f4v v = {0.0f, 0.0f, 0.0f, 0.0f};
   if (ids[j] >= 0) {
-    const float4* a = reinterpret_cast<const float4*>(eout + (size_t)j * H);
-    const float4* b = reinterpret_cast<const float4*>(dy + (size_t)(j / K) * H);
-    for (int h = lane; h < H / 4; h += 64) {
-      const float4 x = a[h], y = b[h];
-      v = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, v))));
+    const f4v* a = reinterpret_cast<const f4v*>(eout + (size_t)j * H);
+    const f4v* b = reinterpret_cast<const f4v*>(dy + (size_t)(j / K) * H);
+    const int n = H / 4;
+    int h = lane;
+    for (; h + 64 * (kSlotLoads - 1) < n; h += 64 * kSlotLoads) {
+      f4v x[kSlotLoads], y[kSlotLoads];
+#pragma unroll
+      for (int i = 0; i < kSlotLoads; ++i) x[i] = __builtin_nontemporal_load(a + h + 64 * i);
+#pragma unroll
+      for (int i = 0; i < kSlotLoads; ++i) y[i] = b[h + 64 * i];
+#pragma unroll
+      for (int i = 0; i < kSlotLoads; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = fmaf(x[i][c], y[i][c], v[c]);
+    }
+    for (; h < n; h += 64) {
+      const f4v x = a[h], y = b[h];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = fmaf(x[c], y[c], v[c]);
     }
   }
-  v = wave_sum(v);
-  if (lane == 0) dw[j] = v;
+  const float sum = wave_sum((v[0] + v[1]) + (v[2] + v[3]));
+  if (lane == 0) dw[j] = sum;
 }
 
 }  // namespace
 
 // ------------------------------------------------------------ launches
 constexpr int kRouteMaxWaves = 8192;  // persistent grid: 8 wavefronts per SIMD
-// With statistics a workgroup leaves one row of partial sums; from this many tokens on it has 16 wavefronts, so that
-// there are at most 512 rows to add up.
+// With statistics a workgroup leaves one row of partial sums; from this many tokens on it has 8 wavefronts, so that
+// there are at most 1,024 rows to add up.
 constexpr int kRouteWideT = 2048;
-constexpr int kWideWaves = 16;
+constexpr int kWideWaves = 8;
 
 static int route_blocks(int T, int waves = kWaves) {
   const int need = (T + waves - 1) / waves, most = kRouteMaxWaves / waves;

@@ -171,6 +171,27 @@ def test_route_many_tokens_equal_single_ones():
     assert abs(float(imp.double().sum()) - 9001) < 9001 * 64 * U
 
 
+@pytest.mark.parametrize("E,K,G,KG,dtype", [(1024, 32, 64, 9, "f32"), (500, 16, 1, 1, "bf16"), (256, 8, 8, 4, "f16")])
+def test_route_statistics_of_long_batches(E, K, G, KG, dtype):
+    """2,500 tokens, with padding: the workgroups of 16 wavefronts, every expert width; sums against 64 bits."""
+    rng = np.random.default_rng(E)
+    T = 2500
+    z, z64 = _logits(rng, T, E, dtype)
+    bias = rng.uniform(-0.1, 0.1, E).astype(np.float32)
+    valid = (rng.random(T) < 0.8).astype(np.uint8)
+    for softmax in (False, True):
+        cfg = _cfg(E, K, G, KG, softmax=softmax)
+        gi, gw, gl, gm = _run(cfg, z, K, torch.from_numpy(bias).to(DEV), torch.from_numpy(valid).to(DEV))
+        pick = rng.permutation(T)[:60]
+        ids, w, _, _ = R.route(z64[pick], dtype, K, G=G, KG=KG, softmax=softmax, bias=bias, valid=valid[pick])
+        assert np.array_equal(gi[pick], ids)
+        assert np.all(np.abs(gw[pick] - w) <= 64 * U * np.abs(w) + 1e-30)
+        assert np.array_equal(gl.cpu().numpy(), np.bincount(gi[gi >= 0], minlength=E))
+        s = np.exp(z64 - z64.max(1, keepdims=True)) if softmax else 1 / (1 + np.exp(-z64))
+        imp = ((s / s.sum(1, keepdims=True)) * valid[:, None]).sum(0)
+        assert np.all(np.abs(gm.cpu().numpy() - imp) <= (64 + T) * U * imp)
+
+
 def _grad_case(rng, T, E, K, dtype, pad=0):
     z, z64 = _logits(rng, T, E, dtype, pad)
     ids = np.stack([rng.permutation(E)[:K] for _ in range(T)]).astype(np.int32)
