@@ -545,7 +545,7 @@ struct RouteGradArgs {
 template <int NE, class TZ, bool SOFTMAX>
 __global__ __launch_bounds__(64 * kWaves) void k_route_grad(RouteGradArgs a) {
   __shared__ float s_add[kWaves][64 * NE];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int E = a.E, K = a.K;
   float* add = s_add[wave];
   float dimp[NE];
@@ -582,8 +582,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_grad(RouteGradArgs a) {
       float m = 0.0f, rs = 0.0f;
       if (dense) {
         live = load_row<NE, TZ>(row, E, a.vec, lane, z);
-        m = row_max<NE>(z);
         if (SOFTMAX) {
+          m = row_max<NE>(z);
           float sum = 0.0f;
 #pragma unroll
           for (int i = 0; i < NE; ++i) {
@@ -598,14 +598,17 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_grad(RouteGradArgs a) {
       // the slots' own part
       float dk = 0.0f;
       if (a.renorm) {
-        const float ref = unkey(wave_max_i(on ? okey(zk + 0.0f) : kDead));
-        float q = 0.0f, miss = 1.0f;
-        if (on) {
-          q = SOFTMAX ? exp_neg(zk - ref) : sigmoid_rel(zk, fminf(ref, 0.0f));
+        float q, miss = 1.0f;
+        if (SOFTMAX || __ballot(on && zk < -40.0f)) {
+          const float ref = unkey(wave_max_i(on ? okey(zk + 0.0f) : kDead));
+          q = !on ? 0.0f : SOFTMAX ? exp_neg(zk - ref) : sigmoid_rel(zk, fminf(ref, 0.0f));
           if (!SOFTMAX) {
             float s;
             sigmoid2(zk, s, miss);
           }
+        } else {
+          sigmoid2(zk, q, miss);
+          q = on ? q : 0.0f;
         }
         const float r = q * safe_rcp(wave_sum(q));
         const float mean = wave_sum(r * u);
@@ -639,11 +642,15 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_grad(RouteGradArgs a) {
 #pragma unroll
         for (int i = 0; i < NE; ++i) out[i] += p[i] * (dimp[i] - dot);
       } else if (dense) {
-        float miss[NE], sum = 0.0f, dot = 0.0f;
+        float miss[NE], sum = 0.0f, dot = 0.0f, zm = z[0];
+#pragma unroll
+        for (int i = 1; i < NE; ++i) zm = fmaxf(zm, z[i]);
+        const bool low = __ballot(zm >= -40.0f) == 0;  // the sum would underflow: relative to the largest logit
+        const float ref = low ? row_max<NE>(z) : 0.0f;
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
           sigmoid2(z[i], p[i], miss[i]);
-          if (m < -40.0f) p[i] = sigmoid_rel(z[i], m);
+          if (low) p[i] = sigmoid_rel(z[i], ref);
           p[i] = live >> i & 1 ? p[i] : 0.0f;
           sum += p[i];
           dot = fmaf(p[i], dimp[i], dot);
