@@ -326,7 +326,8 @@ typedef struct moe_route_config {
   float scale;         /* finite, > 0 */
 } moe_route_config;
 
-/* Bytes of workspace of moe_route with load or importance, for up to max_tokens tokens; 0 for an invalid config. */
+/* Bytes of workspace of moe_route with load or importance, for up to max_tokens tokens; 0 for an invalid config. Calls
+ * that may overlap need a workspace each; its contents need not be initialized. */
 size_t moe_route_workspace_bytes(const moe_route_config* cfg, int32_t max_tokens);
 
 /* logits [T][E] of `dtype`, rows ld elements apart (ld >= E); bias [E] fp32 and valid [T] bytes may be NULL.
@@ -377,11 +378,12 @@ typedef struct moe_linear_config {
   int32_t act;         /* MOE_ACT_* */
 } moe_linear_config;
 
-/* Bytes of workspace for up to max_tokens tokens of any type; 0 for an invalid config. */
+/* Bytes of workspace for up to max_tokens tokens of any type; 0 for an invalid config. Calls that may overlap need a
+ * workspace each; its contents need not be initialized. */
 size_t moe_linear_workspace_bytes(const moe_linear_config* cfg, int32_t max_tokens);
 
 /* x, residual and y are of `dtype`, with rows ldx, ldr and ldy elements apart; bias [rows] fp32 and residual may be
- * NULL; residual may be y itself (same pointer and stride). y may not overlap x. codes 16-byte aligned, the others
+ * NULL; residual may be y itself (same pointer and stride), else y overlaps neither it nor x. codes 16-byte aligned, the others
  * aligned to their elements; ws 256-byte aligned. The sums W x of a token whose x holds an infinity or NaN are all
  * infinite or NaN; other tokens are not touched by it. 1 <= T <= 2^20.
  * Errors: MOE_E_NULL, MOE_E_SHAPE, MOE_E_ARG, MOE_E_WORKSPACE, MOE_E_HIP. */

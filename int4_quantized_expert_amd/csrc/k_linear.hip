@@ -4,8 +4,8 @@
 // Both operands go to the matrix cores as fp16, without loss:
 //  - a code (at most 8 bits) is an integer that fp16 holds exactly; its scale multiplies the fp32 sum.
 //  - an activation is multiplied by a power of two per token, such that the token's largest lies in [2^14, 2^15).
-//    fp16 then holds every bf16 value down to 2^-32 of the largest exactly, and any smaller one to 2^-39 of the
-//    largest. fp32 values are split, v = hi + lo, both fp16: what is lost is below 2^-23 of the value (or 2^-39 of
+//    fp16 then holds every bf16 value down to 2^-31 of the largest exactly, and any smaller one to 2^-38 of the
+//    largest. fp32 values are split, v = hi + lo, both fp16: what is lost is below 2^-23 of the value (or 2^-38 of
 //    the token's largest). fp16 values are taken as they are.
 // Products are exact in fp32, sums are fp32.
 //

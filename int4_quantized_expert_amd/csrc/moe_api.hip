@@ -442,6 +442,8 @@ int32_t layer_forward_impl(const moe_config* cfg, const moe_layer_weights* wts, 
   if (!wts->w13 || !wts->s13 || !wts->w2 || !wts->s2) return MOE_E_NULL;
   if (cfg->n_shared > 0 && (!wts->sh_w13 || !wts->sh_s13 || !wts->sh_w2 || !wts->sh_s2)) return MOE_E_NULL;
   if (!layer_ptrs_aligned(wts, x, y, true)) return MOE_E_ARG;
+  if (given && (reinterpret_cast<uintptr_t>(given->ids) % 4 || reinterpret_cast<uintptr_t>(given->w) % 4))
+    return MOE_E_ARG;
   WeightView wv{wts->w13, wts->s13, wts->w2, wts->s2, wts->sh_w13, wts->sh_s13, wts->sh_w2, wts->sh_s2, nullptr};
   Fwd f;
   if ((rc = fwd_setup(cfg, wv, T, ws, ws_bytes, taps, &f, given != nullptr))) return rc;

@@ -112,7 +112,7 @@ def test_routed_layer_arguments_refused():
     assert call(ids=None) == call(wt=None) == call(x=None) == call(y=None) == L.MOE_E_NULL
     assert call(wts=L.moe_layer_weights()) == L.MOE_E_NULL
     assert call(T=0) == L.MOE_E_SHAPE
-    assert call(x=P(4100)) == L.MOE_E_ARG
+    assert call(x=P(4100)) == call(ids=P(4098)) == call(wt=P(4097)) == L.MOE_E_ARG
     assert call(n=16) == call(ws=P(65536 + 4)) == L.MOE_E_WORKSPACE
     for name in ("topk_ids", "topk_w", "near_tie"):
         t = L.moe_taps()
@@ -173,3 +173,15 @@ def test_reference_gradient_against_differences(renorm, softmax):
                 zz[t, e] += sg
                 v.append(R.route_value(zz, "f32", ids, dw, dimp, softmax, renorm, 1.5))
             assert abs((v[0] - v[1]) / (2 * h) - g[t, e]) < 1e-8
+
+
+def test_configs_keep_their_struct_until_a_field_changes():
+    import copy
+    import pickle
+    for cfg, field in ((moe.RouteConfig(256, 8), "top_k"), (moe.LinearConfig(128, 256), "act")):
+        a = cfg.ref()
+        assert cfg.ref() is a
+        for other in (copy.copy(cfg), copy.deepcopy(cfg), pickle.loads(pickle.dumps(cfg))):
+            assert other == cfg and getattr(other.ref()._obj, field) == getattr(cfg, field)
+        setattr(cfg, field, 2)
+        assert getattr(cfg.ref()._obj, field) == 2 and getattr(a._obj, field) != 2
