@@ -383,10 +383,10 @@ typedef struct moe_linear_config {
 size_t moe_linear_workspace_bytes(const moe_linear_config* cfg, int32_t max_tokens);
 
 /* x, residual and y are of `dtype`, with rows ldx, ldr and ldy elements apart; bias [rows] fp32 and residual may be
- * NULL; residual may be y itself (same pointer and stride), else y overlaps neither it nor x. codes 16-byte aligned, the others
- * aligned to their elements; ws 256-byte aligned. The sums W x of a token whose x holds an infinity or NaN are all
- * infinite or NaN; other tokens are not touched by it. 1 <= T <= 2^20.
- * Errors: MOE_E_NULL, MOE_E_SHAPE, MOE_E_ARG, MOE_E_WORKSPACE, MOE_E_HIP. */
+ * NULL; residual may be y itself (same pointer and stride), else y overlaps neither it nor x. codes are 16-byte
+ * aligned, the others to their elements, ws 256 bytes. The sums W x of a token whose x holds an infinity or NaN are
+ * all infinite or NaN, and no activation turns a NaN into a number; other tokens are not touched by it.
+ * 1 <= T <= 2^20. Errors: MOE_E_NULL, MOE_E_SHAPE, MOE_E_ARG, MOE_E_WORKSPACE, MOE_E_HIP. */
 int32_t moe_linear(const moe_linear_config* cfg, const uint8_t* codes, const float* scales, const float* bias,
                    const void* x, int64_t ldx, int32_t T, int32_t dtype, const void* residual, int64_t ldr, void* y,
                    int64_t ldy, void* ws, size_t ws_bytes, hipStream_t stream);

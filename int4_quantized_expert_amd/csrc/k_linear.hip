@@ -224,7 +224,7 @@ __device__ __forceinline__ h8 codes_h8(uint32_t even, uint32_t odd) {
 __device__ __forceinline__ float activate(float v, int act) {
   float s, miss;
   switch (act) {
-    case MOE_ACT_RELU: return v > 0.0f ? v : 0.0f;
+    case MOE_ACT_RELU: return v <= 0.0f ? 0.0f : v;  // NaN stays
     case MOE_ACT_SILU: sigmoid2(v, s, miss); return v * s;
     case MOE_ACT_GELU: return 0.5f * v * erfcf(v * -0.707106781f);
     case MOE_ACT_GELU_TANH: sigmoid2(1.59576912f * v * fmaf(0.044715f * v, v, 1.0f), s, miss); return v * s;
@@ -809,9 +809,7 @@ __global__ __launch_bounds__(kSlimLanes, 2) void k_linear_slim(LinearArgs a, int
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
   const int rw = wave % RW, kw = wave / RW;
   const int b0 = blockIdx.y * kblocks, nblk = min(kblocks, a.nb - b0), nq = (nblk + 3) / 4;
-
   const int t0 = blockIdx.z * 16 * NT;
-
   const int tk = threadIdx.x & 15, g0 = threadIdx.x >> 4, ng = nblk * 4;
   Granule<TX> raw[NT][kRounds];
 #pragma unroll

@@ -197,6 +197,55 @@ def test_extreme_activations(T, N, dtype):
             assert torch.equal(y2[keep], y[keep])
 
 
+@pytest.mark.parametrize("act", list(ACT))
+@pytest.mark.parametrize("T,N", [(2, 128), (20, 128), (70, 6144)])
+def test_nan_stays_behind_every_activation(T, N, act):
+    rng = np.random.default_rng(N)
+    K = 64
+    _, _, codes, scales = _weights(rng, N, K, 4, 0)
+    x, _ = _x(rng, T, K, "f32")
+    x[1, 7] = float("nan")
+    y = _call(moe.LinearConfig(N, K, 4, 0, ACT[act]), codes, scales, x, N // 2 if act == "swiglu" else N)
+    assert bool(y[1].isnan().all()) and bool(y[0].isfinite().all()) and bool(y[2:].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype,pad,shift", [("f32", 0, 0), ("f32", 1, 3), ("bf16", 8, 0), ("bf16", 3, 1), ("f16", 24, 8),
+                                             ("f16", 0, 1)])
+@pytest.mark.parametrize("T,N,K", [(100, 4160, 8352), (130, 4096, 16448)])
+def test_long_rows_in_batches(T, N, K, dtype, pad, shift):
+    """Rows longer than the lanes that convert them hold at once, aligned and not; the residual in place in a buffer
+    whose rows are four apart, and one whose rows are not."""
+    rng = np.random.default_rng(K + pad)
+    q, s, codes, scales = _weights(rng, N, K, 4, 0, whole=True)
+    x, x64 = _x(rng, T, K, dtype, pad, shift, whole=True)
+    res = torch.from_numpy(rng.integers(-64, 65, (T, N)).astype(np.float32)).to(DT[dtype]).to(DEV)
+    want = torch.mm(torch.from_numpy(x64).to(DEV), torch.from_numpy(q * s).to(DEV).t().contiguous())
+    want = (want + res.double()).float().to(DT[dtype])
+    for extra in (4, 3):
+        y = torch.full((T + 1, N + extra), 9.0, dtype=DT[dtype], device=DEV)
+        y[:T, :N] = res
+        assert torch.equal(_call(moe.LinearConfig(N, K), codes, scales, x, N, res=y[:T, :N], y=y), want)
+
+
+def test_calls_at_once():
+    """Calls on two streams that run at the same time, each with its own workspace."""
+    rng = np.random.default_rng(5)
+    N, K = 6144, 1024
+    _, _, codes, scales = _weights(rng, N, K, 4, 64)
+    cfg = moe.LinearConfig(N, K, 4, 64)
+    xs = [_x(rng, T, K, "bf16")[0] for T in (2, 40, 300, 700)]
+    want = [_call(cfg, codes, scales, x, N).clone() for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [torch.empty((x.shape[0], N), dtype=torch.bfloat16, device=DEV) for x in xs]
+    ws = [torch.empty(moe.moe_linear_workspace_bytes(cfg, x.shape[0]), dtype=torch.uint8, device=DEV) for x in xs]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for x, y, w, st in zip(xs, got, ws, streams):
+            moe.moe_linear(cfg, codes, scales, x, y, w, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_codes_beyond_2_to_the_31_elements():
     """Rows beyond 2^31 code elements apart (a head of 131,072 rows over 16,416 columns)."""
     N, K, T = 131072, 16416, 2
