@@ -16,7 +16,7 @@
 #include <type_traits>
 
 #include "moe_float.h"
-#include "moe_internal.h"
+#include "moe_ops.h"
 
 namespace moe {
 
@@ -292,9 +292,11 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, int t, int col, int
 
 // ------------------------------------------------------------ product
 // A wavefront multiplies 32*TT tokens by two fragments of 32 weight rows (64 consecutive rows; with SwiGLU 32 gate
-// rows and the 32 up rows that go with them) with v_mfma_f32_32x32x16_f16; four wavefronts of a workgroup take the same
-// tokens. A code fragment costs 10 vector instructions to unpack and serves TT matrix instructions of 8 passes, so
-// with TT = 4 the unpacking hides behind them.
+// rows and the 32 up rows that go with them) with v_mfma_f32_32x32x16_f16; RW wavefronts of a workgroup take the same
+// tokens. A code fragment costs 10 vector instructions to unpack and serves TT matrix instructions of 8 passes: with
+// TT = 4 the unpacking fits between them, with TT = 1 it takes the longer time. 2,048 tokens 12288 x 6144 with SwiGLU:
+// 178 us for the 512 whole tiles and 98 for the rest, 1.16 PFLOP/s and 1.05, matrix instructions busy for 61% and 53%;
+// 191 tokens 6144 x 2048 int8 at TT = 1: 18 us. fp32 at TT = 1, 1,001 tokens 6144 x 4096: 107 us, 0.94 PFLOP/s of halves.
 // The activations of a step (two blocks of columns) pass through LDS in two buffers: the next step's are loaded to
 // registers while this one is multiplied. Each wavefront reads its own codes from memory into registers, also a step
 // ahead.
@@ -552,8 +554,9 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int wt0, int t0, c
 }
 
 // Tiles of 32*BT tokens by 256 rows, numbered so that 8 row tiles are walked by all token tiles; a launch takes `count`
-// of them from `first` on, each cut into BT / TT by 4 / RW workgroups of 32*TT tokens and 64*RW rows. Workgroups go to the eight dies in turn:
-// die d takes the d-th eighth of a launch, so that what a die works on at a time shares its cache.
+// of them from `first` on, each cut into BT / TT by 4 / RW workgroups of 32*TT tokens and 64*RW rows. Workgroups go to
+// the eight dies in turn: die d takes the d-th eighth of a launch, so that what a die works on at a time shares its
+// cache.
 constexpr int kTileRowGroup = 8, kDies = 8;
 template <class TX, int GSH>
 constexpr int base_frags() {  // 128 tokens need too many registers with two halves of them or a second set of sums

@@ -7,7 +7,7 @@
 #include <type_traits>
 
 #include "moe_float.h"
-#include "moe_internal.h"
+#include "moe_ops.h"
 
 namespace moe {
 

@@ -174,8 +174,9 @@ static int prof_begin() {
   return g_prof.n++;
 }
 
-int fwd_setup(const moe_config* cfg, const WeightView& wv, int32_t T, void* ws, size_t ws_bytes,
-              const moe_taps* tp, Fwd* f, bool any_ids) {
+// any_ids: the ids come from the caller and may repeat within a token, so a bucket may hold more than T positions
+static int setup(const moe_config* cfg, const WeightView& wv, int32_t T, void* ws, size_t ws_bytes,
+                 const moe_taps* tp, Fwd* f, bool any_ids) {
   int rc;
   if ((rc = check_tokens(cfg, T))) return rc;
   f->cfg = cfg;
@@ -259,6 +260,11 @@ int fwd_setup(const moe_config* cfg, const WeightView& wv, int32_t T, void* ws, 
   // many buckets stream at once: the GEMV keeps more blocks in flight
   f->many = L.TK + L.NS > 40;
   return MOE_OK;
+}
+
+int fwd_setup(const moe_config* cfg, const WeightView& wv, int32_t T, void* ws, size_t ws_bytes,
+              const moe_taps* tp, Fwd* f) {
+  return setup(cfg, wv, T, ws, ws_bytes, tp, f, false);
 }
 
 static DispatchArgs fwd_dispatch_args(const Fwd& f) {
@@ -432,9 +438,14 @@ constexpr int kSelfDispatchMaxSlots = 512;
 // One resident-layer forward on `stream`. With use_helper the MFMA chain runs on
 // the helper stream beside the GEMV chain (fork/join); without it both chains
 // run one after the other on `stream` and nothing is created.
-int32_t layer_forward_impl(const moe_config* cfg, const moe_layer_weights* wts, const float* x, int32_t T, float* y,
-                           void* ws, size_t ws_bytes, const moe_taps* taps, hipStream_t stream, bool use_helper,
-                           const Routing* given) {
+// given: the routing, null for the layer's own router.
+struct Routing {
+  const int32_t* ids;  // [T][K]
+  const float* w;      // [T][K]
+};
+static int32_t layer_forward(const moe_config* cfg, const moe_layer_weights* wts, const float* x, int32_t T, float* y,
+                             void* ws, size_t ws_bytes, const moe_taps* taps, hipStream_t stream, bool use_helper,
+                             const Routing* given) {
   int rc = validate_config(cfg);
   if (rc) return rc;
   if (!wts || !x || !y) return MOE_E_NULL;
@@ -446,7 +457,7 @@ int32_t layer_forward_impl(const moe_config* cfg, const moe_layer_weights* wts, 
     return MOE_E_ARG;
   WeightView wv{wts->w13, wts->s13, wts->w2, wts->s2, wts->sh_w13, wts->sh_s13, wts->sh_w2, wts->sh_s2, nullptr};
   Fwd f;
-  if ((rc = fwd_setup(cfg, wv, T, ws, ws_bytes, taps, &f, given != nullptr))) return rc;
+  if ((rc = setup(cfg, wv, T, ws, ws_bytes, taps, &f, given != nullptr))) return rc;
   if (given) {  // read only from here on
     f.ids = const_cast<int32_t*>(given->ids);
     f.w = const_cast<float*>(given->w);
@@ -516,6 +527,11 @@ int32_t layer_forward_impl(const moe_config* cfg, const moe_layer_weights* wts, 
   return e == hipSuccess ? MOE_OK : hip_fail(e);
 }
 
+int32_t layer_forward_impl(const moe_config* cfg, const moe_layer_weights* wts, const float* x, int32_t T, float* y,
+                           void* ws, size_t ws_bytes, const moe_taps* taps, hipStream_t stream, bool use_helper) {
+  return layer_forward(cfg, wts, x, T, y, ws, ws_bytes, taps, stream, use_helper, nullptr);
+}
+
 }  // namespace moe
 
 extern "C" {
@@ -530,7 +546,7 @@ int32_t moe_layer_forward_routed(const moe_config* cfg, const moe_layer_weights*
                                  const moe_taps* taps, hipStream_t stream) {
   if (taps && (taps->topk_ids || taps->topk_w || taps->near_tie)) return MOE_E_ARG;
   const Routing given{ids, w};
-  return layer_forward_impl(cfg, wts, x, T, y, ws, ws_bytes, taps, stream, true, &given);
+  return layer_forward(cfg, wts, x, T, y, ws, ws_bytes, taps, stream, true, &given);
 }
 
 int32_t moe_prof_enable(int32_t max_calls, uint32_t stage_mask) {

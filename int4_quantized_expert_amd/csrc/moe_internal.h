@@ -137,22 +137,16 @@ struct Fwd {
   ExpertArgs a;
 };
 
-// any_ids: the ids come from the caller and may repeat within a token, so a bucket may hold more than T positions
 int fwd_setup(const moe_config* cfg, const WeightView& wv, int32_t T, void* ws, size_t ws_bytes, const moe_taps* tp,
-              Fwd* f, bool any_ids = false);
+              Fwd* f);
 // router + top-K + Q8_0(x), and the dispatch unless defer_dispatch (then fwd_dispatch launches it)
 hipError_t fwd_front(Fwd& f, const float* x, const float* router_w, const float* router_bias, const moe_taps* tp,
                      hipStream_t stream, int call, bool defer_dispatch = false);
 hipError_t fwd_dispatch(Fwd& f, hipStream_t stream);
 hipError_t fwd_combine(Fwd& f, float* y, hipStream_t stream);
-// moe_layer_forward with or without the helper stream (see moe_api.hip), routed by its own router or by the caller
-struct Routing {
-  const int32_t* ids;  // [T][K]
-  const float* w;      // [T][K]
-};
+// moe_layer_forward with or without the helper stream (see moe_api.hip)
 int32_t layer_forward_impl(const moe_config* cfg, const moe_layer_weights* wts, const float* x, int32_t T, float* y,
-                           void* ws, size_t ws_bytes, const moe_taps* taps, hipStream_t stream, bool use_helper,
-                           const Routing* given = nullptr);
+                           void* ws, size_t ws_bytes, const moe_taps* taps, hipStream_t stream, bool use_helper);
 int32_t hip_fail(hipError_t e);
 // Arrays the kernels read or write as 16-byte vectors must start on a 16-byte boundary.
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -293,21 +287,6 @@ hipError_t launch_mfma_gateup(const ExpertArgs& a, int grid, int ntt, bool group
                               const int32_t* n_tiles, hipStream_t st);
 hipError_t launch_mfma_down(const ExpertArgs& a, int grid, int ntt, bool grouped, const int32_t* tiles,
                             const int32_t* n_tiles, hipStream_t st);
-// routing from logits and its gradients (k_route.hip)
-size_t route_ws_bytes(int E, int T);
-hipError_t launch_moe_route(const moe_route_config& c, const void* logits, int dtype, int64_t ld, int T,
-                            const float* bias, const uint8_t* valid, int32_t* ids, float* w, int32_t* load, float* imp,
-                            void* ws, hipStream_t st);
-hipError_t launch_moe_route_grad(const moe_route_config& c, const void* logits, int dtype, int64_t ld, int T,
-                                 const uint8_t* valid, const int32_t* ids, const float* dw, const float* dimp, void* dz,
-                                 int64_t ld_d, hipStream_t st);
-hipError_t launch_slot_grad(const float* eout, const int32_t* ids, const float* dy, int T, int K, int H, float* dw,
-                            hipStream_t st);
-// product over weight codes with its epilogue (k_linear.hip)
-size_t linear_ws_bytes(const moe_linear_config& c, int64_t T);
-hipError_t launch_linear(const moe_linear_config& c, const uint8_t* codes, const float* scales, const float* bias,
-                         const void* x, int64_t ldx, int T, int dtype, const void* res, int64_t ldr, void* y,
-                         int64_t ldy, void* ws, hipStream_t st);
 hipError_t launch_combine(const float* eout, const float* w, const int32_t* slotpos, int T, const moe_config& c,
                           float* y, hipStream_t st);
 

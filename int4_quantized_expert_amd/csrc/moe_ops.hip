@@ -2,7 +2,7 @@
 // anything is enqueued. Nothing here synchronizes, allocates or keeps state.
 #include <cmath>
 
-#include "moe_internal.h"
+#include "moe_ops.h"
 
 using namespace moe;
 
