@@ -482,9 +482,9 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int wt0, int t0, c
   } else {
     // 64 tokens and two groups of columns: the second group, the other wavefront of each SIMD, unpacks the next step's
     // codes behind its matrix instructions, so that between two barriers one's unpacking runs beside the other's products
-    // (400 tokens, 8192 x 4096: 45.7 us, 49.4 with both in front). With 32 tokens it was up to 5% slower, and reading
-    // codes two or three steps ahead gained nothing.
-    const bool late = TT == 2 && KW == 2 && kw > 0;
+    // (400 tokens, 8192 x 4096: 45.7 us, 49.4 with both in front). With 32 tokens it was up to 5% slower, with a scale a
+    // block it takes too many registers, and reading codes two or three steps ahead gained nothing.
+    const bool late = TT == 2 && KW == 2 && GSH != 0 && kw > 0;
     if (late && p0 < p1) {
       unpack(wf, sc);
       fetch_w(min(p0 + 1, p1 - 1));
@@ -710,7 +710,9 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 // Up to 4 tokens (TOK 1 or 4): a workgroup finishes 16*F rows in one launch. Its wavefronts share the columns; each
-// converts its own columns of the tokens, with a power of two of its own, and waits for no other before the sum.
+// converts its own columns of the tokens, with a power of two of its own, and waits for no other before the sum. Bound
+// by the latency of one pass over the codes: 1 token, 6144 x 6144 int4, 8.4 us on codes that come from HBM (19 MB: 3.6 to
+// 4.0 by a plain read), 10.4 in the form below; 4 tokens 10.1 and 11.2; 4096 x 2048 4.5 and 7.6.
 constexpr int kTinyWaves = 8;
 constexpr int tiny_rounds(size_t size) { return size == 4 ? 4 : 8; }  // granules of 32 bytes or 16 that a lane converts
 
@@ -813,7 +815,8 @@ __global__ __launch_bounds__(64 * kTinyWaves, 4) void k_linear_tiny(LinearArgs a
 
 // More: a workgroup takes 128 rows (64 gate and 64 up) by 16*NT tokens over a part of the columns, because every
 // workgroup reads and converts the activations of its columns; four wavefronts of 32 rows for each half of them. Parts
-// are added by k_linear_join.
+// are added by k_linear_join. 32 tokens, 4096 x 6144 int4 g64 with SwiGLU: 10.9 us and 2.3 to add, on 15 MB; latency: the
+// conversion, then three quads of codes a wavefront, then the sum.
 constexpr int kSlimRowWaves = 4, kSlimColWaves = 2, kSlimLanes = 64 * kSlimRowWaves * kSlimColWaves;
 constexpr int kSlimRounds = 8;  // granules that a lane converts, over all token fragments
 
@@ -1068,7 +1071,10 @@ void few_tokens(const LinearArgs& a, float* ws, hipStream_t st) {
 
 // More tokens. What fills the card twice over (two workgroups on each of 256 compute units) runs in whole tiles of four
 // wavefronts; of what is left, up to 256 tiles run one a compute unit, with eight wavefronts that share the columns, and
-// fewer than that are cut into halves or quarters first.
+// fewer than that are cut into halves or quarters first. Each step against the one before it, us: 128 x 256 tiles, 256
+// of them 103 against 111, 128 44.7 / 62.6, 48 22.0 / 28.1 (2,048 columns; 6,144 42.4 / 71.8), 24 22.0 / 30.6; 64 x 256
+// tiles of group scales 384 of them 88 / 87, 192 52.7 / 63.9, 96 39.1 / 50.9, 48 25.6 / 38.5, of fp32 111 / 119, 77 / 75,
+// 42 / 74, 30 / 40.
 constexpr int kUnits = 256;
 template <class TX, int W, int GSH>
 void tile_launch(const LinearArgs& a, hipStream_t st) {
@@ -1096,12 +1102,25 @@ void tile_launch(const LinearArgs& a, hipStream_t st) {
         at += left;
       }
     } else {
-      if (left >= 2 * kUnits) k_linear_tile<TX, 2, W, GSH, 4, 1><<<left, 256, 0, st>>>(a, row_tiles, tok_tiles, at, left);
-      else if (left > kUnits) k_linear_tile<TX, 1, W, GSH, 4, 1><<<2 * left, 256, 0, st>>>(a, row_tiles, tok_tiles, at, left);
-      else if (left > kUnits / 2) k_linear_tile<TX, 2, W, GSH, 4, 2><<<left, 512, 0, st>>>(a, row_tiles, tok_tiles, at, left);
-      else if (left > kUnits / 4) k_linear_tile<TX, 1, W, GSH, 4, KQ><<<2 * left, 256 * KQ, 0, st>>>(a, row_tiles, tok_tiles, at, left);
-      else k_linear_tile<TX, 1, W, GSH, 2, 2 * KQ><<<4 * left, 256 * KQ, 0, st>>>(a, row_tiles, tok_tiles, at, left);
-      at += left;
+      // fp32 with a scale a block: 64 tokens take too many registers (2,048 tokens 12288 x 4096: 466 us with 32, 488)
+      constexpr bool kWhole = GSH != 0 || !std::is_same<TX, float>::value;
+      int n = left;
+      if (kWhole && left >= 2 * kUnits) {
+        // a last turn of few tiles is cut too (bf16 with group scales, us: 64 over 134 whole, 114 cut; 32 118 / 109; fp32 128
+        // 281 / 282; 176 210 / 216; 400 190 / 220)
+        const int over = left % (2 * kUnits);
+        n = over > kUnits / 2 ? left : left - over;
+        k_linear_tile<TX, kWhole ? 2 : 1, W, GSH, 4, 1><<<n, 256, 0, st>>>(a, row_tiles, tok_tiles, at, n);
+      } else if (left > kUnits) {
+        k_linear_tile<TX, 1, W, GSH, 4, 1><<<2 * left, 256, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+      } else if (left > kUnits / 2) {
+        k_linear_tile<TX, 2, W, GSH, 4, 2><<<left, 512, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+      } else if (left > kUnits / 4) {
+        k_linear_tile<TX, 1, W, GSH, 4, KQ><<<2 * left, 256 * KQ, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+      } else {
+        k_linear_tile<TX, 1, W, GSH, 2, 2 * KQ><<<4 * left, 256 * KQ, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+      }
+      at += n;
     }
   }
 }

@@ -158,7 +158,8 @@ __device__ __forceinline__ void merge_top2_dpp(int& a, int& b) {
 // best groups stay, the lower index first on equal scores. *near is set where the last kept and the first dropped
 // group lie within thr + 1e-6 (|a| + |b|).
 // glog >= 0: a group is 2^glog whole lanes, its two largest are merged across them in registers; else its run is
-// scanned in LDS by one lane. 32,768 tokens x 256 experts in 8 groups: 73 us for the kernel with the scan alone.
+// scanned in LDS by one lane. 32,768 tokens x 256 experts in 8 groups: 33.9 us with the merge, 43.2 with the scan; one
+// token 3.8 and 5.1.
 template <int NE>
 __device__ __forceinline__ uint32_t keep_groups(const int (&g)[NE], int E, int G, int KG, int glog, bool gmax, int lane,
                                                 int* s_row, float thr, bool* near) {
@@ -313,9 +314,11 @@ __device__ __forceinline__ float sigmoid_fast(float z) {
 constexpr int resident_waves(int ne) { return ne <= 4 ? 6 : ne == 8 ? 4 : 2; }
 
 // The definition compares fl32(score) + bias, the score taken in 64 bits, so that every implementation chooses the
-// same experts. Taking 256 exponentials a token in 64 bits is most of the work; so the choice is made with 32-bit
+// same experts. Taking 256 exponentials a token in 64 bits would be most of the work; so the choice is made with 32-bit
 // scores, and a token where two neighbours in the order (or two groups) lie closer than twice the error of those (see
 // thr) is set aside and done once more with the definition's: 2 tokens in 1,000 of 256 biased sigmoid scores.
+// Bound by instruction issue, not by its bytes: 330 vector and 270 scalar instructions a token of 256 experts in 8
+// groups with bias and statistics, 33.9 us for 32,768 of them (36 MB); one token 3.8 us, 192 softmax ones of 128 5.0.
 template <int NE, class TZ, bool SOFTMAX, bool STATS, int WV>
 __global__ __launch_bounds__(64 * WV, resident_waves(NE)) void k_route(RouteArgs a) {
   __shared__ __align__(8) int s_row[WV][64 * NE];  // a wavefront's scratch
@@ -533,6 +536,12 @@ __global__ __launch_bounds__(1024) void k_route_stats(const int32_t* __restrict_
 }
 
 // ------------------------------------------------------------ backward
+// With renormalised weights w_k = scale * r_k, r = s / (sum of the chosen s): dz_k = r_k (u_k - sum_j r_j u_j) m_k, where
+// u = scale * dw and m = 1 for softmax scores (their sum cancels), 1 - s for sigmoid ones; without, dz_k = s_k (1 - s_k)
+// u_k, or p_e (u_e - sum_j p_j u_j) over all experts. Importance p = s / (sum of s): p_e (g_e - sum_f p_f g_f) m_e.
+// One wavefront a token; a slot's part goes through LDS to the lane that holds its expert, and a row is read and written
+// once. 32,768 x 256 sigmoid with importance: 18.4 us for 69 MB (10.8 at 6.4 TB/s), bound by instruction issue, 186
+// vector instructions a token; 381 x 128 softmax 3.1 us.
 struct RouteGradArgs {
   const void* logits;
   int64_t ld, ld_d;
@@ -682,7 +691,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_grad(RouteGradArgs a) {
 // ------------------------------------------------------------ gradient of the routing weights
 // dw[t][k] = sum_h dy[t][h] e_out[t*K + k][h]. Reads every slot's row once: HBM-bound. One wavefront takes one slot,
 // eight 16-byte loads of its row in flight (not kept in the caches); the K slots of a token sit next to each other, so
-// dy comes from the caches after the first.
+// dy comes from the caches after the first. 2,048 x 8 x 6144: 70.4 us, 6.4 TB/s (80.4 with one load in flight).
 constexpr int kSlotLoads = 8;
 typedef float f4v __attribute__((ext_vector_type(4)));
 __global__ __launch_bounds__(256) void k_slot_grad(const float* __restrict__ eout, const int32_t* __restrict__ ids,
@@ -723,7 +732,7 @@ __global__ __launch_bounds__(256) void k_slot_grad(const float* __restrict__ eou
 // ------------------------------------------------------------ launches
 constexpr int kSimds = 1024;
 // With statistics a workgroup leaves one row of partial sums; from this many tokens on it has 8 wavefronts, so that
-// there are at most 768 rows to add up.
+// there are at most 768 rows to add up (32,768 x 256: 5.2 us for them, 8.2 for twice as many).
 constexpr int kRouteWideT = 2048;
 constexpr int kWideWaves = 8;
 
