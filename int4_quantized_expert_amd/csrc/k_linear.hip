@@ -709,19 +709,25 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Up to 4 tokens (TOK 1 or 4): a workgroup finishes 16*F rows in one launch. Its wavefronts share the columns; each
-// converts its own columns of the tokens, with a power of two of its own, and waits for no other before the sum. Bound
-// by the latency of one pass over the codes: 1 token, 6144 x 6144 int4, 8.4 us on codes that come from HBM (19 MB: 3.6 to
-// 4.0 by a plain read), 10.4 in the form below; 4 tokens 10.1 and 11.2; 4096 x 2048 4.5 and 7.6.
+// Up to 4 tokens (TOK 1 or 4): a workgroup finishes 16 rows (with SwiGLU 16 gate and 16 up rows) in one launch. Its
+// wavefronts share the columns; each converts its own columns of the tokens, with a power of two of its own, and waits
+// for no other before the sum. Bound by the latency of one pass over the codes: 1 token, 6144 x 6144 int4, 8.4 us on
+// codes that come from HBM (19 MB: 3.6 to 4.0 by a plain read), 10.4 in the form below; 4 tokens 10.1 and 11.2; 4096 x
+// 2048 4.5 and 7.6.
+// TURNS: rows for more than three times the workgroups that run at a time, a head's: a workgroup converts once and takes
+// its share of the rows in turns, the next rows' codes on their way while it finishes some. 32768 x 6144, 1 token: 24.0
+// us, 27.4 without; 65536 x 4096 g64, 3 tokens: 40.3 and 48.3; three turns (16448 rows) 18.0 and 16.9, two of SwiGLU (24576
+// rows) 19.1 and 17.9.
 constexpr int kTinyWaves = 8;
+constexpr int kTinyGroups = 512;  // workgroups at most: two a compute unit
 constexpr int tiny_rounds(size_t size) { return size == 4 ? 4 : 8; }  // granules of 32 bytes or 16 that a lane converts
 
-template <class TX, int TOK, int W, int GSH, int F>
+template <class TX, int TOK, int W, int GSH, int F, bool TURNS>
 __global__ __launch_bounds__(64 * kTinyWaves, 4) void k_linear_tiny(LinearArgs a) {
   constexpr int NX = std::is_same<TX, float>::value ? 2 : 1;
   constexpr int kRing = W == 8 || F == 2 ? 3 : 4;  // quads of codes in flight
   extern __shared__ __align__(16) _Float16 xs[];   // per wavefront [NX][its blocks][4][TOK][8]
-  __shared__ float s_sum[kTinyWaves][F][TOK][16];
+  __shared__ float s_sum[TURNS ? 2 : 1][kTinyWaves][F][TOK][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, rt = min(lane & 15, TOK - 1);
   const int nq = (a.nb + 3) / 4, per = (nq + kTinyWaves - 1) / kTinyWaves;
   const int qa = min(wave * per, nq), qb = min(qa + per, nq);
@@ -734,12 +740,20 @@ __global__ __launch_bounds__(64 * kTinyWaves, 4) void k_linear_tiny(LinearArgs a
   for (int k = 0; k < kRounds; ++k)
     if (g0 + k * kPer < ng) load8(xrow + (g0 + k * kPer) * 8, a.vec_x, raw[k]);
   __builtin_amdgcn_sched_barrier(0);
-  const int out0 = blockIdx.x * (a.half ? 16 : 16 * F);
-  const Rows<W, GSH, F> rows(a, out0, lane);
+  const int outs = a.half ? a.half : a.N;
+  constexpr int kOuts = 16;  // of a workgroup at a time
+  int out0 = blockIdx.x * kOuts;
+  Rows<W, GSH, F> rows(a, out0, lane);
   Quad<W, GSH> ring[kRing][F];
+  float scale[F];
+  auto begin = [&]() __attribute__((always_inline)) {
 #pragma unroll
-  for (int k = 0; k < kRing; ++k)
-    if (qa + k < qb) rows.load(ring[k], 4 * (qa + k));
+    for (int f = 0; f < F; ++f) scale[f] = TURNS && GSH < 0 ? *rows.scale[f] : 1.0f;
+#pragma unroll
+    for (int k = 0; k < kRing; ++k)
+      if (qa + k < qb) rows.load(ring[k], 4 * (qa + k));
+  };
+  begin();
   __builtin_amdgcn_sched_barrier(0);
   bool finite = true;
   int sh = 0;
@@ -768,48 +782,60 @@ __global__ __launch_bounds__(64 * kTinyWaves, 4) void k_linear_tiny(LinearArgs a
   }
   wave_sync();
   f4v acc[1][F];
-#pragma unroll
-  for (int f = 0; f < F; ++f) acc[0][f] = f4v{0.0f, 0.0f, 0.0f, 0.0f};
   auto multiply = [&](Quad<W, GSH> (&d)[F], int q) __attribute__((always_inline)) {
     multiply_quad<NX, 1, TOK, W, GSH, F>(d, x + (q - qa) * 128 * TOK, stride, rt, g, acc);
   };
-  int q0 = qa;
-  for (; q0 + kRing < qb; q0 += kRing) {
+  for (int buf = 0;; buf ^= TURNS) {
 #pragma unroll
-    for (int k = 0; k < kRing; ++k) {
-      multiply(ring[k], q0 + k);
-      rows.load(ring[k], 4 * min(q0 + k + kRing, qb - 1));
+    for (int f = 0; f < F; ++f) acc[0][f] = f4v{0.0f, 0.0f, 0.0f, 0.0f};
+    int q0 = qa;
+    for (; q0 + kRing < qb; q0 += kRing) {
+#pragma unroll
+      for (int k = 0; k < kRing; ++k) {
+        multiply(ring[k], q0 + k);
+        rows.load(ring[k], 4 * min(q0 + k + kRing, qb - 1));
+      }
     }
-  }
 #pragma unroll
-  for (int k = 0; k < kRing; ++k)
-    if (q0 + k < qb) multiply(ring[k], q0 + k);
-  // lane group 0 holds the real tokens: row r, token j; token j's power of two is in lane j
+    for (int k = 0; k < kRing; ++k)
+      if (q0 + k < qb) multiply(ring[k], q0 + k);
+    // lane group 0 holds the real tokens: row r, token j; token j's power of two is in lane j
 #pragma unroll
-  for (int j = 0; j < TOK; ++j) {
-    const int back = -__builtin_amdgcn_readlane(sh, j);
-    if (g == 0)
+    for (int j = 0; j < TOK; ++j) {
+      const int back = -__builtin_amdgcn_readlane(sh, j);
+      if (g == 0)
 #pragma unroll
-      for (int f = 0; f < F; ++f) s_sum[wave][f][j][lane] = ldexpf(acc[0][f][j], back);
-  }
-  __syncthreads();
-  if (threadIdx.x >= 16 * TOK) return;
-  const int j = threadIdx.x >> 4, r = threadIdx.x & 15;
-  if (j >= a.T) return;
-  float v[F];
+        for (int f = 0; f < F; ++f) s_sum[buf][wave][f][j][lane] = ldexpf(acc[0][f][j], back);
+    }
+    const int at = out0;
+    float rs[F];
 #pragma unroll
-  for (int f = 0; f < F; ++f) {
-    v[f] = s_sum[0][f][j][r];
+    for (int f = 0; f < F; ++f) rs[f] = scale[f];
+    out0 += gridDim.x * kOuts;
+    const bool more = TURNS && out0 < outs;
+    if (more) {  // the next rows' codes are on their way while these are finished
+      rows = Rows<W, GSH, F>(a, out0, lane);
+      begin();
+    }
+    __syncthreads();  // the only one a turn: a buffer is written again two turns on
+    const int j = threadIdx.x >> 4, r = threadIdx.x & 15;
+    if (threadIdx.x < 16 * TOK && j < a.T) {
+      float v[F];
 #pragma unroll
-    for (int w = 1; w < kTinyWaves; ++w) v[f] += s_sum[w][f][j][r];  // columns in ascending order
-    const int row = a.half ? f * a.half + out0 + r : out0 + 16 * f + r;
-    if (GSH < 0) v[f] *= a.scales[row];
-  }
-  if (a.half) {
-    finish<TX>(a, j, out0 + r, v[0], v[F - 1]);
-  } else {
+      for (int f = 0; f < F; ++f) {
+        v[f] = s_sum[buf][0][f][j][r];
 #pragma unroll
-    for (int f = 0; f < F; ++f) finish<TX>(a, j, out0 + 16 * f + r, v[f], 0.0f);
+        for (int w = 1; w < kTinyWaves; ++w) v[f] += s_sum[buf][w][f][j][r];  // columns in ascending order
+        if (TURNS) v[f] *= rs[f];
+        else if (GSH < 0) v[f] *= a.scales[a.half ? f * a.half + at + r : at + r];
+      }
+      if (a.half) {
+        finish<TX>(a, j, at + r, v[0], v[F - 1]);
+      } else {
+        finish<TX>(a, j, at + r, v[0], 0.0f);
+      }
+    }
+    if (!more) break;
   }
 }
 
@@ -1038,8 +1064,12 @@ template <class TX, int TOK, int F, int W, int GSH>
 void tiny_launch(const LinearArgs& a, hipStream_t st) {
   constexpr int NX = std::is_same<TX, float>::value ? 2 : 1;
   const int quads = (a.nb + 3) / 4, per = (quads + kTinyWaves - 1) / kTinyWaves;
-  const int rows = a.half ? a.half / 16 : a.N / (16 * F);
-  k_linear_tiny<TX, TOK, W, GSH, F><<<rows, 64 * kTinyWaves, (size_t)kTinyWaves * per * 256 * TOK * NX, st>>>(a);
+  const int rows = (a.half ? a.half : a.N) / 16, turns = (rows + kTinyGroups - 1) / kTinyGroups;
+  const size_t lds = (size_t)kTinyWaves * per * 256 * TOK * NX;
+  if (F == 1 && turns > 3)
+    k_linear_tiny<TX, TOK, W, GSH, F, F == 1><<<(rows + turns - 1) / turns, 64 * kTinyWaves, lds, st>>>(a);
+  else
+    k_linear_tiny<TX, TOK, W, GSH, F, false><<<rows, 64 * kTinyWaves, lds, st>>>(a);
 }
 template <class TX, int NT, int W, int GSH>
 void slim_launch(const LinearArgs& a, float* ws, hipStream_t st) {

@@ -102,6 +102,22 @@ def test_whole_numbers_are_exact_in_large_batches(T, N, K, bits, group, act, dty
     assert torch.equal(y, want.float().to(DT[dtype]))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("bits,group,act", [(4, 0, "none"), (8, 0, "relu"), (4, 32, "none"), (4, 64, "none"), (4, 128, "none")])
+@pytest.mark.parametrize("T,N,K", [(1, 16448, 256), (3, 33024, 384), (4, 24640, 1152), (1, 8256, 2176)])
+def test_heads_are_exact(T, N, K, bits, group, act, dtype):
+    """Few tokens and many rows, whole numbers: a workgroup's rows in several turns, the last of them not full."""
+    rng = np.random.default_rng(T + N + K)
+    q, s, codes, scales = _weights(rng, N, K, bits, group, whole=True)
+    x, x64 = _x(rng, T, K, dtype, whole=True)
+    b = rng.integers(-64, 65, N).astype(np.float32)
+    y = _call(moe.LinearConfig(N, K, bits, group, ACT[act]), codes, scales, x, N, torch.from_numpy(b).to(DEV))
+    want = torch.mm(torch.from_numpy(x64).to(DEV), torch.from_numpy(q * np.repeat(s, K // s.shape[1], axis=1)).to(DEV).t().contiguous())
+    want = want + torch.from_numpy(b).to(DEV).double()
+    want = want.clamp(min=0) if act == "relu" else want
+    assert torch.equal(y, want.float().to(DT[dtype]))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T,N,K,bits,group", [(1024, 16384, 64, 4, 0), (600, 8064, 96, 8, 0), (300, 8192, 160, 4, 0),
                                               (191, 6080, 352, 4, 0), (520, 16320, 128, 4, 128), (33, 12352, 544, 4, 32)])
