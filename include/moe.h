@@ -384,7 +384,8 @@ size_t moe_linear_workspace_bytes(const moe_linear_config* cfg, int32_t max_toke
 
 /* x, residual and y are of `dtype`, with rows ldx, ldr and ldy elements apart; bias [rows] fp32 and residual may be
  * NULL; residual may be y itself (same pointer and stride), else y overlaps neither it nor x. codes are 16-byte
- * aligned, the others to their elements, ws 256 bytes. The sums W x of a token whose x holds an infinity or NaN are
+ * aligned, the others to their elements, ws 256 bytes. Scales of up to 2^80: a result in fp32's range is not lost where
+ * x times the codes is beyond it. The sums W x of a token whose x holds an infinity or NaN are
  * all infinite or NaN, and no activation turns a NaN into a number; other tokens are not touched by it.
  * 1 <= T <= 2^20. Errors: MOE_E_NULL, MOE_E_SHAPE, MOE_E_ARG, MOE_E_WORKSPACE, MOE_E_HIP. */
 int32_t moe_linear(const moe_linear_config* cfg, const uint8_t* codes, const float* scales, const float* bias,

@@ -722,12 +722,21 @@ constexpr int kTinyWaves = 8;
 constexpr int kTinyGroups = 512;  // workgroups at most: two a compute unit
 constexpr int tiny_rounds(size_t size) { return size == 4 ? 4 : 8; }  // granules of 32 bytes or 16 that a lane converts
 
+// One scale a row is taken apart into a power of two and a factor of 1 to 2: the former is applied together with the
+// token's to each wavefront's sum, the latter to the sum of all. So no partial result leaves fp32's range unless the
+// scaled one does (x near 1e36: the sum of its products with the codes is beyond), and the roundings are those of sum
+// times scale. The lanes that finish do it, with the powers of two through LDS: read earlier, the scales cost registers
+// in the loop (int8, 6144 x 6144, 1 token: 12.7 to 13.0 us, 12.3 so).
+__device__ __forceinline__ int scale_exp(float s) { return __builtin_amdgcn_frexp_expf(s) - 1; }
+__device__ __forceinline__ float scale_factor(float s) { return 2.0f * __builtin_amdgcn_frexp_mantf(s); }
+
 template <class TX, int TOK, int W, int GSH, int F, bool TURNS>
 __global__ __launch_bounds__(64 * kTinyWaves, 4) void k_linear_tiny(LinearArgs a) {
   constexpr int NX = std::is_same<TX, float>::value ? 2 : 1;
   constexpr int kRing = W == 8 || F == 2 ? 3 : 4;  // quads of codes in flight
   extern __shared__ __align__(16) _Float16 xs[];   // per wavefront [NX][its blocks][4][TOK][8]
   __shared__ float s_sum[TURNS ? 2 : 1][kTinyWaves][F][TOK][16];
+  __shared__ int s_sh[TURNS ? 2 : 1][kTinyWaves][TOK];  // read with one scale a row
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, rt = min(lane & 15, TOK - 1);
   const int nq = (a.nb + 3) / 4, per = (nq + kTinyWaves - 1) / kTinyWaves;
   const int qa = min(wave * per, nq), qb = min(qa + per, nq);
@@ -800,12 +809,21 @@ __global__ __launch_bounds__(64 * kTinyWaves, 4) void k_linear_tiny(LinearArgs a
     for (int k = 0; k < kRing; ++k)
       if (q0 + k < qb) multiply(ring[k], q0 + k);
     // lane group 0 holds the real tokens: row r, token j; token j's power of two is in lane j
-#pragma unroll
-    for (int j = 0; j < TOK; ++j) {
-      const int back = -__builtin_amdgcn_readlane(sh, j);
+    if constexpr (GSH < 0) {
       if (g == 0)
 #pragma unroll
-        for (int f = 0; f < F; ++f) s_sum[buf][wave][f][j][lane] = ldexpf(acc[0][f][j], back);
+        for (int j = 0; j < TOK; ++j)
+#pragma unroll
+          for (int f = 0; f < F; ++f) s_sum[buf][wave][f][j][lane] = acc[0][f][j];
+      if (lane < TOK) s_sh[buf][wave][lane] = sh;
+    } else {
+#pragma unroll
+      for (int j = 0; j < TOK; ++j) {
+        const int back = -__builtin_amdgcn_readlane(sh, j);
+        if (g == 0)
+#pragma unroll
+          for (int f = 0; f < F; ++f) s_sum[buf][wave][f][j][lane] = ldexpf(acc[0][f][j], back);
+      }
     }
     const int at = out0;
     float rs[F];
@@ -823,11 +841,18 @@ __global__ __launch_bounds__(64 * kTinyWaves, 4) void k_linear_tiny(LinearArgs a
       float v[F];
 #pragma unroll
       for (int f = 0; f < F; ++f) {
-        v[f] = s_sum[buf][0][f][j][r];
+        if constexpr (GSH < 0) {
+          const float sc = TURNS ? rs[f] : a.scales[a.half ? f * a.half + at + r : at + r];
+          const int e = scale_exp(sc);
+          v[f] = ldexpf(s_sum[buf][0][f][j][r], e - s_sh[buf][0][j]);
 #pragma unroll
-        for (int w = 1; w < kTinyWaves; ++w) v[f] += s_sum[buf][w][f][j][r];  // columns in ascending order
-        if (TURNS) v[f] *= rs[f];
-        else if (GSH < 0) v[f] *= a.scales[a.half ? f * a.half + at + r : at + r];
+          for (int w = 1; w < kTinyWaves; ++w) v[f] += ldexpf(s_sum[buf][w][f][j][r], e - s_sh[buf][w][j]);
+          v[f] *= scale_factor(sc);
+        } else {
+          v[f] = s_sum[buf][0][f][j][r];
+#pragma unroll
+          for (int w = 1; w < kTinyWaves; ++w) v[f] += s_sum[buf][w][f][j][r];  // columns in ascending order
+        }
       }
       if (a.half) {
         finish<TX>(a, j, at + r, v[0], v[F - 1]);

@@ -329,3 +329,23 @@ def test_streams_and_graph_replays(T, N, K):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(ya, yb)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bits,group", [(4, 0), (8, 0), (4, 64)])
+@pytest.mark.parametrize("T,N", [(1, 128), (2, 128), (4, 128), (5, 128), (20, 128), (70, 128), (70, 6144), (1, 24704),
+                                 (3, 24704)])
+@pytest.mark.parametrize("size,scale", [(3e37, 1.0), (1e-39, 1e24)])
+def test_sums_beyond_fp32_before_their_scales(T, N, bits, group, dtype, size, scale):
+    """Activations near fp32's largest, whose sums with the codes (about 70 or 1,200 times as large) leave its range
+    until the scales bring them back, and activations below its normal range under large scales. Both results lie far
+    inside the range (about 1e37 and 3e-16), so the bound has no term for overflow or underflow."""
+    rng = np.random.default_rng(T + N + bits)
+    K = 256
+    q, s, codes, scales = _weights(rng, N, K, bits, group)
+    s, scales = s * scale, scales * scale
+    s = np.float64(np.float32(s / scale) * np.float32(scale))  # as the device multiplies
+    x = torch.from_numpy((rng.normal(0, 1, (T, K)) * size).astype(np.float32)).to(DT[dtype])
+    y = _call(moe.LinearConfig(N, K, bits, group), codes, scales, x.to(DEV), N)
+    ref, err = R.linear(q, s, x.double().numpy())
+    assert np.all(np.abs(y.double().cpu().numpy() - ref) <= err + R.HALF_STEP[dtype] * (np.abs(ref) + err))
