@@ -355,6 +355,11 @@ int32_t moe_route_backward(const moe_route_config* cfg, const void* logits, int3
  * aligned. Errors: MOE_E_NULL, MOE_E_SHAPE, MOE_E_ARG, MOE_E_HIP. */
 int32_t moe_slot_weight_grad(const float* e_out, const int32_t* ids, const float* dy, int32_t T, int32_t K, int32_t H,
                              float* d_w, hipStream_t stream);
+/* The same for ids that drop a slot by any value outside [0, n_experts), as moe_layer_forward_routed and
+ * moe_route_backward take them: 0 for each of those. The entry above, which is not told the number of experts, would
+ * read a row of e_out that the layer never wrote. n_experts: 1..1024, else MOE_E_SHAPE. */
+int32_t moe_slot_weight_grad_experts(const float* e_out, const int32_t* ids, const float* dy, int32_t T, int32_t K,
+                                     int32_t H, int32_t n_experts, float* d_w, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
  * A product over the library's weight codes outside the experts: dense layers, projections, heads.

@@ -100,6 +100,7 @@ _sig("moe_route_workspace_bytes", SZ, [P, I32])
 _sig("moe_route", I32, [P, P, I32, I64, I32, P, P, P, P, P, P, P, SZ, P])
 _sig("moe_route_backward", I32, [P, P, I32, I64, I32, P, P, P, P, P, I64, P])
 _sig("moe_slot_weight_grad", I32, [P, P, P, I32, I32, I32, P, P])
+_sig("moe_slot_weight_grad_experts", I32, [P, P, P, I32, I32, I32, I32, P, P])
 _sig("moe_linear_workspace_bytes", SZ, [P, I32])
 _sig("moe_linear", I32, [P, P, P, P, P, I64, I32, I32, P, I64, P, I64, P, SZ, P])
 _sig("moe_expert_cache_create", I32, [P, I32, I32, ctypes.POINTER(P)])
@@ -121,7 +122,8 @@ EXPORTED = ("moe_version", "moe_strerror", "moe_last_hip_error", "moe_workspace_
             "moe_quantize_int8", "moe_quantize_int4_grouped", "moe_quantize_q8_0",
             "moe_tile_int4", "moe_tile_int8", "moe_tile_group_scales", "moe_router", "moe_dispatch", "moe_layer_forward",
             "moe_layer_forward_noalloc", "moe_layer_forward_routed", "moe_route_workspace_bytes", "moe_route",
-            "moe_route_backward", "moe_slot_weight_grad", "moe_linear_workspace_bytes", "moe_linear",
+            "moe_route_backward", "moe_slot_weight_grad", "moe_slot_weight_grad_experts",
+            "moe_linear_workspace_bytes", "moe_linear",
             "moe_expert_cache_create",
             "moe_expert_cache_forward", "moe_expert_cache_stats", "moe_expert_cache_usage", "moe_expert_cache_set_usage",
             "moe_expert_cache_pin_hottest", "moe_expert_cache_destroy", "moe_prof_enable",
@@ -580,8 +582,10 @@ def moe_route_backward(cfg: RouteConfig, logits, ids, d_logits, d_w=None, d_impo
                    _same_dev(d_logits, "d_logits", dev), ld_d)
 
 
-def moe_slot_weight_grad(e_out, ids, dy, d_w, stream=None):
-    """d_w [T][K] = <dy[t], e_out[t*K + k]>, 0 for dropped slots; e_out is the layer's tap (its first T*K rows)."""
+def moe_slot_weight_grad(e_out, ids, dy, d_w, stream=None, n_experts=None):
+    """d_w [T][K] = <dy[t], e_out[t*K + k]>, 0 for dropped slots; e_out is the layer's tap (its first T*K rows). With
+    n_experts every id outside [0, n_experts) drops its slot, as in moe_layer_forward_routed; without it only negative
+    ids do."""
     _need(ids, "ids", "i32")
     _need(dy, "dy", "f32")
     if ids.dim() != 2 or dy.dim() != 2 or dy.shape[0] < ids.shape[0]:
@@ -589,8 +593,9 @@ def moe_slot_weight_grad(e_out, ids, dy, d_w, stream=None):
     (T, K), H = ids.shape, dy.shape[1]
     _need(e_out, "e_out", "f32", rows=T * K, cols=H)
     dev = e_out.get_device()
-    return _launch(_lib.moe_slot_weight_grad, dev, stream, e_out.data_ptr(), _same_dev(ids, "ids", dev),
-                   _same_dev(dy, "dy", dev), T, K, H, _dev_ptr(d_w, "d_w", "f32", T * K, dev))
+    fn, limit = (_lib.moe_slot_weight_grad, ()) if n_experts is None else (_lib.moe_slot_weight_grad_experts, (n_experts,))
+    return _launch(fn, dev, stream, e_out.data_ptr(), _same_dev(ids, "ids", dev), _same_dev(dy, "dy", dev), T, K, H,
+                   *limit, _dev_ptr(d_w, "d_w", "f32", T * K, dev))
 
 
 @dataclass

@@ -696,12 +696,12 @@ constexpr int kSlotLoads = 8;
 typedef float f4v __attribute__((ext_vector_type(4)));
 __global__ __launch_bounds__(256) void k_slot_grad(const float* __restrict__ eout, const int32_t* __restrict__ ids,
                                                    const float* __restrict__ dy, int64_t slots, int K, int H,
-                                                   float* __restrict__ dw) {
+                                                   uint32_t id_end, float* __restrict__ dw) {
   const int lane = threadIdx.x & 63;
   const int64_t j = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (j >= slots) return;
   f4v v = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (ids[j] >= 0) {
+  if ((uint32_t)ids[j] < id_end) {
     const f4v* a = reinterpret_cast<const f4v*>(eout + (size_t)j * H);
     const f4v* b = reinterpret_cast<const f4v*>(dy + (size_t)(j / K) * H);
     const int n = H / 4;
@@ -848,10 +848,10 @@ hipError_t launch_moe_route_grad(const moe_route_config& c, const void* logits, 
   return hipGetLastError();
 }
 
-hipError_t launch_slot_grad(const float* eout, const int32_t* ids, const float* dy, int T, int K, int H, float* dw,
-                            hipStream_t st) {
+hipError_t launch_slot_grad(const float* eout, const int32_t* ids, const float* dy, int T, int K, int H, uint32_t id_end,
+                            float* dw, hipStream_t st) {
   const int64_t slots = (int64_t)T * K;
-  k_slot_grad<<<(unsigned)((slots + 3) / 4), 256, 0, st>>>(eout, ids, dy, slots, K, H, dw);
+  k_slot_grad<<<(unsigned)((slots + 3) / 4), 256, 0, st>>>(eout, ids, dy, slots, K, H, id_end, dw);
   return hipGetLastError();
 }
 

@@ -13,8 +13,9 @@ hipError_t launch_moe_route(const moe_route_config& c, const void* logits, int d
 hipError_t launch_moe_route_grad(const moe_route_config& c, const void* logits, int dtype, int64_t ld, int T,
                                  const uint8_t* valid, const int32_t* ids, const float* dw, const float* dimp, void* dz,
                                  int64_t ld_d, hipStream_t st);
-hipError_t launch_slot_grad(const float* eout, const int32_t* ids, const float* dy, int T, int K, int H, float* dw,
-                            hipStream_t st);
+// slots whose id, taken as unsigned, is not below id_end are dropped
+hipError_t launch_slot_grad(const float* eout, const int32_t* ids, const float* dy, int T, int K, int H, uint32_t id_end,
+                            float* dw, hipStream_t st);
 // product over weight codes with its epilogue
 size_t linear_ws_bytes(const moe_linear_config& c, int64_t T);
 hipError_t launch_linear(const moe_linear_config& c, const uint8_t* codes, const float* scales, const float* bias,

@@ -47,6 +47,14 @@ int check_linear(const moe_linear_config* c) {
   return MOE_OK;
 }
 
+int check_slot_grad(const float* e_out, const int32_t* ids, const float* dy, int32_t T, int32_t K, int32_t H,
+                    const float* d_w) {
+  if (!e_out || !ids || !dy || !d_w) return MOE_E_NULL;
+  if (!tokens_ok(T) || K < 1 || K > kMaxTopK || H < 4 || H % 4 != 0 || H > kMaxHidden) return MOE_E_SHAPE;
+  if (!aligned16(e_out) || !aligned16(dy) || !aligned(ids, 4) || !aligned(d_w, 4)) return MOE_E_ARG;
+  return MOE_OK;
+}
+
 int32_t done(hipError_t e) { return e == hipSuccess ? MOE_OK : hip_fail(e); }
 
 }  // namespace
@@ -90,10 +98,16 @@ int32_t moe_route_backward(const moe_route_config* cfg, const void* logits, int3
 
 int32_t moe_slot_weight_grad(const float* e_out, const int32_t* ids, const float* dy, int32_t T, int32_t K, int32_t H,
                              float* d_w, hipStream_t stream) {
-  if (!e_out || !ids || !dy || !d_w) return MOE_E_NULL;
-  if (!tokens_ok(T) || K < 1 || K > kMaxTopK || H < 4 || H % 4 != 0 || H > kMaxHidden) return MOE_E_SHAPE;
-  if (!aligned16(e_out) || !aligned16(dy) || !aligned(ids, 4) || !aligned(d_w, 4)) return MOE_E_ARG;
-  return done(launch_slot_grad(e_out, ids, dy, T, K, H, d_w, stream));
+  const int rc = check_slot_grad(e_out, ids, dy, T, K, H, d_w);
+  return rc ? rc : done(launch_slot_grad(e_out, ids, dy, T, K, H, 1u << 31, d_w, stream));  // every id >= 0 counts
+}
+
+int32_t moe_slot_weight_grad_experts(const float* e_out, const int32_t* ids, const float* dy, int32_t T, int32_t K,
+                                     int32_t H, int32_t n_experts, float* d_w, hipStream_t stream) {
+  const int rc = check_slot_grad(e_out, ids, dy, T, K, H, d_w);
+  if (rc) return rc;
+  if (n_experts < 1 || n_experts > kMaxExperts) return MOE_E_SHAPE;
+  return done(launch_slot_grad(e_out, ids, dy, T, K, H, (uint32_t)n_experts, d_w, stream));
 }
 
 size_t moe_linear_workspace_bytes(const moe_linear_config* cfg, int32_t max_tokens) {

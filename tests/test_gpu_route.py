@@ -276,6 +276,25 @@ def test_slot_weight_grad(T, K, H):
     assert np.all(got[:-1].reshape(T, K)[ids < 0] == 0)
 
 
+@pytest.mark.parametrize("T,K,H", [(1, 1, 4), (5, 8, 1000), (9, 3, 6144)])
+def test_slot_weight_grad_of_ids_beyond_the_experts(T, K, H):
+    """With the number of experts, ids from it on drop their slot as negative ones do; their rows hold NaN."""
+    rng = np.random.default_rng(H + T)
+    E = 16
+    e = rng.normal(0, 1, (T * K, H)).astype(np.float32)
+    dy = rng.normal(0, 1, (T, H)).astype(np.float32)
+    ids = rng.choice([0, 3, E - 1, E, E + 3, 2 ** 31 - 1, -1, -2 ** 31], (T, K)).astype(np.int32)
+    on = (ids >= 0) & (ids < E)
+    ref = np.einsum("tkh,th->tk", e.reshape(T, K, H).astype(np.float64), dy.astype(np.float64)) * on
+    mag = np.einsum("tkh,th->tk", np.abs(e.reshape(T, K, H)).astype(np.float64), np.abs(dy).astype(np.float64))
+    e[~on.ravel()] = np.nan
+    out = torch.full((T, K), 5.0, device=DEV)
+    moe.moe_slot_weight_grad(torch.from_numpy(e).to(DEV), torch.from_numpy(ids).to(DEV), torch.from_numpy(dy).to(DEV),
+                             out, n_experts=E)
+    got = out.cpu().numpy()
+    assert np.all(np.abs(got - ref) <= (H + 8) * 2.0 ** -24 * mag) and np.all(got[~on] == 0)
+
+
 # ------------------------------------------------------------------------------------------- with the layer
 
 _LAYER = {}
@@ -438,3 +457,32 @@ def test_route_streams_and_graph_replays():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got[:5], want[:5]))
+
+
+def test_dropped_slots_from_the_layer_to_the_logits():
+    """Slots dropped by -1, by the number of experts and by ids beyond it mean the same to the layer, to the gradient
+    of its weights and to the gradient of the logits, although the layer writes no expert output for any of them."""
+    sh = synth.TINY
+    cfg, layer = config_of(sh), _layer()
+    T, K, E, H = 6, sh.top_k, sh.n_experts, sh.hidden
+    rng = np.random.default_rng(9)
+    x = torch.from_numpy(synth.hidden_states(sh, T)).to(DEV)
+    kept = np.stack([rng.permutation(E)[:K] for _ in range(T)]).astype(np.int32)
+    drop = rng.random((T, K)) < 0.4
+    drop[2] = True
+    dy = torch.from_numpy(rng.normal(0, 1, (T, H)).astype(np.float32)).to(DEV)
+    w = torch.from_numpy(rng.uniform(0.1, 1, (T, K)).astype(np.float32)).to(DEV)
+    logits, _ = _logits(rng, T, E, "f32")
+    rc = _cfg(E, K)
+    results = []
+    for away in (-1, E, E + 3):
+        ids = torch.from_numpy(np.where(drop, away, kept).astype(np.int32)).to(DEV)
+        ws, y, e_out = _buffers(sh, T)
+        e_out.fill_(float("nan"))
+        moe.moe_layer_forward_routed(cfg, layer.weights(), x, ids, w, y, ws, moe.taps(e_out=e_out))
+        dw, dz = torch.empty((T, K), device=DEV), torch.empty((T, E), device=DEV)
+        moe.moe_slot_weight_grad(e_out, ids, dy, dw, n_experts=E)
+        moe.moe_route_backward(rc, logits, ids, dz, d_w=dw)
+        assert bool((dw[torch.from_numpy(drop).to(DEV)] == 0).all()) and bool(dz.isfinite().all())
+        results.append((y, dw, dz))
+    assert all(torch.equal(a, b) for r in results[1:] for a, b in zip(r, results[0]))

@@ -68,6 +68,14 @@ def test_slot_weight_grad_arguments_refused():
     assert f(P(4104), A, A, 1, 1, 4, A, None) == f(A, A, P(4104), 1, 1, 4, A, None) == L.MOE_E_ARG
 
 
+def test_slot_weight_grad_experts_arguments_refused():
+    f = L._lib.moe_slot_weight_grad_experts
+    assert f(None, A, A, 1, 1, 4, 8, A, None) == f(A, A, A, 1, 1, 4, 8, None, None) == L.MOE_E_NULL
+    for T, K, H, E in ((0, 1, 4, 8), (1, 33, 4, 8), (1, 1, 6, 8), (1, 1, 4, 0), (1, 1, 4, -1), (1, 1, 4, 1025)):
+        assert f(A, A, A, T, K, H, E, A, None) == L.MOE_E_SHAPE
+    assert f(P(4104), A, A, 1, 1, 4, 8, A, None) == f(A, P(4098), A, 1, 1, 4, 8, A, None) == L.MOE_E_ARG
+
+
 def _linear(cfg, codes=A, scales=A, bias=None, x=A, ldx=256, T=2, dtype=0, res=None, ldr=0, y=P(1 << 20), ldy=128, ws=WS,
             n=1 << 30):
     c = cfg.c()
