@@ -486,3 +486,25 @@ def test_dropped_slots_from_the_layer_to_the_logits():
         assert bool((dw[torch.from_numpy(drop).to(DEV)] == 0).all()) and bool(dz.isfinite().all())
         results.append((y, dw, dz))
     assert all(torch.equal(a, b) for r in results[1:] for a, b in zip(r, results[0]))
+
+
+@pytest.mark.parametrize("size", [1.0e4, 6.0e4])
+def test_route_groups_of_large_opposite_biases(size):
+    """Group sums whose two addends are large and of opposite sign: what a score loses by its addition to the bias is
+    of the size of the addends, not of the sum. One expert of each group has the bias +size, the others -size, and the
+    former's score lies within a few steps of a value where its sum with the bias falls between two floats, so that a
+    score off by one step moves the sum by a whole one (2^-10 at 1e4). The groups are the definition's."""
+    rng = np.random.default_rng(int(size))
+    G, n, T = 8, 4, 400
+    step = 2.0 ** (np.floor(np.log2(size)) - 23)
+    # scores (k + 1/2) step, which size + score cannot hold, in (0.3, 0.7)
+    s = (rng.integers(int(0.3 / step), int(0.7 / step), (T, 1)) + 0.5) * step
+    z = np.full((T, G, n), 0.25)
+    z[:, :, 0] = np.log(s / (1 - s)) + rng.integers(-3, 4, (T, G)) * 2.0 ** -24
+    z = z.reshape(T, G * n).astype(np.float32)
+    bias = np.full((G, n), -size)
+    bias[:, 0] = size
+    for K, KG in ((4, 2), (1, 1), (8, 5)):
+        kw = dict(G=G, KG=KG, scale=2.5)
+        _check(_cfg(G * n, K, **kw), torch.from_numpy(z).to(DEV), z.astype(np.float64), "f32", kw,
+               bias.ravel().astype(np.float32))
