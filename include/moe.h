@@ -343,8 +343,9 @@ int32_t moe_route(const moe_route_config* cfg, const void* logits, int32_t dtype
 /* Gradient of the logits: d_logits [T][E] (`dtype`, rows ld_d apart, may not overlap logits) from the gradients d_w
  * [T][K] of moe_route's weights and d_importance [E] of its importance sums, one of which may be NULL. logits,
  * valid and ids are those of the forward call; the choice itself has no gradient, and neither has the bias. Slots
- * with id outside [0, E) or a masked expert add nothing, and masked experts and padding get zeros. A token's ids
- * are distinct (moe_route's are). Errors as moe_route's. */
+ * with id outside [0, E) or a masked expert add nothing, and masked experts and padding get zeros; what d_w holds for
+ * such a slot, or d_importance for an expert in the tokens where it is masked, is not used (it may be infinite or NaN).
+ * A token's ids are distinct (moe_route's are). Errors as moe_route's. */
 int32_t moe_route_backward(const moe_route_config* cfg, const void* logits, int32_t dtype, int64_t ld, int32_t T,
                            const uint8_t* valid, const int32_t* ids, const float* d_w, const float* d_importance,
                            void* d_logits, int64_t ld_d, hipStream_t stream);

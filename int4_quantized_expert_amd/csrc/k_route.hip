@@ -647,11 +647,23 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_grad(RouteGradArgs a) {
         for (int i = 0; i < NE; ++i) out[i] = add[lane * NE + i];
         __builtin_amdgcn_wave_barrier();
       }
+      // A masked expert's entry of dimp may be infinite or NaN (its importance is 0 where a loss may take a logarithm);
+      // the token does not depend on it. Seen in dot, which is then taken again without them: 15.7 us for 32,768 x 256
+      // softmax, 16.5 with the masked ones left out always.
+      bool odd = false;
       if (SOFTMAX && dense) {
-        float dot = a.renorm ? 0.0f : dk;
+        const float own = a.renorm ? 0.0f : dk;
+        float dot = own;
 #pragma unroll
         for (int i = 0; i < NE; ++i) dot = fmaf(p[i], dimp[i], dot);
         dot = wave_sum(dot);
+        odd = !(fabsf(dot) < INFINITY);
+        if (odd) {
+          dot = own;
+#pragma unroll
+          for (int i = 0; i < NE; ++i) dot = live >> i & 1 ? fmaf(p[i], dimp[i], dot) : dot;
+          dot = wave_sum(dot);
+        }
 #pragma unroll
         for (int i = 0; i < NE; ++i) out[i] += p[i] * (dimp[i] - dot);
       } else if (dense) {
@@ -669,10 +681,21 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_grad(RouteGradArgs a) {
           dot = fmaf(p[i], dimp[i], dot);
         }
         rs = safe_rcp(wave_sum(sum));
-        dot = wave_sum(dot) * rs;
+        dot = wave_sum(dot);
+        odd = !(fabsf(dot) < INFINITY);
+        if (odd) {
+          dot = 0.0f;
+#pragma unroll
+          for (int i = 0; i < NE; ++i) dot = live >> i & 1 ? fmaf(p[i], dimp[i], dot) : dot;
+          dot = wave_sum(dot);
+        }
+        dot *= rs;
 #pragma unroll
         for (int i = 0; i < NE; ++i) out[i] += p[i] * rs * (dimp[i] - dot) * miss[i];
       }
+      if (odd)
+#pragma unroll
+        for (int i = 0; i < NE; ++i) out[i] = live >> i & 1 ? out[i] : 0.0f;
     }
     TZ* drow = static_cast<TZ*>(a.dz) + (size_t)t * a.ld_d;
     const int e0 = lane * NE;

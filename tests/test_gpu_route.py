@@ -508,3 +508,33 @@ def test_route_groups_of_large_opposite_biases(size):
         kw = dict(G=G, KG=KG, scale=2.5)
         _check(_cfg(G * n, K, **kw), torch.from_numpy(z).to(DEV), z.astype(np.float64), "f32", kw,
                bias.ravel().astype(np.float32))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("E", [24, 256])
+def test_route_backward_with_infinite_gradients_of_masked_experts(E, softmax, dtype):
+    """An expert that is masked in every token has importance 0, where the logarithm of a balance loss has an infinite
+    gradient: the tokens do not depend on it, and their gradients are those without it."""
+    rng = np.random.default_rng(E)
+    T, K = 5, 4
+    z, _ = _logits(rng, T, E, dtype)
+    z[:, 2], z[:, 9], z[:, E - 1] = float("-inf"), float("nan"), R.LOWEST[dtype]
+    z[3, :4] = float("-inf")  # one token with more of them masked
+    z[4, :] = float("-inf")  # and one without live experts
+    z[1, :] -= 60.0  # scores so low that the sum is taken relative to the largest
+    z64 = z.double().cpu().numpy()
+    ids = np.stack([rng.permutation(E)[:K] for _ in range(T)]).astype(np.int32)
+    dw, dimp = rng.normal(0, 1, (T, K)).astype(np.float32), rng.normal(0, 1, E).astype(np.float32)
+    dimp[[2, 9, E - 1]] = 0.0
+    bad = dimp.copy()
+    bad[[2, 9, E - 1]] = np.inf, np.nan, -np.inf
+    for renorm in (False, True):
+        cfg = _cfg(E, K, softmax=softmax, renorm=renorm, scale=2.5)
+        ref, size = R.route_grad(z64, dtype, ids, dw, dimp, softmax, renorm, 2.5)
+        d = torch.full((T, E), 7.0, dtype=DT[dtype], device=DEV)
+        moe.moe_route_backward(cfg, z, torch.from_numpy(ids).to(DEV), d, d_w=torch.from_numpy(dw).to(DEV),
+                               d_importance=torch.from_numpy(bad).to(DEV))
+        tiny = {"f32": 1e-30, "bf16": 1e-30, "f16": 2.0 ** -25}[dtype]
+        tol = R.HALF_STEP[dtype] * (1 + 64 * U) * np.abs(ref) + 64 * U * size + tiny
+        assert np.all(np.abs(d.double().cpu().numpy() - ref) <= tol)
