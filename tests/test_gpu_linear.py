@@ -349,3 +349,92 @@ def test_sums_beyond_fp32_before_their_scales(T, N, bits, group, dtype, size, sc
     y = _call(moe.LinearConfig(N, K, bits, group), codes, scales, x.to(DEV), N)
     ref, err = R.linear(q, s, x.double().numpy())
     assert np.all(np.abs(y.double().cpu().numpy() - ref) <= err + R.HALF_STEP[dtype] * (np.abs(ref) + err))
+
+
+def _device_weights(seed, N, K, bits, group):
+    """_weights(whole=True) made on the device, for large matrices: codes, scales and W in 64 bits."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    lim = 8 if bits == 4 else 128
+    q = torch.randint(-lim, lim, (N, K), generator=g, device=DEV, dtype=torch.int8)
+    G = group or K
+    s = torch.exp2(torch.randint(-1, 2, (N, K // G), generator=g, device=DEV).float())
+    if bits == 4:
+        u = (q & 15).view(torch.uint8)
+        row = (u[:, 0::2] | (u[:, 1::2] << 4)).contiguous()
+    else:
+        row = q
+    codes = torch.empty(row.numel(), dtype=torch.uint8, device=DEV)
+    (moe.moe_tile_int4 if bits == 4 else moe.moe_tile_int8)(row, codes)
+    scales = s.view(-1)
+    if group:
+        scales = torch.empty_like(scales)
+        moe.moe_tile_group_scales(s, scales)
+    return codes, scales, (q.double().view(N, K // G, G) * s.double()[:, :, None]).view(N, K)
+
+
+# For 1 to 4 tokens: 6 to 32 blocks of four a wavefront, in whole and in ragged numbers, heads in turns among them; for
+# 5 to 32: 7 to 16 a workgroup, with a short last part, 128 KB of fp32 activations (6,656 rows x 8,320), and 65 and more
+# parts to add (64 rows). Columns that are no multiple of a group are rounded up to one.
+FEW_LONG = [(1, 192, 6144), (1, 64, 8320), (1, 64, 16384), (1, 24640, 4704), (3, 128, 6144), (4, 64, 8160), (2, 24704, 5216),
+            (5, 4096, 6144), (8, 6656, 8320), (16, 6144, 6240), (17, 4096, 6144), (24, 6656, 8320), (32, 6144, 6144),
+            (32, 64, 8320), (9, 64, 6176), (64, 6144, 2080)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("bits,group", [(4, 0), (8, 0), (4, 32), (4, 64), (4, 128)])
+@pytest.mark.parametrize("T,N,K", FEW_LONG)
+def test_few_tokens_over_long_rows_are_exact(T, N, K, bits, group, dtype):
+    """Whole numbers again, over rows so long that every code in flight is replaced by later ones, and every round in
+    which activations are converted is used. A row's sums are multiples of its smallest scale, and the sum of their
+    absolute products stays below 2^24 of those, so every partial sum is exact in any order."""
+    K = (K + group - 1) // group * group if group else K
+    codes, scales, wt = _device_weights(T + N + K, N, K, bits, group)
+    x, x64 = _x(np.random.default_rng(K), T, K, dtype, whole=True)
+    xd = torch.from_numpy(x64).to(DEV)
+    least = scales.view(N // 64, -1, 64).amin(1).view(N) if group else scales
+    assert bool((torch.mm(xd.abs(), wt.abs().t().contiguous()) < 2 ** 24 * least.double()).all())
+    b = torch.arange(N, device=DEV).float() % 129 - 64
+    res = torch.arange(T * N, device=DEV).view(T, N).remainder(17).to(DT[dtype])
+    y = _call(moe.LinearConfig(N, K, bits, group), codes, scales, x, N, b, res)
+    want = torch.mm(xd, wt.t().contiguous()) + b.double() + res.double()
+    assert torch.equal(y, want.float().to(DT[dtype]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("bits,group", [(4, 0), (8, 0), (4, 32), (4, 64), (4, 128)])
+@pytest.mark.parametrize("T,N,K", [(1, 512, 6144), (3, 256, 8192), (1, 49280, 2208), (7, 4096, 6144), (30, 8192, 6240)])
+def test_swiglu_of_few_tokens_over_long_rows(T, N, K, bits, group, dtype):
+    """The same with SwiGLU, whole numbers times 2^-14: the sums are exact multiples of 2^-15, so only the epilogue
+    rounds. Its error relative to the value, counted in 2^-24: the exponential 3 and its argument's part beyond fp32 1,
+    1 + e 1, the reciprocal 2, three products 3, the residual's addition 1 of the larger of the two. fp16 below its
+    normal range: half of its smallest step, 2^-25."""
+    K = (K + group - 1) // group * group if group else K
+    codes, scales, wt = _device_weights(T + N + K, N, K, bits, group)
+    scales *= 2.0 ** -14
+    x, x64 = _x(np.random.default_rng(K), T, K, dtype, whole=True)
+    v = torch.mm(torch.from_numpy(x64).to(DEV), wt.t().contiguous()) * 2.0 ** -14
+    res = torch.arange(T * (N // 2), device=DEV).view(T, N // 2).remainder(17).to(DT[dtype])
+    y = _call(moe.LinearConfig(N, K, bits, group, ACT["swiglu"]), codes, scales, x, N // 2, None, res)
+    gate, up = v[:, :N // 2], v[:, N // 2:]
+    a = gate / (1 + torch.exp(-gate)) * up
+    want = a + res.double()
+    err = 2.0 ** -24 * (10 * a.abs() + torch.maximum(want.abs(), a.abs())) + (2.0 ** -25 if dtype == "f16" else 0.0)
+    assert bool(((y.double() - want).abs() <= err + R.HALF_STEP[dtype] * (want.abs() + err)).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,N,K,act", [(1 << 20, 64, 32, "none"), (6100, 64, 160, "none"), (1, 1 << 20, 32, "none"),
+                                       (20, 1 << 20, 32, "none"), (40, 1 << 20, 64, "relu"), (1, 64, 65536, "none"),
+                                       (4, 64, 65536, "none"), (24, 128, 65536, "none"), (70, 64, 65536, "none"),
+                                       (70, 6144, 65536, "relu")])
+def test_largest_sizes_are_exact(T, N, K, act, dtype):
+    """The most tokens, rows and columns that the operator takes, whole numbers; the sums as in the test of long rows."""
+    codes, scales, wt = _device_weights(T + N + K, N, K, 4, 0)
+    x = torch.randint(-2, 3, (T, K), device=DEV, generator=torch.Generator(device=DEV).manual_seed(T)).to(DT[dtype])
+    assert 2 * 8 * K < 2 ** 24
+    y = _call(moe.LinearConfig(N, K, 4, 0, ACT[act]), codes, scales, x, N)
+    for t0 in range(0, T, 1 << 16):
+        want = torch.mm(x[t0:t0 + (1 << 16)].double(), wt.t().contiguous())
+        want = want.clamp(min=0) if act == "relu" else want
+        assert torch.equal(y[t0:t0 + (1 << 16)], want.float().to(DT[dtype]))

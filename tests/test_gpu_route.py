@@ -538,3 +538,78 @@ def test_route_backward_with_infinite_gradients_of_masked_experts(E, softmax, dt
         tiny = {"f32": 1e-30, "bf16": 1e-30, "f16": 2.0 ** -25}[dtype]
         tol = R.HALF_STEP[dtype] * (1 + 64 * U) * np.abs(ref) + 64 * U * size + tiny
         assert np.all(np.abs(d.double().cpu().numpy() - ref) <= tol)
+
+
+@pytest.mark.parametrize("weight_bits,group_size", [(8, 0), (4, 32), (4, 64)])
+@pytest.mark.parametrize("T", [1, 3, 40, 300])
+def test_routed_layer_equals_the_layer_in_other_formats(T, weight_bits, group_size):
+    """int8 experts and int4 ones with group scales: the routed layer's output is the layer's, bit for bit."""
+    sh = synth.TINY
+    key = (weight_bits, group_size)
+    if key not in _LAYER:
+        _LAYER[key] = GpuLayer(sh, weight_bits=weight_bits, group_size=group_size)
+    layer, cfg = _LAYER[key], config_of(sh, 0, weight_bits, group_size)
+    x = torch.from_numpy(synth.hidden_states(sh, T)).to(DEV)
+    ws = torch.empty(moe.moe_workspace_bytes(cfg, T), dtype=torch.uint8, device=DEV)
+    y, y2 = torch.empty((T, sh.hidden), device=DEV), torch.empty((T, sh.hidden), device=DEV)
+    ids = torch.empty((T, sh.top_k), dtype=torch.int32, device=DEV)
+    w = torch.empty((T, sh.top_k), device=DEV)
+    moe.moe_layer_forward(cfg, layer.weights(), x, y, ws, moe.taps(topk_ids=ids, topk_w=w))
+    ws.fill_(0xA5)
+    moe.moe_layer_forward_routed(cfg, layer.weights(), x, ids, w, y2, ws)
+    assert torch.equal(y, y2)
+
+
+@pytest.mark.parametrize("T", [1, 4, 32, 192, 700])
+def test_routed_layer_equals_the_layer_at_full_size(T):
+    """The same with hidden 6144, 256 experts of 2048 and top 8; and under moe_route's own routing of the logits, with
+    a third of the tokens masked, whose rows are the shared expert's output alone."""
+    sh = synth.GLM
+    if "glm" not in _LAYER:
+        _LAYER["glm"] = GpuLayer(sh)
+    layer, cfg = _LAYER["glm"], config_of(sh)
+    E, K, H = sh.n_experts, sh.top_k, sh.hidden
+    x = torch.from_numpy(synth.hidden_states(sh, T)).to(DEV)
+    ws = torch.empty(moe.moe_workspace_bytes(cfg, T), dtype=torch.uint8, device=DEV)
+    y, y2 = torch.empty((T, H), device=DEV), torch.empty((T, H), device=DEV)
+    ids, w = torch.empty((T, K), dtype=torch.int32, device=DEV), torch.empty((T, K), device=DEV)
+    moe.moe_layer_forward(cfg, layer.weights(), x, y, ws, moe.taps(topk_ids=ids, topk_w=w))
+    moe.moe_layer_forward_routed(cfg, layer.weights(), x, ids, w, y2, ws)
+    assert torch.equal(y, y2)
+    rc = _cfg(E, K, sh.n_group, sh.topk_group, scale=sh.rsf)
+    valid = (torch.arange(T, device=DEV) % 3 != 1).to(torch.uint8)
+    ids2, w2 = torch.empty_like(ids), torch.empty_like(w)
+    moe.moe_route(rc, (x @ layer.router_w.t()).contiguous(), ids2, w2, bias=layer.bias, valid=valid)
+    e_out = torch.empty((T * K + sh.n_shared * T, H), device=DEV)
+    moe.moe_layer_forward_routed(cfg, layer.weights(), x, ids2, w2, y2, ws, moe.taps(e_out=e_out))
+    assert torch.equal(y2[valid == 0], e_out[T * K:T * K + T][valid == 0])
+    if T == 700:
+        del _LAYER["glm"]
+
+
+@pytest.mark.parametrize("softmax", [False, True])
+def test_route_largest_batch(softmax):
+    """2^20 tokens, the most that the operators take: tokens at both ends and between as they come out alone, counts
+    and sums over all; the gradient and the slots' gradient of the same batch."""
+    T, E, K = 1 << 20, 8, 2
+    g = torch.Generator(device=DEV).manual_seed(3)
+    z = torch.randn((T, E), device=DEV, generator=g)
+    cfg = _cfg(E, K, softmax=softmax)
+    ids, w, load, imp = _run(cfg, z, K)
+    assert np.array_equal(load.cpu().numpy(), np.bincount(ids.ravel(), minlength=E))
+    assert abs(float(imp.double().sum()) - T) < T * 64 * U
+    idd, dw, dimp = torch.from_numpy(ids).to(DEV), torch.randn((T, K), device=DEV, generator=g), torch.randn(E, device=DEV)
+    dz = torch.empty_like(z)
+    moe.moe_route_backward(cfg, z, idd, dz, d_w=dw, d_importance=dimp)
+    for t in (0, 1, 65535, 524288, T - 1):
+        i1, w1, _, _ = _run(cfg, z[t:t + 1], K, stats=False)
+        assert np.array_equal(i1[0], ids[t]) and np.array_equal(w1[0], w[t])
+        d1 = torch.empty((1, E), device=DEV)
+        moe.moe_route_backward(cfg, z[t:t + 1], idd[t:t + 1].contiguous(), d1, d_w=dw[t:t + 1].contiguous(), d_importance=dimp)
+        assert torch.equal(d1[0], dz[t])
+    e_out, dy = torch.randn((T * K, E), device=DEV, generator=g), z
+    got = torch.empty((T, K), device=DEV)
+    moe.moe_slot_weight_grad(e_out, idd, dy, got)
+    ref = (e_out.view(T, K, E).double() * dy.double()[:, None, :]).sum(2)
+    mag = (e_out.view(T, K, E).double() * dy.double()[:, None, :]).abs().sum(2)
+    assert bool(((got.double() - ref).abs() <= (E + 8) * 2.0 ** -24 * mag).all())

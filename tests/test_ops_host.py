@@ -193,3 +193,22 @@ def test_configs_keep_their_struct_until_a_field_changes():
             assert other == cfg and getattr(other.ref()._obj, field) == getattr(cfg, field)
         setattr(cfg, field, 2)
         assert getattr(cfg.ref()._obj, field) == 2 and getattr(a._obj, field) != 2
+
+
+@pytest.mark.parametrize("rows,cols,act", [(64, 32, 0), (64, 65536, 0), (192, 6144, 5), (2048, 2048, 0), (6144, 6144, 5),
+                                           (12352, 8320, 0), (131072, 6144, 0), (1 << 20, 32, 0)])
+def test_a_workspace_serves_every_smaller_batch(rows, cols, act):
+    """A workspace sized for the largest batch is large enough for any other: its size never falls with the tokens."""
+    cfg = moe.LinearConfig(rows, cols, act=act)
+    last = 0
+    for T in (*range(1, 70), *range(70, 7000, 31), 1 << 14, 1 << 17, 1 << 20):
+        need = moe.moe_linear_workspace_bytes(cfg, T)
+        assert need >= last
+        last = need
+    assert last >= (1 << 20) * cols * 2
+    for E in (1, 64, 100, 256, 512, 1024):
+        route, last = moe.RouteConfig(E, 1), 0
+        for T in (*range(1, 200), *range(200, 9000, 61), 1 << 20):
+            need = moe.moe_route_workspace_bytes(route, T)
+            assert need >= last
+            last = need
