@@ -295,8 +295,9 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, int t, int col, int
 // rows and the 32 up rows that go with them) with v_mfma_f32_32x32x16_f16; RW wavefronts of a workgroup take the same
 // tokens. A code fragment costs 10 vector instructions to unpack and serves TT matrix instructions of 8 passes: with
 // TT = 4 the unpacking fits between them, with TT = 1 it takes the longer time. 2,048 tokens 12288 x 6144 with SwiGLU:
-// 178 us for the 512 whole tiles and 98 for the rest, 1.16 PFLOP/s and 1.05, matrix instructions busy for 61% and 53%;
-// 191 tokens 6144 x 2048 int8 at TT = 1: 18 us. fp32 at TT = 1, 1,001 tokens 6144 x 4096: 107 us, 0.94 PFLOP/s of halves.
+// 181 us for the 512 whole tiles and 99 for the rest, 1.14 PFLOP/s and 1.04, matrix instructions busy for 61% and 52%;
+// 191 tokens 6144 x 2048 int8 at TT = 1: 20.5 us, 18%. fp32 at TT = 1, 1,001 tokens 6144 x 4096: 119 us in the median,
+// 108 at best, 0.85 to 0.94 PFLOP/s of halves, 51%.
 // The activations of a step (two blocks of columns) pass through LDS in two buffers: the next step's are loaded to
 // registers while this one is multiplied. Each wavefront reads its own codes from memory into registers, also a step
 // ahead.
@@ -712,8 +713,10 @@ __device__ __forceinline__ void wave_sync() {
 // Up to 4 tokens (TOK 1 or 4): a workgroup finishes 16 rows (with SwiGLU 16 gate and 16 up rows) in one launch. Its
 // wavefronts share the columns; each converts its own columns of the tokens, with a power of two of its own, and waits
 // for no other before the sum. Bound by the latency of one pass over the codes: 1 token, 6144 x 6144 int4, 8.4 us on
-// codes that come from HBM (19 MB: 3.6 to 4.0 by a plain read), 10.4 in the form below; 4 tokens 10.1 and 11.2; 4096 x
-// 2048 4.5 and 7.6.
+// codes that come from HBM (19 MB: 3.6 to 4.0 by a plain read), 10.4 in the form below; 4 tokens 9.9 and 11.2; 4096 x
+// 2048 4.5 and 7.6. int8 6144 x 6144 12.4, SwiGLU 12288 x 6144 11.8. Of the 128 registers of four wavefronts a SIMD some
+// forms spill: with SwiGLU int8 (fp32, fp16) and fp16 in groups of 32, 12 to 30; fp16 in groups of 64 with SwiGLU, bf16
+// int8 and fp16 heads in groups of 32, 2 to 8.
 // TURNS: rows for more than three times the workgroups that run at a time, a head's: a workgroup converts once and takes
 // its share of the rows in turns, the next rows' codes on their way while it finishes some. 32768 x 6144, 1 token: 24.0
 // us, 27.4 without; 65536 x 4096 g64, 3 tokens: 40.3 and 48.3; three turns (16448 rows) 18.0 and 16.9, two of SwiGLU (24576
@@ -866,8 +869,10 @@ __global__ __launch_bounds__(64 * kTinyWaves, 4) void k_linear_tiny(LinearArgs a
 
 // More: a workgroup takes 128 rows (64 gate and 64 up) by 16*NT tokens over a part of the columns, because every
 // workgroup reads and converts the activations of its columns; four wavefronts of 32 rows for each half of them. Parts
-// are added by k_linear_join. 32 tokens, 4096 x 6144 int4 g64 with SwiGLU: 10.9 us and 2.3 to add, on 15 MB; latency: the
-// conversion, then three quads of codes a wavefront, then the sum.
+// are added by k_linear_join. 32 tokens, 4096 x 6144 int4 g64 with SwiGLU: 11.1 us and 2.5 to 3.9 to add, on 15 MB;
+// latency: the conversion, then three quads of codes a wavefront, then the sum. A head, 65536 x 6144 int4: 55.8 us for 8
+// tokens, 96.6 for 32, on 205 MB: its columns are cut by what the lanes convert, into 3 and 6 parts whose sums are written
+// and read.
 constexpr int kSlimRowWaves = 4, kSlimColWaves = 2, kSlimLanes = 64 * kSlimRowWaves * kSlimColWaves;
 constexpr int kSlimRounds = 8;  // granules that a lane converts, over all token fragments
 
@@ -1038,7 +1043,8 @@ size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // Where the codes' way through memory, and having enough workgroups, counts more than the products: up to 32 tokens, and
 // up to kSlimWork tokens times rows, at which the tiles below take as long (64 tokens x 6144 rows: 16 us over 2048
-// columns either way, 32 and 29 over 6144; 192 x 2048: 16 either way, 30 and 30).
+// columns either way, 32 and 29 over 6144; 192 x 2048: 16 either way, 30 and 30; 32 tokens x 65536 rows over 6144: 97
+// here, 33 tokens in tiles 97).
 constexpr int kSlimTokens = 32;
 constexpr int64_t kSlimWork = 3 << 17;
 constexpr int kTinyTokens = 4;

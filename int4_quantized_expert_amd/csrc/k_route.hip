@@ -159,8 +159,8 @@ __device__ __forceinline__ void merge_top2_dpp(int& a, int& b) {
 // group lie within thr + 1e-6 of the sum of their addends' magnitudes: adding a score to its bias loses up to 2^-24 of
 // either's result, which the sum of two opposite ones need not show. A difference that is no number is near, too.
 // glog >= 0: a group is 2^glog whole lanes, its two largest are merged across them in registers; else its run is
-// scanned in LDS by one lane. 32,768 tokens x 256 experts in 8 groups: 33.9 us with the merge, 43.2 with the scan; one
-// token 3.8 and 5.1.
+// scanned in LDS by one lane. 32,768 tokens x 256 experts in 8 groups: 35.4 us with the merge, 44.5 with the scan; one
+// token 4.2 and 5.5.
 template <int NE>
 __device__ __forceinline__ uint32_t keep_groups(const int (&g)[NE], int E, int G, int KG, int glog, bool gmax, int lane,
                                                 int* s_row, float thr, bool* near) {
@@ -318,8 +318,10 @@ constexpr int resident_waves(int ne) { return ne <= 4 ? 6 : ne == 8 ? 4 : 2; }
 // same experts. Taking 256 exponentials a token in 64 bits would be most of the work; so the choice is made with 32-bit
 // scores, and a token where two neighbours in the order (or two groups) lie closer than twice the error of those (see
 // thr) is set aside and done once more with the definition's: 2 tokens in 1,000 of 256 biased sigmoid scores.
-// Bound by instruction issue, not by its bytes: 330 vector and 270 scalar instructions a token of 256 experts in 8
-// groups with bias and statistics, 33.9 us for 32,768 of them (36 MB); one token 3.8 us, 192 softmax ones of 128 5.0.
+// Bound by instruction issue, not by its bytes: 340 vector and 270 scalar instructions a token of 256 experts in 8
+// groups with bias and statistics, the former 73% of the SIMDs' cycles, 35.8 us for 32,768 of them (36 MB); one token
+// 3.9 us, 192 softmax ones of 128 5.0. The six wavefronts a SIMD of 129 to 256 experts cost 2 to 6 spilled vector
+// registers with softmax or statistics.
 template <int NE, class TZ, bool SOFTMAX, bool STATS, int WV>
 __global__ __launch_bounds__(64 * WV, resident_waves(NE)) void k_route(RouteArgs a) {
   __shared__ __align__(8) int s_row[WV][64 * NE];  // a wavefront's scratch
@@ -541,8 +543,9 @@ __global__ __launch_bounds__(1024) void k_route_stats(const int32_t* __restrict_
 // u = scale * dw and m = 1 for softmax scores (their sum cancels), 1 - s for sigmoid ones; without, dz_k = s_k (1 - s_k)
 // u_k, or p_e (u_e - sum_j p_j u_j) over all experts. Importance p = s / (sum of s): p_e (g_e - sum_f p_f g_f) m_e.
 // One wavefront a token; a slot's part goes through LDS to the lane that holds its expert, and a row is read and written
-// once. 32,768 x 256 sigmoid with importance: 18.4 us for 69 MB (10.8 at 6.4 TB/s), bound by instruction issue, 186
-// vector instructions a token; 381 x 128 softmax 3.1 us.
+// once. 32,768 x 256 sigmoid with importance: 18.8 us for 69 MB (10.8 at 6.4 TB/s), bound by instruction issue: 187
+// vector instructions a token, 80% of the SIMDs' cycles; 10.5 us without importance, softmax with it 15.7; 381 x 128
+// softmax 3.2.
 struct RouteGradArgs {
   const void* logits;
   int64_t ld, ld_d;
@@ -715,7 +718,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_grad(RouteGradArgs a) {
 // ------------------------------------------------------------ gradient of the routing weights
 // dw[t][k] = sum_h dy[t][h] e_out[t*K + k][h]. Reads every slot's row once: HBM-bound. One wavefront takes one slot,
 // eight 16-byte loads of its row in flight (not kept in the caches); the K slots of a token sit next to each other, so
-// dy comes from the caches after the first. 2,048 x 8 x 6144: 70.4 us, 6.4 TB/s (80.4 with one load in flight).
+// dy comes from the caches after the first. 2,048 x 8 x 6144: 70.6 us, 6.4 TB/s (80.4 with one load in flight).
 constexpr int kSlotLoads = 8;
 typedef float f4v __attribute__((ext_vector_type(4)));
 __global__ __launch_bounds__(256) void k_slot_grad(const float* __restrict__ eout, const int32_t* __restrict__ ids,
@@ -763,7 +766,8 @@ constexpr int kWideWaves = 8;
 static int elems_per_lane(int E) { return E <= 64 ? 1 : E <= 128 ? 2 : E <= 256 ? 4 : E <= 512 ? 8 : 16; }
 
 // Workgroups of `waves` wavefronts for T tokens, at most `per_simd` wavefronts on each SIMD: as many as fit at a time,
-// so that all end together. 32,768 tokens x 256 experts with statistics: 34.1 us, 38.0 with 8 wavefronts, of which 6 fit.
+// so that all end together. 32,768 tokens x 256 experts, with their statistics added up: 43.7 us, 45.4 with 8 wavefronts a
+// SIMD, of which 6 fit.
 static int route_blocks(int T, int waves, int per_simd) {
   const int need = (T + waves - 1) / waves, most = kSimds * per_simd / waves;
   return need < most ? need : most;
