@@ -438,3 +438,17 @@ def test_largest_sizes_are_exact(T, N, K, act, dtype):
         want = torch.mm(x[t0:t0 + (1 << 16)].double(), wt.t().contiguous())
         want = want.clamp(min=0) if act == "relu" else want
         assert torch.equal(y[t0:t0 + (1 << 16)], want.float().to(DT[dtype]))
+
+
+@pytest.mark.parametrize("bits,group", [(4, 0), (8, 0), (4, 32)])
+@pytest.mark.parametrize("T,N", [(1, 128), (4, 128), (20, 128), (70, 128), (300, 8192)])
+def test_activations_below_the_normal_range_of_fp16(T, N, bits, group):
+    """fp16 activations that are all whole multiples of its smallest step 2^-24, up to 2^-18: none is lost. The sums are
+    exact (whole numbers times 2^-25), and scales of 2^12 to 2^14 bring the results back into fp16's range."""
+    rng = np.random.default_rng(T + N)
+    K = 256
+    q, s, codes, scales = _weights(rng, N, K, bits, group, whole=True)
+    v = torch.from_numpy(rng.integers(-64, 65, (T, K)) * 2.0 ** -24).to(torch.float16)
+    y = _call(moe.LinearConfig(N, K, bits, group), codes, scales * 2.0 ** 13, v.to(DEV), N)
+    want = v.double().numpy() @ (q * np.repeat(s, K // s.shape[1], axis=1)).T * 2.0 ** 13
+    assert torch.equal(y.cpu(), torch.from_numpy(want.astype(np.float32)).to(torch.float16))

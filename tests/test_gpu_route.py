@@ -613,3 +613,70 @@ def test_route_largest_batch(softmax):
     ref = (e_out.view(T, K, E).double() * dy.double()[:, None, :]).sum(2)
     mag = (e_out.view(T, K, E).double() * dy.double()[:, None, :]).abs().sum(2)
     assert bool(((got.double() - ref).abs() <= (E + 8) * 2.0 ** -24 * mag).all())
+
+
+@pytest.mark.parametrize("T", [1, 7, 200])
+def test_router_tuning_step_captured(T):
+    """Route, layer, both gradients, on a captured stream: every replay, with other inputs and eager work between the
+    replays, equals the eager chain. Weights of dropped slots are NaN for the layer, which does not use them."""
+    sh = synth.TINY
+    cfg, layer = config_of(sh), _layer()
+    K, E, H = sh.top_k, sh.n_experts, sh.hidden
+    rc = _cfg(E, K, sh.n_group, sh.topk_group, scale=2.5)
+    valid = (torch.arange(T, device=DEV) % 5 != 3).to(torch.uint8)
+    target = torch.randn((T, H), device=DEV)
+    rws = [torch.empty(moe.moe_route_workspace_bytes(rc, T), dtype=torch.uint8, device=DEV) for _ in range(2)]
+
+    def bufs():
+        ws, y, e_out = _buffers(sh, T)
+        return dict(ws=ws, y=y, e_out=e_out, ids=torch.empty((T, K), dtype=torch.int32, device=DEV),
+                    w=torch.empty((T, K), device=DEV), load=torch.empty(E, dtype=torch.int32, device=DEV),
+                    imp=torch.empty(E, device=DEV), dw=torch.empty((T, K), device=DEV), dz=torch.empty((T, E), device=DEV),
+                    dy=torch.empty((T, H), device=DEV))
+
+    def step(x, z, b, rw):
+        moe.moe_route(rc, z, b["ids"], b["w"], bias=layer.bias, valid=valid, load=b["load"], importance=b["imp"], ws=rw)
+        b["w"].masked_fill_(b["ids"] < 0, float("nan"))
+        moe.moe_layer_forward_routed(cfg, layer.weights(), x, b["ids"], b["w"], b["y"], b["ws"], moe.taps(e_out=b["e_out"]))
+        torch.sub(b["y"], target, out=b["dy"])
+        moe.moe_slot_weight_grad(b["e_out"], b["ids"], b["dy"], b["dw"], n_experts=E)
+        moe.moe_route_backward(rc, z, b["ids"], b["dz"], d_w=b["dw"], d_importance=b["imp"], valid=valid)
+
+    xs = [torch.from_numpy(synth.hidden_states(sh, T, step=i)).to(DEV) for i in range(4)]
+    zs = [(x @ layer.router_w.t()).contiguous() for x in xs]
+    x, z, got, want = xs[0].clone(), zs[0].clone(), bufs(), bufs()
+    step(x, z, got, rws[0])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(x, z, got, rws[0])
+    for xx, zz in zip(xs, zs):
+        x.copy_(xx)
+        z.copy_(zz)
+        step(xx, zz, want, rws[1])
+        g.replay()
+        torch.cuda.synchronize()
+        assert bool(want["y"].isfinite().all()) and bool(want["dz"].isfinite().all())
+        for k in ("ids", "load", "imp", "y", "dw", "dz"):
+            assert torch.equal(got[k], want[k]), k
+        assert torch.equal(got["w"][got["ids"] >= 0], want["w"][want["ids"] >= 0])
+
+
+@pytest.mark.parametrize("T", [3, 2500])
+def test_route_load_or_importance_alone(T):
+    """Each of the two sums without the other, with the same bits as together; and without live experts or tokens."""
+    rng = np.random.default_rng(T)
+    E, K = 96, 6
+    z, _ = _logits(rng, T, E, "bf16")
+    cfg = _cfg(E, K, 6, 2)
+    ids, w, load, imp = _run(cfg, z, K)
+    ws = torch.empty(moe.moe_route_workspace_bytes(cfg, T), dtype=torch.uint8, device=DEV)
+    i2, w2 = torch.empty((T, K), dtype=torch.int32, device=DEV), torch.empty((T, K), device=DEV)
+    l2, m2 = torch.full_like(load, -1), torch.full_like(imp, -1.0)
+    moe.moe_route(cfg, z, i2, w2, load=l2, ws=ws)
+    moe.moe_route(cfg, z, i2, w2, importance=m2, ws=ws)
+    assert torch.equal(l2, load) and torch.equal(m2, imp) and np.array_equal(i2.cpu().numpy(), ids)
+    moe.moe_route(cfg, z, i2, w2, valid=torch.zeros(T, dtype=torch.uint8, device=DEV), load=l2, importance=m2, ws=ws)
+    assert bool((i2 == -1).all()) and not bool(w2.any()) and not bool(l2.any()) and not bool(m2.any())
+    moe.moe_route(cfg, torch.full_like(z, float("-inf")), i2, w2, load=l2, importance=m2, ws=ws)
+    assert bool((i2 == -1).all()) and not bool(w2.any()) and not bool(l2.any()) and not bool(m2.any())
