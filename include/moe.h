@@ -399,6 +399,85 @@ int32_t moe_linear(const moe_linear_config* cfg, const uint8_t* codes, const flo
                    int64_t ldy, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Low-rank adapters beside such a product, for requests that each bring their own, and the gradients that train them
+ * through frozen codes.
+ *   z = W x + bias + scale[e] B_e (A_e x),   e = ids[t];   y = act(z) + residual
+ * A token whose id is outside [0, n_adapters) has no adapter. ids NULL: adapter 0 for every token. The adapters' sums
+ * are fp32, and so is scale (A x) between the two.
+ * ---------------------------------------------------------------------- */
+typedef struct moe_adapters {
+  int32_t n_adapters; /* 1..1024 */
+  int32_t rank;       /* R: multiple of 8, 8..128 (a smaller rank: zeros behind it) */
+  const void* a;      /* [n_adapters][R][cols], of the call's type */
+  const void* b;      /* [n_adapters][rows][R], of the call's type */
+  const float* scale; /* [n_adapters] */
+} moe_adapters;
+
+/* Bytes of workspace for up to max_tokens tokens of any type (adapters may be NULL; its arrays are not looked at); 0 for an
+ * invalid config. Calls that may overlap need a workspace each; its contents need not be initialized. */
+size_t moe_linear_adapted_workspace_bytes(const moe_linear_config* cfg, const moe_adapters* adapters, int32_t max_tokens);
+
+/* moe_linear with adapters (NULL: none) and, where pre is not NULL, z [T][rows] in the call's type, rows ldp apart: what
+ * moe_linear_backward needs of the forward pass. pre overlaps no other array. What an adapter holds, infinities and NaN
+ * included, changes its own tokens only. a and b are 16-byte aligned. Errors as moe_linear's. */
+int32_t moe_linear_adapted(const moe_linear_config* cfg, const uint8_t* codes, const float* scales, const float* bias,
+                           const moe_adapters* adapters, const int32_t* ids, const void* x, int64_t ldx, int32_t T,
+                           int32_t dtype, const void* residual, int64_t ldr, void* y, int64_t ldy, void* pre, int64_t ldp,
+                           void* ws, size_t ws_bytes, hipStream_t stream);
+
+size_t moe_linear_backward_workspace_bytes(const moe_linear_config* cfg, const moe_adapters* adapters,
+                                           int32_t max_tokens);
+
+/* Gradients of moe_linear_adapted (adapters NULL: of moe_linear) from dy, the gradient of y:
+ *   dz = dy act'(z)  (SwiGLU: of the gate dy up silu'(gate), of the up part dy silu(gate))
+ *   dx = W^T dz + scale A^T (B^T dz) + residual
+ *   d_a [n_adapters][R][cols] = sum over the adapter's tokens of (scale B^T dz) x^T, d_b [n_adapters][rows][R] = of
+ *   dz (scale A x)^T; zeros for adapters without tokens.
+ * pre is the z that the forward call saved (any activation but MOE_ACT_NONE needs it; a ReLU passes where z > 0). dx,
+ * d_a and d_b may each be NULL, not all of them; x is read for d_a and d_b. All are of the call's type. residual may be
+ * NULL or dx itself: the gradients of several products of one x are added so. The gradient of the forward call's residual
+ * is dy. The weights, the bias and the scales have none. dx overlaps no input but residual, d_a and d_b none.
+ * W^T dz is summed in fp32 over one rounding of dz times its row's scale (2^-12 of each term, fp32 2^-23; with group scales
+ * 2^-10 more of each weight, fp32 2^-19). A token whose dz holds an infinity or NaN
+ * has a dx of them, and so have the gradients of its adapter; others are not touched. Sums run in a fixed order: equal calls
+ * give equal bits. Errors: MOE_E_NULL, MOE_E_SHAPE, MOE_E_ARG, MOE_E_WORKSPACE, MOE_E_HIP. */
+int32_t moe_linear_backward(const moe_linear_config* cfg, const uint8_t* codes, const float* scales,
+                            const moe_adapters* adapters, const int32_t* ids, const void* x, int64_t ldx, int32_t T,
+                            int32_t dtype, const void* pre, int64_t ldp, const void* dy, int64_t ldd,
+                            const void* residual, int64_t ldr, void* dx, int64_t ldg, void* d_a, void* d_b, void* ws,
+                            size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The norm over many gradients (adapters', a router's), and the gradients scaled to a largest norm:
+ *   norm = sqrt(sum over all tensors of g^2);  out = g * min(1, max_norm / norm)
+ * A program lays out a table of its tensors once and clips them each step with two launches.
+ * ---------------------------------------------------------------------- */
+typedef struct moe_grad {
+  const void* g;
+  void* out;     /* g itself (in place), or another tensor of the same size and type */
+  int64_t n;     /* elements, 0 or more, at most 2^40 */
+  int32_t dtype; /* MOE_DTYPE_* */
+} moe_grad;
+
+typedef struct moe_grads { /* what moe_grad_table gives */
+  int32_t count;
+  int64_t chunks;
+  void* table;
+} moe_grads;
+
+/* Bytes of a table of these tensors (host array); 0 for invalid ones. */
+size_t moe_grad_table_bytes(const moe_grad* grads /* host */, int32_t count);
+/* Writes the table (device, 256-byte aligned) on `stream` and *out (host). The tensors are not read. An out may overlap no
+ * other tensor of the list and its own g only as a whole. count: 1..65536. Errors: MOE_E_NULL, MOE_E_SHAPE (count, n),
+ * MOE_E_ARG (dtype, alignment, overlap), MOE_E_WORKSPACE (the table), MOE_E_NOMEM, MOE_E_HIP. */
+int32_t moe_grad_table(const moe_grad* grads /* host */, int32_t count, void* table, size_t table_bytes, moe_grads* out,
+                       hipStream_t stream);
+/* norm [1] fp32 (device). max_norm > 0; infinity: the norm alone (in place; else a copy). Squares are summed in 64 bits in
+ * a fixed order. An infinite or NaN norm leaves the gradients as they are (out: a copy). The table holds the sums
+ * between the two launches: calls on one table must not overlap, as those on one list of gradients do not. */
+int32_t moe_grad_clip(const moe_grads* grads, float max_norm, float* norm, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Per-layer LRU expert cache [A][C]: routed experts live in pinned host
  * memory; an HBM pool of n_slots expert slots holds the recently used ones.
  * moe_expert_cache_forward routes on the GPU, reads the unique expert list

@@ -58,6 +58,18 @@ class moe_linear_config(ctypes.Structure):
     _fields_ = [("rows", I32), ("cols", I32), ("weight_bits", I32), ("group_size", I32), ("act", I32)]
 
 
+class moe_adapters(ctypes.Structure):
+    _fields_ = [("n_adapters", I32), ("rank", I32), ("a", P), ("b", P), ("scale", P)]
+
+
+class moe_grad(ctypes.Structure):
+    _fields_ = [("g", P), ("out", P), ("n", I64), ("dtype", I32)]
+
+
+class moe_grads(ctypes.Structure):
+    _fields_ = [("count", I32), ("chunks", I64), ("table", P)]
+
+
 class moe_taps(ctypes.Structure):
     _fields_ = [("topk_ids", P), ("topk_w", P), ("near_tie", P), ("qx", P), ("dx", P), ("h", P), ("qh", P),
                 ("dh", P), ("e_out", P), ("sum_slot", I32), ("gateup_sums", P), ("down_sums", P), ("counts", P),
@@ -103,6 +115,13 @@ _sig("moe_slot_weight_grad", I32, [P, P, P, I32, I32, I32, P, P])
 _sig("moe_slot_weight_grad_experts", I32, [P, P, P, I32, I32, I32, I32, P, P])
 _sig("moe_linear_workspace_bytes", SZ, [P, I32])
 _sig("moe_linear", I32, [P, P, P, P, P, I64, I32, I32, P, I64, P, I64, P, SZ, P])
+_sig("moe_linear_adapted_workspace_bytes", SZ, [P, P, I32])
+_sig("moe_linear_adapted", I32, [P, P, P, P, P, P, P, I64, I32, I32, P, I64, P, I64, P, I64, P, SZ, P])
+_sig("moe_linear_backward_workspace_bytes", SZ, [P, P, I32])
+_sig("moe_linear_backward", I32, [P, P, P, P, P, P, I64, I32, I32, P, I64, P, I64, P, I64, P, I64, P, P, P, SZ, P])
+_sig("moe_grad_table_bytes", SZ, [P, I32])
+_sig("moe_grad_table", I32, [P, I32, P, SZ, P, P])
+_sig("moe_grad_clip", I32, [P, F32, P, P])
 _sig("moe_expert_cache_create", I32, [P, I32, I32, ctypes.POINTER(P)])
 _sig("moe_expert_cache_forward", I32, [P, P, P, P, I32, P, P, SZ, P, P, P, P])
 _sig("moe_expert_cache_stats", I32, [P, P])
@@ -124,6 +143,8 @@ EXPORTED = ("moe_version", "moe_strerror", "moe_last_hip_error", "moe_workspace_
             "moe_layer_forward_noalloc", "moe_layer_forward_routed", "moe_route_workspace_bytes", "moe_route",
             "moe_route_backward", "moe_slot_weight_grad", "moe_slot_weight_grad_experts",
             "moe_linear_workspace_bytes", "moe_linear",
+            "moe_linear_adapted_workspace_bytes", "moe_linear_adapted", "moe_linear_backward_workspace_bytes",
+            "moe_linear_backward", "moe_grad_table_bytes", "moe_grad_table", "moe_grad_clip",
             "moe_expert_cache_create",
             "moe_expert_cache_forward", "moe_expert_cache_stats", "moe_expert_cache_usage", "moe_expert_cache_set_usage",
             "moe_expert_cache_pin_hottest", "moe_expert_cache_destroy", "moe_prof_enable",
@@ -639,6 +660,139 @@ def moe_linear(cfg: LinearConfig, codes, scales, x, y, ws, bias=None, residual=N
                    _dev_ptr(scales, "scales", "f32", n_scales, dev), _opt_ptr(bias, "bias", "f32", rows, dev),
                    x.data_ptr(), ldx, T, dt, res, ldr, _same_dev(y, "y", dev), ldy, _dev_ptr(ws, "ws", None, 0, dev),
                    ws.numel() * ws.element_size())
+
+
+class Adapters:
+    """moe_adapters: a [n][R][cols] and b [n][rows][R] of the activations' type, scale [n] fp32, on one GPU (kept alive
+    here)."""
+
+    def __init__(self, a, b, scale):
+        for t, name in ((a, "a"), (b, "b")):
+            _need(t, name)
+            if t.dim() != 3 or t.dtype not in _float_types():
+                raise ArgError(f"{name}: {t.dtype} {tuple(t.shape)}, expected three dimensions of float32, bfloat16 or float16")
+        n, R, cols = a.shape
+        if b.shape[0] != n or b.shape[2] != R or b.dtype != a.dtype:
+            raise ArgError(f"b: {b.dtype} {tuple(b.shape)}, expected {a.dtype} [{n}, rows, {R}]")
+        _need(scale, "scale", "f32", n)
+        self.device, self.dtype, self.n, self.rank, self.cols, self.rows = a.get_device(), _FLOAT_DT[a.dtype], n, R, cols, b.shape[1]
+        self._keep = (a, b, scale)
+        self.c = moe_adapters(n, R, a.data_ptr(), _same_dev(b, "b", self.device), _same_dev(scale, "scale", self.device))
+        self._ref = ctypes.byref(self.c)
+
+    def ref(self):
+        return self._ref
+
+
+def _adapters_ref(adapters, ids, cfg, T, dt, dev):
+    """References to the adapters and the tokens' ids, or (None, None)."""
+    if adapters is None:
+        return None, None
+    if adapters.device != dev or adapters.dtype != dt or adapters.cols != cfg.cols or adapters.rows != cfg.rows:
+        raise ArgError(f"adapters: [{adapters.rows}, {adapters.cols}] of type {adapters.dtype} on cuda:{adapters.device}, "
+                       f"the call's [{cfg.rows}, {cfg.cols}] of type {dt} on cuda:{dev}")
+    return adapters._ref, _opt_ptr(ids, "ids", "i32", T, dev)
+
+
+def moe_linear_adapted_workspace_bytes(cfg: LinearConfig, adapters, max_tokens: int) -> int:
+    return int(_lib.moe_linear_adapted_workspace_bytes(cfg.ref(), adapters and adapters.ref(), int(max_tokens)))
+
+
+def _rows_like(t, name, dt, T, cols, dev):
+    """(address, elements between rows) of an optional matrix of the call's type and tokens."""
+    if t is None:
+        return None, 0
+    dt_t, rows, ld = _matrix(t, name, cols)
+    if dt_t != dt or rows < T:
+        raise ArgError(f"{name}: {t.dtype} {tuple(t.shape)}, expected the call's type and [>= {T}, {cols}]")
+    return _same_dev(t, name, dev), ld
+
+
+def _code_ptrs(cfg, codes, scales, dev):
+    # an invalid configuration is the library's to reject, before it looks at the data: sizes as if it were valid
+    rows, cols, G = cfg.rows, cfg.cols, cfg.group_size
+    return (_dev_ptr(codes, "codes", "u8", rows * cols * (8 if cfg.weight_bits == 8 else 4) // 8, dev),
+            _dev_ptr(scales, "scales", "f32", rows * (cols // G) if G > 0 else rows, dev))
+
+
+def moe_linear_adapted(cfg: LinearConfig, codes, scales, adapters, ids, x, y, ws, bias=None, residual=None, pre=None,
+                       stream=None):
+    """moe_linear with a low-rank adapter by token: ids [T] int32 (outside [0, n): none; None: adapter 0 for all). pre
+    [T][rows] takes the values in front of the activation, for moe_linear_backward."""
+    rows = cfg.rows
+    out = rows // 2 if cfg.act == MOE_ACT_SWIGLU else rows
+    dt, T, ldx = _matrix(x, "x", cfg.cols)
+    dev = x.get_device()
+    ad, ids = _adapters_ref(adapters, ids, cfg, T, dt, dev)
+    if y is None:
+        raise ArgError("y: a device tensor is required")
+    return _launch(_lib.moe_linear_adapted, dev, stream, cfg.ref(), *_code_ptrs(cfg, codes, scales, dev),
+                   _opt_ptr(bias, "bias", "f32", rows, dev), ad, ids, x.data_ptr(), ldx, T, dt,
+                   *_rows_like(residual, "residual", dt, T, out, dev), *_rows_like(y, "y", dt, T, out, dev),
+                   *_rows_like(pre, "pre", dt, T, rows, dev), _dev_ptr(ws, "ws", None, 0, dev),
+                   ws.numel() * ws.element_size())
+
+
+def moe_linear_backward_workspace_bytes(cfg: LinearConfig, adapters, max_tokens: int) -> int:
+    return int(_lib.moe_linear_backward_workspace_bytes(cfg.ref(), adapters and adapters.ref(), int(max_tokens)))
+
+
+def moe_linear_backward(cfg: LinearConfig, codes, scales, dy, dx, ws, pre=None, adapters=None, ids=None, x=None, d_a=None,
+                        d_b=None, residual=None, stream=None):
+    """Gradients of moe_linear_adapted (without adapters: of moe_linear) from dy: dx [T][cols] (+ residual, which may be dx
+    itself), d_a and d_b like the adapters' a and b. pre is what the forward call saved (not needed without an activation),
+    x its activations (needed for d_a and d_b). dx, d_a or d_b may be None."""
+    rows, cols = cfg.rows, cfg.cols
+    dt, T, ldd = _matrix(dy, "dy", rows // 2 if cfg.act == MOE_ACT_SWIGLU else rows)
+    dev = dy.get_device()
+    ad, ids = _adapters_ref(adapters, ids, cfg, T, dt, dev)
+    grads = []
+    for t, name, k in ((d_a, "d_a", cols), (d_b, "d_b", rows)):
+        if t is not None and ad is None:
+            raise ArgError(f"{name}: there are no adapters")
+        if t is not None and t.dtype != dy.dtype:
+            raise ArgError(f"{name}: dtype {t.dtype}, expected {dy.dtype}")
+        grads.append(None if t is None else _dev_ptr(t, name, None, adapters.n * adapters.rank * k, dev))
+    return _launch(_lib.moe_linear_backward, dev, stream, cfg.ref(), *_code_ptrs(cfg, codes, scales, dev), ad, ids,
+                   *_rows_like(x, "x", dt, T, cols, dev), T, dt, *_rows_like(pre, "pre", dt, T, rows, dev),
+                   dy.data_ptr(), ldd, *_rows_like(residual, "residual", dt, T, cols, dev),
+                   *_rows_like(dx, "dx", dt, T, cols, dev), *grads, _dev_ptr(ws, "ws", None, 0, dev),
+                   ws.numel() * ws.element_size())
+
+
+class GradTable:
+    """moe_grad_table of a list of contiguous gradients (kept alive here) and where they go: `out`, as many tensors of the
+    same sizes and types, or None for in place. Building it waits for the current stream."""
+
+    def __init__(self, grads, out=None):
+        grads = list(grads)
+        out = grads if out is None else list(out)
+        if not grads or len(out) != len(grads):
+            raise ArgError(f"{len(grads)} gradients, {len(out)} outputs")
+        self.device = _need(grads[0], "grads").get_device()
+        types = _float_types()
+        c = (moe_grad * len(grads))()
+        for i, (g, o) in enumerate(zip(grads, out)):
+            for t, name in ((g, f"grads[{i}]"), (o, f"out[{i}]")):
+                _need(t, name)
+                _same_dev(t, name, self.device)
+            if g.dtype not in types or o.dtype != g.dtype or o.numel() != g.numel():
+                raise ArgError(f"grads[{i}]: {g.dtype} {tuple(g.shape)} to {o.dtype} {tuple(o.shape)}")
+            c[i] = moe_grad(g.data_ptr(), o.data_ptr(), g.numel(), types[g.dtype])
+        self._keep = (grads, out)
+        with torch.cuda.device(self.device):
+            size = int(_lib.moe_grad_table_bytes(c, len(grads)))
+            self._table = torch.empty((max(size, 1),), dtype=torch.uint8, device=f"cuda:{self.device}")
+            self.c = moe_grads()
+            _launch(_lib.moe_grad_table, self.device, None, c, len(grads), self._table.data_ptr(), size, ctypes.byref(self.c))
+            torch.cuda.current_stream().synchronize()
+        self._ref = ctypes.byref(self.c)
+
+
+def moe_grad_clip(table: GradTable, max_norm: float, norm, stream=None):
+    """norm [1] = the 2-norm over all gradients of the table; out = gradient * min(1, max_norm / norm)."""
+    dev = table.device
+    return _launch(_lib.moe_grad_clip, dev, stream, table._ref, max_norm, _dev_ptr(norm, "norm", "f32", 1, dev))
 
 
 def moe_prof_enable(max_calls: int, stages=None):

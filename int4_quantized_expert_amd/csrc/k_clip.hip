@@ -1,0 +1,202 @@
+// k_clip.hip — the norm over many gradients, and the gradients scaled to a largest norm.
+//
+// Memory decides: one pass for the norm, one that reads again and writes. A table on the device, written once by the
+// caller's program, holds the tensors and which tensor each run of kChunk elements belongs to, so a pass is one launch
+// over all of them. Squares are taken and summed in 64 bits: no gradient's square overflows or vanishes. The second
+// launch adds the first one's sums itself, in a fixed order.
+#include "linear_types.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kChunk = 8192;        // elements; 32 of a lane, its loads all in flight
+constexpr int kClipBlocks = 2048;   // workgroups at most: eight a compute unit
+constexpr int kTableArgs = 64;      // tensors of a launch that writes the table
+
+struct ClipEntry {
+  const void* g;
+  void* out;
+  int64_t n;
+  int64_t first;  // chunk
+  int32_t dtype;
+  int32_t skip;   // elements between the 16-byte boundary in front of g and g
+};
+struct ClipHead {
+  double sums[kClipBlocks];
+};
+// table: ClipHead, entries [count], tensor of each chunk [chunks]
+struct ClipPlan {
+  size_t entries, owner, total;
+};
+ClipPlan clip_plan(int64_t count, int64_t chunks) {
+  ClipPlan p;
+  p.entries = sizeof(ClipHead);
+  p.owner = p.entries + (size_t)count * sizeof(ClipEntry);
+  p.total = (p.owner + (size_t)chunks * 4 + 255) & ~(size_t)255;
+  return p;
+}
+size_t size_of(int32_t dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
+int32_t skip_of(const moe_grad& g) { return (int32_t)(reinterpret_cast<uintptr_t>(g.g) % 16 / size_of(g.dtype)); }
+int64_t chunks_of(const moe_grad& g) { return g.n == 0 ? 0 : (g.n + skip_of(g) + kChunk - 1) / kChunk; }
+
+struct TableArgs {
+  ClipEntry e[kTableArgs];
+  int32_t first, count;
+  ClipEntry* entries;
+  int32_t* owner;
+};
+// a workgroup for each tensor
+__global__ __launch_bounds__(256) void k_clip_table(TableArgs a) {
+  const ClipEntry e = a.e[blockIdx.x];
+  if (threadIdx.x == 0) a.entries[a.first + blockIdx.x] = e;
+  const int64_t chunks = e.n == 0 ? 0 : (e.n + e.skip + kChunk - 1) / kChunk;
+  for (int64_t k = threadIdx.x; k < chunks; k += 256) a.owner[e.first + k] = a.first + blockIdx.x;
+}
+
+// The vectors of a chunk: lane's k-th is 256 k + tid; elements in front of and behind the tensor's are not touched.
+template <class T, class F>
+__device__ __forceinline__ void each_vector(const ClipEntry& e, int64_t chunk, F&& f) {
+  constexpr int V = 16 / sizeof(T), kPer = kChunk / (256 * V);
+  const int64_t v0 = chunk * (kChunk / V);
+  u4v d[kPer];
+  const T* g = static_cast<const T*>(e.g) - e.skip;  // on a 16-byte boundary
+  const int64_t end = e.n + e.skip;
+  auto load = [&](int64_t at) __attribute__((always_inline)) {
+    if (at >= e.skip && at + V <= end) return *reinterpret_cast<const u4v*>(g + at);
+    T t[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) t[i] = at + i >= e.skip && at + i < end ? g[at + i] : from_f32<T>(0.0f);
+    return __builtin_bit_cast(u4v, t);
+  };
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) d[k] = load((v0 + 256 * k + threadIdx.x) * V);
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) f((v0 + 256 * k + threadIdx.x) * V, d[k]);
+}
+
+template <class T>
+__device__ __forceinline__ double squares(const ClipEntry& e, int64_t chunk) {
+  double s = 0.0;
+  each_vector<T>(e, chunk, [&](int64_t, const u4v& d) __attribute__((always_inline)) {
+    T t[16 / sizeof(T)];
+    __builtin_memcpy(t, &d, 16);
+#pragma unroll
+    for (int i = 0; i < (int)(16 / sizeof(T)); ++i) {
+      const double v = (double)to_f32<T>(t[i]);
+      s = fma(v, v, s);
+    }
+  });
+  return s;
+}
+
+__device__ __forceinline__ double block_sum(double v, double* s_wave) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  if ((threadIdx.x & 63) == 0) s_wave[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return s_wave[0] + s_wave[1] + s_wave[2] + s_wave[3];
+}
+
+__global__ __launch_bounds__(256) void k_clip_norm(const ClipEntry* __restrict__ entries, const int32_t* __restrict__ owner,
+                                                   int64_t chunks, double* __restrict__ sums) {
+  __shared__ double s_wave[4];
+  double s = 0.0;
+  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const ClipEntry e = entries[owner[c]];
+    if (e.dtype == MOE_DTYPE_F32) s += squares<float>(e, c - e.first);
+    else if (e.dtype == MOE_DTYPE_BF16) s += squares<bf16_t>(e, c - e.first);
+    else s += squares<_Float16>(e, c - e.first);
+  }
+  s = block_sum(s, s_wave);
+  if (threadIdx.x == 0) sums[blockIdx.x] = s;
+}
+
+template <class T>
+__device__ __forceinline__ void scale_chunk(const ClipEntry& e, int64_t chunk, float factor) {
+  constexpr int V = 16 / sizeof(T);
+  T* out = static_cast<T*>(e.out) - e.skip;
+  const bool whole = reinterpret_cast<uintptr_t>(out) % 16 == 0;
+  const int64_t end = e.n + e.skip;
+  each_vector<T>(e, chunk, [&](int64_t at, const u4v& d) __attribute__((always_inline)) {
+    T t[V];
+    __builtin_memcpy(t, &d, 16);
+#pragma unroll
+    for (int i = 0; i < V; ++i) t[i] = from_f32<T>(to_f32<T>(t[i]) * factor);
+    if (whole && at >= e.skip && at + V <= end) {
+      *reinterpret_cast<u4v*>(out + at) = __builtin_bit_cast(u4v, t);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (at + i >= e.skip && at + i < end) out[at + i] = t[i];
+    }
+  });
+}
+
+__global__ __launch_bounds__(256) void k_clip_scale(const ClipEntry* __restrict__ entries, const int32_t* __restrict__ owner,
+                                                    int64_t chunks, const double* __restrict__ sums, int count,
+                                                    float max_norm, float* __restrict__ norm) {
+  __shared__ double s_wave[4];
+  double v[kClipBlocks / 256];
+#pragma unroll
+  for (int k = 0; k < kClipBlocks / 256; ++k) {
+    const int i = 256 * k + threadIdx.x;
+    v[k] = i < count ? sums[i] : 0.0;
+  }
+  double s = 0.0;
+#pragma unroll
+  for (int k = 0; k < kClipBlocks / 256; ++k) s += v[k];
+  const double n = sqrt(block_sum(s, s_wave));
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
+  // an infinite or NaN norm leaves the gradients as they are
+  const float factor = n > (double)max_norm && (float)n < INFINITY ? (float)((double)max_norm / n) : 1.0f;
+  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const ClipEntry e = entries[owner[c]];
+    if (factor == 1.0f && e.out == e.g) continue;
+    if (e.dtype == MOE_DTYPE_F32) scale_chunk<float>(e, c - e.first, factor);
+    else if (e.dtype == MOE_DTYPE_BF16) scale_chunk<bf16_t>(e, c - e.first, factor);
+    else scale_chunk<_Float16>(e, c - e.first, factor);
+  }
+}
+
+}  // namespace
+
+int64_t clip_chunks(const moe_grad* g, int count) {
+  int64_t n = 0;
+  for (int i = 0; i < count; ++i) n += chunks_of(g[i]);
+  return n;
+}
+size_t clip_table_bytes(const moe_grad* g, int count) { return clip_plan(count, clip_chunks(g, count)).total; }
+
+hipError_t launch_clip_table(const moe_grad* g, int count, void* table, hipStream_t st) {
+  const ClipPlan p = clip_plan(count, clip_chunks(g, count));
+  char* w = static_cast<char*>(table);
+  int64_t chunk = 0;
+  for (int at = 0; at < count; at += kTableArgs) {
+    TableArgs a;
+    a.first = at;
+    a.count = count - at < kTableArgs ? count - at : kTableArgs;
+    a.entries = reinterpret_cast<ClipEntry*>(w + p.entries);
+    a.owner = reinterpret_cast<int32_t*>(w + p.owner);
+    for (int i = 0; i < a.count; ++i) {
+      a.e[i] = ClipEntry{g[at + i].g, g[at + i].out, g[at + i].n, chunk, g[at + i].dtype, skip_of(g[at + i])};
+      chunk += chunks_of(g[at + i]);
+    }
+    k_clip_table<<<a.count, 256, 0, st>>>(a);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_clip(const moe_grads& t, float max_norm, float* norm, hipStream_t st) {
+  const ClipPlan p = clip_plan(t.count, t.chunks);
+  char* w = static_cast<char*>(t.table);
+  double* sums = reinterpret_cast<double*>(w);
+  const ClipEntry* entries = reinterpret_cast<const ClipEntry*>(w + p.entries);
+  const int32_t* owner = reinterpret_cast<const int32_t*>(w + p.owner);
+  const int blocks = (int)(t.chunks < 1 ? 1 : t.chunks < kClipBlocks ? t.chunks : kClipBlocks);
+  k_clip_norm<<<blocks, 256, 0, st>>>(entries, owner, t.chunks, sums);
+  k_clip_scale<<<blocks, 256, 0, st>>>(entries, owner, t.chunks, sums, blocks, max_norm, norm);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,69 @@
+// k_linear_adapted.hip — y = act(W x + b + s B (A x)) + r with low-rank adapters by token, and the values in front of the
+// activation for a backward pass: the kernels of the product with the adapters' second half in their epilogue. The first
+// half, s (A x), R values a token, is k_adapt.hip's. For more than a few tokens the tiles work on tokens ordered by adapter.
+#define MOE_ADAPTED 1
+#define MOE_TRANSPOSED 0
+#include "linear_kernels.h"
+
+namespace moe {
+
+namespace {
+struct AdaptedPlan {
+  size_t h, order, ad, total;
+};
+AdaptedPlan adapted_plan(const moe_linear_config& c, int R, int64_t T) {
+  AdaptedPlan p;
+  p.h = up256(linear_ws_bytes(c, T));
+  p.order = p.h + up256((size_t)T * R * 4);
+  p.ad = p.order + up256((size_t)T * 4);
+  p.total = p.ad + up256((size_t)T * 4);
+  return p;
+}
+
+template <class TX>
+hipError_t run(LinearArgs& a, int bits, const moe_adapters* ad, const int32_t* ids, int dtype, void* ws,
+               const AdaptedPlan& p, hipStream_t st) {
+  char* w = static_cast<char*>(ws);
+  const bool few = is_slim(a.T, a.N);
+  if (ad) {
+    a.h = reinterpret_cast<const float*>(w + p.h);
+    a.ab = ad->b;
+    a.n_ad = ad->n_adapters;
+    a.R = ad->rank;
+    a.ad = ids;
+    if (!few && ids) {
+      int32_t* order = reinterpret_cast<int32_t*>(w + p.order);
+      int32_t* pos_ad = reinterpret_cast<int32_t*>(w + p.ad);
+      const hipError_t e = launch_adapt_order(ids, a.T, a.n_ad, order, pos_ad, st);
+      if (e != hipSuccess) return e;
+      a.order = order;
+      a.ad = pos_ad;
+    }
+    const AdaptDown d{a.x, a.ldx, a.vec_x, a.T, a.K, a.R, a.n_ad, a.order, a.ad, ad->a, ad->scale,
+                      reinterpret_cast<float*>(w + p.h), nullptr, 0};
+    const hipError_t e = launch_adapt_down(d, dtype, st);
+    if (e != hipSuccess) return e;
+  }
+  linear_launch<TX>(a, bits, ws, st);
+  return hipGetLastError();
+}
+}  // namespace
+
+size_t adapted_ws_bytes(const moe_linear_config& c, int R, int64_t T) { return adapted_plan(c, R, T).total; }
+
+hipError_t launch_linear_adapted(const moe_linear_config& c, const uint8_t* codes, const float* scales, const float* bias,
+                                 const moe_adapters* ad, const int32_t* ids, const void* x, int64_t ldx, int T, int dtype,
+                                 const void* res, int64_t ldr, void* y, int64_t ldy, void* pre, int64_t ldp, void* ws,
+                                 hipStream_t st) {
+  LinearArgs a = linear_args(c, codes, scales, bias, x, ldx, T, dtype, res, ldr, y, ldy, ws);
+  a.pre = pre;
+  a.ldp = ldp;
+  a.vec_p = reinterpret_cast<uintptr_t>(pre) % (dtype == MOE_DTYPE_F32 ? 16 : 8) == 0 && ldp % 4 == 0;
+  const AdaptedPlan p = adapted_plan(c, ad ? ad->rank : 0, T);
+  const int bits = c.weight_bits == 8 ? 8 : 4;
+  if (dtype == MOE_DTYPE_F32) return run<float>(a, bits, ad, ids, dtype, ws, p, st);
+  if (dtype == MOE_DTYPE_BF16) return run<bf16_t>(a, bits, ad, ids, dtype, ws, p, st);
+  return run<_Float16>(a, bits, ad, ids, dtype, ws, p, st);
+}
+
+}  // namespace moe
