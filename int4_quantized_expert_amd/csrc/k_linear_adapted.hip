@@ -9,14 +9,17 @@ namespace moe {
 
 namespace {
 struct AdaptedPlan {
-  size_t h, order, ad, total;
+  size_t h, order, ad, n_runs, runs, total;
 };
-AdaptedPlan adapted_plan(const moe_linear_config& c, int R, int64_t T) {
+AdaptedPlan adapted_plan(const moe_linear_config& c, const moe_adapters* ad, int64_t T) {
+  const size_t R = ad ? ad->rank : 0;
   AdaptedPlan p;
   p.h = up256(linear_ws_bytes(c, T));
-  p.order = p.h + up256((size_t)T * R * 4);
-  p.ad = p.order + up256((size_t)T * 4);
-  p.total = p.ad + up256((size_t)T * 4);
+  p.order = p.h + up256(T * R * 4);
+  p.ad = p.order + up256(T * 4);
+  p.n_runs = p.ad + up256(T * 4);
+  p.runs = p.n_runs + 256;
+  p.total = p.runs + (ad ? up256(sizeof(AdaptChunk) * adapt_max_runs(T, ad->n_adapters)) : 0);
   return p;
 }
 
@@ -31,16 +34,20 @@ hipError_t run(LinearArgs& a, int bits, const moe_adapters* ad, const int32_t* i
     a.n_ad = ad->n_adapters;
     a.R = ad->rank;
     a.ad = ids;
-    if (!few && ids) {
-      int32_t* order = reinterpret_cast<int32_t*>(w + p.order);
-      int32_t* pos_ad = reinterpret_cast<int32_t*>(w + p.ad);
-      const hipError_t e = launch_adapt_order(ids, a.T, a.n_ad, order, pos_ad, st);
+    AdaptDown d{};
+    d.T = a.T, d.R = a.R, d.n_ad = a.n_ad, d.parts = 1, d.by_token = few;
+    d.scale = ad->scale;
+    const bool sorted = ids && !(few && adapt_few(a.T, a.R));
+    const AdaptOrder o{reinterpret_cast<int32_t*>(w + p.order), reinterpret_cast<int32_t*>(w + p.ad),
+                       reinterpret_cast<int32_t*>(w + p.n_runs), reinterpret_cast<AdaptChunk*>(w + p.runs)};
+    if (sorted) {
+      const hipError_t e = launch_adapt_order(ids, a.T, a.n_ad, o, st);
       if (e != hipSuccess) return e;
-      a.order = order;
-      a.ad = pos_ad;
+      d.n_runs = o.n_runs, d.runs = o.runs;
+      if (!few) a.order = o.order, a.ad = o.ad;
     }
-    const AdaptDown d{a.x, a.ldx, a.vec_x, a.T, a.K, a.R, a.n_ad, a.order, a.ad, ad->a, ad->scale,
-                      reinterpret_cast<float*>(w + p.h), nullptr, 0};
+    d.ad = sorted ? o.ad : ids;
+    d.part[0] = {a.x, a.ldx, a.vec_x, a.K, sorted ? o.order : nullptr, ad->a, reinterpret_cast<float*>(w + p.h), nullptr};
     const hipError_t e = launch_adapt_down(d, dtype, st);
     if (e != hipSuccess) return e;
   }
@@ -49,7 +56,9 @@ hipError_t run(LinearArgs& a, int bits, const moe_adapters* ad, const int32_t* i
 }
 }  // namespace
 
-size_t adapted_ws_bytes(const moe_linear_config& c, int R, int64_t T) { return adapted_plan(c, R, T).total; }
+size_t adapted_ws_bytes(const moe_linear_config& c, const moe_adapters* ad, int64_t T) {
+  return adapted_plan(c, ad, T).total;
+}
 
 hipError_t launch_linear_adapted(const moe_linear_config& c, const uint8_t* codes, const float* scales, const float* bias,
                                  const moe_adapters* ad, const int32_t* ids, const void* x, int64_t ldx, int T, int dtype,
@@ -59,7 +68,7 @@ hipError_t launch_linear_adapted(const moe_linear_config& c, const uint8_t* code
   a.pre = pre;
   a.ldp = ldp;
   a.vec_p = reinterpret_cast<uintptr_t>(pre) % (dtype == MOE_DTYPE_F32 ? 16 : 8) == 0 && ldp % 4 == 0;
-  const AdaptedPlan p = adapted_plan(c, ad ? ad->rank : 0, T);
+  const AdaptedPlan p = adapted_plan(c, ad, T);
   const int bits = c.weight_bits == 8 ? 8 : 4;
   if (dtype == MOE_DTYPE_F32) return run<float>(a, bits, ad, ids, dtype, ws, p, st);
   if (dtype == MOE_DTYPE_BF16) return run<bf16_t>(a, bits, ad, ids, dtype, ws, p, st);

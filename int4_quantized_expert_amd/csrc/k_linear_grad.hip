@@ -40,106 +40,165 @@ struct DzArgs {
   void* dz;              // [T][N] by position, or nullptr
 };
 
-template <class TX>
-__device__ __forceinline__ f8v dz8(const DzArgs& d, int64_t t, int n) {
+// dz of eight neighbouring rows n, kind 2 (SwiGLU): of eight gate rows and the up rows that go with them.
+template <class TX, int KIND>
+__device__ __forceinline__ void dz8(const DzArgs& d, int64_t t, int n, f8v (&o)[KIND == 2 ? 2 : 1]) {
   Granule<TX> g, z, u;
-  const int at = d.half && n >= d.half ? n - d.half : n;
-  load8(static_cast<const TX*>(d.dy) + t * d.ldd + at, d.vec_d, g);
-  f8v v = granule_f32<TX>(g);
-  if (d.act == MOE_ACT_NONE) return v;
-  const TX* p = static_cast<const TX*>(d.pre) + t * d.ldp;
-  load8(p + at, d.vec_p, z);
-  const f8v zv = granule_f32<TX>(z);
-  if (!d.half) {
+  load8(static_cast<const TX*>(d.dy) + t * d.ldd + n, d.vec_d, g);
+  const TX* p = static_cast<const TX*>(d.pre) + t * d.ldp + n;
+  if (KIND > 0) load8(p, d.vec_p, z);
+  if (KIND == 2) load8(p + d.half, d.vec_p, u);
+  const f8v v = granule_f32<TX>(g);
+  o[0] = v;
+  if constexpr (KIND == 1) {
+    const f8v zv = granule_f32<TX>(z);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= slope(zv[i], d.act);
-  } else if (n < d.half) {
-    load8(p + d.half + at, d.vec_p, u);
-    const f8v uv = granule_f32<TX>(u);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = v[i] * uv[i] * slope(zv[i], MOE_ACT_SILU);
-  } else {
+    for (int i = 0; i < 8; ++i) o[0][i] = v[i] * slope(zv[i], d.act);
+  }
+  if constexpr (KIND == 2) {
+    const f8v zv = granule_f32<TX>(z), uv = granule_f32<TX>(u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      // gate beyond 1e9: the limits of silu and of its derivative, so that no infinity meets a zero
+      const float c = zv[i] != zv[i] ? zv[i] : fminf(fmaxf(zv[i], -1e9f), 1e9f);
       float s, miss;
-      sigmoid2(zv[i], s, miss);
-      v[i] *= zv[i] < -1e9f ? 0.0f : zv[i] * s;
+      sigmoid2(c, s, miss);
+      o[0][i] = v[i] * uv[i] * fmaf(c * s, miss, s);
+      o[1][i] = v[i] * (zv[i] < -1e9f ? 0.0f : zv[i] * s);
     }
   }
-  return v;
 }
 
-// As k_linear_x, from dz: 8 positions a workgroup, the largest of a token first.
+// Eight values between the search for a token's largest and the conversion: fp32 as they are, for 16-bit types already as
+// fp16 over a power of two of their own, which takes half the registers and is the only rounding (but for values far
+// below the token's largest).
 template <class TX>
-__global__ __launch_bounds__(8 * kPrepLanes) void k_linear_dz(DzArgs d) {
-  constexpr int kRounds = 4;  // granules whose values stay in registers
-  __shared__ uint32_t s_max[16][8];
+struct Held {
+  h8 v;
+  int sh;
+};
+template <>
+struct Held<float> {
+  f8v v;
+};
+template <class TX>
+__device__ __forceinline__ void hold(const f8v& w, uint32_t& m, Held<TX>& o) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(w[i]) & 0x7FFFFFFFu);
+  m = max(m, top);
+  if constexpr (std::is_same<TX, float>::value) {
+    o.v = w;
+  } else {
+    o.sh = scale_shift(top);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float x = ldexpf(w[(i >> 1) + 4 * (i & 1)], o.sh);
+      if (top >= 0x7F800000u && fabsf(x) < INFINITY) x = fminf(fmaxf(x, -65504.0f), 65504.0f);
+      o.v[i] = (_Float16)x;
+    }
+  }
+}
+
+// As k_linear_x, from dz: TOK positions a workgroup, the largest of a token first. kind: 0 no activation, 1 one row at a
+// time, 2 SwiGLU. A row's values stay in registers between the search for the largest and the conversion as far as they fit
+// (kRounds items of a lane), the rest is computed twice. One position a workgroup where there are few.
+template <class TX, int KIND, int TOK>
+__global__ __launch_bounds__(1024) void k_linear_dz(DzArgs d) {
+  constexpr int kLanes = 1024 / TOK, V = KIND == 2 ? 2 : 1;
+  constexpr int kRounds = TOK == 1 ? 2 : (std::is_same<TX, float>::value ? 8 : 12) / V;
+  __shared__ uint32_t s_max[16][TOK];
   const LinearArgs& a = d.a;
-  const int tk = threadIdx.x & 7, g0 = threadIdx.x >> 3;
-  const int p = blockIdx.x * 8 + tk;
+  const int tk = threadIdx.x % TOK, g0 = threadIdx.x / TOK;
+  const int p = blockIdx.x * TOK + tk;
   const bool in = p < a.T;
   const int64_t t = in ? token_of(a, p) : 0;
-  const int ng = in ? d.N / 8 : 0;
-  f8v v[kRounds];
+  const int items = d.N / V / 8, ng = in ? items : 0;
+  Held<TX> v[kRounds][V];
   uint32_t m = 0;
-  auto scaled = [&](int g, bool keep) __attribute__((always_inline)) {
-    f8v w = dz8<TX>(d, t, g * 8);
-    if (keep && d.dz) {
-      TX o[8];
+  auto scaled = [&](int g, bool keep, Held<TX> (&o)[V]) __attribute__((always_inline)) {
+    f8v w[V];
+    dz8<TX, KIND>(d, t, g * 8, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = from_f32<TX>(w[i]);
-      Granule<TX> q;
-      __builtin_memcpy(&q, o, sizeof(q));
-      u4v* to = reinterpret_cast<u4v*>(static_cast<TX*>(d.dz) + (size_t)p * d.N + g * 8);
+    for (int k = 0; k < V; ++k) {
+      const int n = k * d.half + g * 8;
+      if (keep && d.dz) {
+        TX q[8];
 #pragma unroll
-      for (int i = 0; i < (int)sizeof(TX) / 2; ++i) to[i] = u4v{q.w[4 * i], q.w[4 * i + 1], q.w[4 * i + 2], q.w[4 * i + 3]};
+        for (int i = 0; i < 8; ++i) q[i] = from_f32<TX>(w[k][i]);
+        u4v* to = reinterpret_cast<u4v*>(static_cast<TX*>(d.dz) + (size_t)p * d.N + n);
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(TX) / 2; ++i) {
+          u4v u;
+          __builtin_memcpy(&u, reinterpret_cast<const char*>(q) + 16 * i, 16);
+          to[i] = u;
+        }
+      }
+      if (d.mul) {
+        const f8v s = *reinterpret_cast<const f8v*>(d.mul + n);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[k][i] *= s[i];
+        hold<TX>(w[k], m, o[k]);
+      }
     }
-    if (d.mul) {
-      const f8v s = *reinterpret_cast<const f8v*>(d.mul + g * 8);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] *= s[i];
-    }
-    return w;
-  };
-  auto largest = [&](const f8v& w) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(w[i]) & 0x7FFFFFFFu);
   };
 #pragma unroll
   for (int k = 0; k < kRounds; ++k)
-    if (g0 + k * kPrepLanes < ng) {
-      v[k] = scaled(g0 + k * kPrepLanes, true);
-      largest(v[k]);
-    }
-  for (int g = g0 + kRounds * kPrepLanes; g < ng; g += kPrepLanes) largest(scaled(g, true));
+    if (g0 + k * kLanes < ng) scaled(g0 + k * kLanes, true, v[k]);
+  for (int g = g0 + kRounds * kLanes; g < ng; g += kLanes) {
+    Held<TX> o[V];
+    scaled(g, true, o);
+  }
   if (!d.mul) return;
 #pragma unroll
-  for (int o = 8; o < 64; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
-  if ((threadIdx.x & 63) < 8) s_max[threadIdx.x >> 6][tk] = m;
+  for (int o = TOK; o < 64; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
+  if ((threadIdx.x & 63) < TOK) s_max[threadIdx.x >> 6][tk] = m;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 16; ++i) m = max(m, s_max[i][tk]);
-  const bool finite = m < 0x7F800000u;
   const int sh = scale_shift(m);
+  const bool finite = m < 0x7F800000u;
   if (in && g0 == 0) a.sh[p] = sh;
   const size_t base = (size_t)(p >> 5) * a.nbp * 1024 + (size_t)(p & 31) * 8;
-  auto store = [&](int g, f8v w) __attribute__((always_inline)) {
-    h8 hi, lo;
+  auto store = [&](int g, const Held<TX> (&o)[V]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float x = ldexpf(w[(i >> 1) + 4 * (i & 1)], sh);
-      if (!finite && fabsf(x) < INFINITY) x = fminf(fmaxf(x, -65504.0f), 65504.0f);
-      hi[i] = (_Float16)x;
-      lo[i] = fabsf(x) < INFINITY ? (_Float16)(x - (float)hi[i]) : (_Float16)0.0f;
+    for (int k = 0; k < V; ++k) {
+      h8 hi = {}, lo = {};
+      if (in) {
+        if constexpr (std::is_same<TX, float>::value) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float x = ldexpf(o[k].v[(i >> 1) + 4 * (i & 1)], sh);
+            if (!finite && fabsf(x) < INFINITY) x = fminf(fmaxf(x, -65504.0f), 65504.0f);
+            hi[i] = (_Float16)x;
+            lo[i] = fabsf(x) < INFINITY ? (_Float16)(x - (float)hi[i]) : (_Float16)0.0f;
+          }
+        } else {  // a token with an infinity or NaN: its other values only stay finite, whatever they are
+          const int by = finite ? sh - o[k].sh : 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) hi[i] = __builtin_amdgcn_ldexph(o[k].v[i], by);
+        }
+      }
+      const size_t at = base + ((size_t)k * (d.half / 8) + g) * 256;
+      *reinterpret_cast<h8*>(a.xh + at) = hi;
+      if (std::is_same<TX, float>::value) *reinterpret_cast<h8*>(a.xl + at) = lo;
     }
-    const size_t at = base + (size_t)g * 256;
-    *reinterpret_cast<h8*>(a.xh + at) = hi;
-    if (std::is_same<TX, float>::value) *reinterpret_cast<h8*>(a.xl + at) = lo;
   };
 #pragma unroll
   for (int k = 0; k < kRounds; ++k)
-    if (g0 + k * kPrepLanes < d.N / 8) store(g0 + k * kPrepLanes, in ? v[k] : f8v{});
-  for (int g = g0 + kRounds * kPrepLanes; g < d.N / 8; g += kPrepLanes) store(g, in ? scaled(g, false) : f8v{});
+    if (g0 + k * kLanes < items) store(g0 + k * kLanes, v[k]);
+  for (int g = g0 + kRounds * kLanes; g < items; g += kLanes) {
+    Held<TX> o[V] = {};
+    if (in) scaled(g, false, o);
+    store(g, o);
+  }
+}
+
+template <class TX, int KIND>
+void dz_launch(const DzArgs& d, hipStream_t st) {
+  const int padded = (d.a.T + 31) / 32 * 32;
+  if (d.a.T <= 1024) k_linear_dz<TX, KIND, 1><<<padded, 1024, 0, st>>>(d);
+  else k_linear_dz<TX, KIND, 8><<<padded / 8, 1024, 0, st>>>(d);
 }
 
 // ------------------------------------------------------------ group scales
@@ -165,7 +224,7 @@ __global__ __launch_bounds__(256) void k_group_scales(const float* __restrict__ 
     if (!low) {
       gs[o] = (_Float16)v;
     } else {  // eight bits, whose product with a code is exact, and the rest
-      const float hi = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
+      const float hi = to_f32<bf16_t>(from_f32<bf16_t>(v));
       gs[o] = (_Float16)hi;
       gs[gs_low + o] = (_Float16)(v - (float)(_Float16)hi);
     }
@@ -175,7 +234,7 @@ __global__ __launch_bounds__(256) void k_group_scales(const float* __restrict__ 
 // ------------------------------------------------------------ the whole
 struct GradPlan {
   LinearPlan z;
-  size_t mul, gs, dz, order, ad, offsets, slot0, n_chunks, chunks, h, ht, u, ut, at, bt, part, total;
+  size_t mul, gs, dz, order, ad, offsets, slot0, n_chunks, runs, chunks, h, ht, u, ut, at, bt, part, part_a, total;
   int ldt;
 };
 GradPlan grad_plan(const moe_linear_config& c, const moe_adapters* ad, int64_t T) {
@@ -198,7 +257,8 @@ GradPlan grad_plan(const moe_linear_config& c, const moe_adapters* ad, int64_t T
     p.ad = take(T * 4);
     p.offsets = take((n + 1) * 4);
     p.slot0 = take(n * 4);
-    p.n_chunks = take(4);
+    p.n_chunks = take(8);
+    p.runs = take(sizeof(AdaptChunk) * (size_t)adapt_max_runs(T, (int)n));
     p.chunks = take(sizeof(AdaptChunk) * (size_t)adapt_max_chunks(T, (int)n));
     p.h = take(T * R * 4);
     p.ht = take(p.ldt * R * 4);
@@ -206,7 +266,8 @@ GradPlan grad_plan(const moe_linear_config& c, const moe_adapters* ad, int64_t T
     p.ut = take(p.ldt * R * 4);
     p.at = take(n * R * K * 4);
     p.bt = take(n * R * N * 4);
-    p.part = take((size_t)kAdaptSlots * R * std::max(N, K) * 4);
+    p.part = take((size_t)kAdaptSlots * R * N * 4);
+    p.part_a = take((size_t)kAdaptSlots * R * K * 4);
   }
   p.total = at;
   return p;
@@ -248,10 +309,11 @@ hipError_t run(const moe_linear_config& c, const uint8_t* codes, const float* sc
   a.xl = reinterpret_cast<_Float16*>(w + p.z.xl);
   a.sh = i32(p.z.sh);
 
-  AdaptTable table{};
+  AdaptOrder order{};
   if (ad) {
-    table = AdaptTable{i32(p.offsets), i32(p.slot0), i32(p.n_chunks), reinterpret_cast<AdaptChunk*>(w + p.chunks)};
-    MOE_TRY(launch_adapt_order(ids, T, ad->n_adapters, i32(p.order), i32(p.ad), st, &table));
+    order = AdaptOrder{i32(p.order), i32(p.ad), i32(p.n_chunks) + 1, reinterpret_cast<AdaptChunk*>(w + p.runs),
+                       i32(p.offsets), i32(p.slot0), i32(p.n_chunks), reinterpret_cast<AdaptChunk*>(w + p.chunks)};
+    MOE_TRY(launch_adapt_order(ids, T, ad->n_adapters, order, st));
     a.order = i32(p.order);
     a.ad = i32(p.ad);
     a.n_ad = ad->n_adapters;
@@ -270,29 +332,30 @@ hipError_t run(const moe_linear_config& c, const uint8_t* codes, const float* sc
   if (dx || keep) {
     DzArgs d{a, dy, pre, ldd, ldp, vec(dy, ldd), vec(pre, ldp), N, c.act == MOE_ACT_SWIGLU ? N / 2 : 0, c.act,
              dx ? mul : nullptr, keep ? w + p.dz : nullptr};
-    k_linear_dz<TX><<<(T + 31) / 32 * 4, 8 * kPrepLanes, 0, st>>>(d);
+    if (c.act == MOE_ACT_NONE) dz_launch<TX, 0>(d, st);
+    else if (c.act == MOE_ACT_SWIGLU) dz_launch<TX, 2>(d, st);
+    else dz_launch<TX, 1>(d, st);
   }
   if (ad) {
     const void* m = keep ? w + p.dz : dy;  // dz, by position or by token
     const int64_t ldm = keep ? N : ldd;
     const int32_t* m_order = keep ? nullptr : a.order;
-    MOE_TRY(launch_adapt_transpose(ad->b, a.n_ad, N, a.R, elem, table.offsets, w + p.bt, st));
-    MOE_TRY(launch_adapt_down({m, ldm, vec(m, ldm), T, N, a.R, a.n_ad, m_order, a.ad, w + p.bt, ad->scale, f32(p.u),
-                               f32(p.ut), p.ldt}, dtype, st));
+    MOE_TRY(launch_adapt_transpose({a.n_ad, order.offsets, {{ad->b, N, a.R, w + p.bt}, {ad->a, a.R, K, dx ? w + p.at : nullptr}}},
+                                   elem, st));
+    AdaptDown down{T, a.R, a.n_ad, p.ldt, db ? 2 : 1, 0, a.ad, order.n_runs, order.runs, ad->scale, {}};
+    down.part[0] = {m, ldm, vec(m, ldm), N, m_order, w + p.bt, f32(p.u), f32(p.ut)};
+    down.part[1] = {x, ldx, vec(x, ldx), K, a.order, ad->a, f32(p.h), f32(p.ht)};
+    MOE_TRY(launch_adapt_down(down, dtype, st));
+    if (da || db) {
+      AdaptOuter outer{T, a.R, a.n_ad, p.ldt, order, {}};
+      outer.part[0] = {m, ldm, vec(m, ldm), N, 1, m_order, f32(p.h), f32(p.ht), f32(p.part), db};
+      outer.part[1] = {x, ldx, vec(x, ldx), K, 0, a.order, f32(p.u), f32(p.ut), f32(p.part_a), da};
+      MOE_TRY(launch_adapt_outer(outer, dtype, st));
+    }
     if (dx) {
-      MOE_TRY(launch_adapt_transpose(ad->a, a.n_ad, a.R, K, elem, table.offsets, w + p.at, st));
       a.h = f32(p.u);
       a.ab = w + p.at;
     }
-    if (db) {
-      MOE_TRY(launch_adapt_down({x, ldx, vec(x, ldx), T, K, a.R, a.n_ad, a.order, a.ad, ad->a, ad->scale, f32(p.h),
-                                 f32(p.ht), p.ldt}, dtype, st));
-      MOE_TRY(launch_adapt_outer({m, ldm, vec(m, ldm), T, N, a.R, a.n_ad, 1, m_order, f32(p.h), f32(p.ht), p.ldt, table,
-                                  f32(p.part), db}, dtype, st));
-    }
-    if (da)
-      MOE_TRY(launch_adapt_outer({x, ldx, vec(x, ldx), T, K, a.R, a.n_ad, 0, a.order, f32(p.u), f32(p.ut), p.ldt, table,
-                                  f32(p.part), da}, dtype, st));
   }
   if (dx) tiles_launch<TX>(a, c.weight_bits == 8 ? 8 : 4, st);
 #undef MOE_TRY

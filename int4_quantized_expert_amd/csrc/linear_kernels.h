@@ -532,7 +532,7 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int wt0, int t0, c
 constexpr int kTileRowGroup = 8, kDies = 8;
 template <class TX, int GSH>
 constexpr int base_frags() {  // 128 tokens need too many registers with two halves of them or a second set of sums
-  return std::is_same<TX, float>::value || GSH >= 0 ? 2 : 4;
+  return std::is_same<TX, float>::value || (GSH >= 0 && !kTransposed) ? 2 : 4;
 }
 
 template <class TX, int TT, int W, int GSH, int RW, int KW>

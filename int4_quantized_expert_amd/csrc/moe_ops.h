@@ -23,7 +23,7 @@ hipError_t launch_linear(const moe_linear_config& c, const uint8_t* codes, const
                          int64_t ldy, void* ws, hipStream_t st);
 
 // the same with adapters by token (ad may be NULL) and the values in front of the activation
-size_t adapted_ws_bytes(const moe_linear_config& c, int R, int64_t T);
+size_t adapted_ws_bytes(const moe_linear_config& c, const moe_adapters* ad, int64_t T);
 hipError_t launch_linear_adapted(const moe_linear_config& c, const uint8_t* codes, const float* scales, const float* bias,
                                  const moe_adapters* ad, const int32_t* ids, const void* x, int64_t ldx, int T, int dtype,
                                  const void* res, int64_t ldr, void* y, int64_t ldy, void* pre, int64_t ldp, void* ws,
@@ -36,54 +36,81 @@ hipError_t launch_linear_grad(const moe_linear_config& c, const uint8_t* codes, 
                               void* dx, int64_t ldg, void* da, void* db, void* ws, hipStream_t st);
 
 // ------------------------------------------------------------ adapters (k_adapt.hip)
-// A run of positions (tokens in the order of their adapters) of one adapter, for the gradients' sums over tokens.
+// A run of positions (tokens in the order of their adapters) of one adapter.
 struct AdaptChunk {
   int32_t e, p0, p1;
   int32_t slot;  // of the partial sums; -1: the adapter's only chunk
 };
-constexpr int kAdaptSlots = 32;  // cnt > len gives at most 2 cnt / len chunks, and T / len is at most 16
-inline int adapt_chunk_len(int64_t T) { return (int)((T + 4095) / 4096 * 256); }  // at most 16 chunks of T positions
-inline int64_t adapt_max_chunks(int64_t T, int n) { return T / adapt_chunk_len(T) + (T < n ? T : n) + 1; }
-// What the gradients need beside the order of the positions.
-struct AdaptTable {
+// Runs of 16 positions for the products, and chunks for the gradients' sums over tokens: T positions make at most 16 of
+// the latter, and adapters of several chunks have at most kAdaptSlots together (count > len gives at most 2 count / len).
+constexpr int kAdaptSlots = 32;
+inline int adapt_chunk_len(int64_t T) { return T <= 1024 ? 64 : (int)((T + 511) / 512 * 32); }
+inline int64_t adapt_max_chunks(int64_t T, int n) { return 16 + (T < n ? T : n); }
+inline int64_t adapt_max_runs(int64_t T, int n) { return T / 16 + (T < n ? T : n); }
+struct AdaptOrder {
+  int32_t* order;  // [T] token of a position
+  int32_t* ad;     // [T] its adapter, -1: none
+  int32_t* n_runs;
+  AdaptChunk* runs;
+  // for the gradients, or nullptr
   int32_t* offsets;  // [n + 1] first position of each adapter, and of the tokens without one
   int32_t* slot0;    // [n] first partial sum of an adapter of several chunks
   int32_t* n_chunks;
   AdaptChunk* chunks;
 };
-hipError_t launch_adapt_order(const int32_t* ids, int T, int n_ad, int32_t* order, int32_t* pos_ad, hipStream_t st,
-                              const AdaptTable* table = nullptr);
-// h[p][r] = scale * sum over c of x[order[p]][c] a[ad[p]][r][c], 0 without an adapter; ht, where given, the same as [R][ldt]
+hipError_t launch_adapt_order(const int32_t* ids, int T, int n_ad, const AdaptOrder& out, hipStream_t st);
+// Whether s (A x) takes a workgroup for a token and four rows (no order needed), or one for a run of 16 positions.
+inline bool adapt_few(int64_t T, int R) { return T * R <= 4096; }
+// h[p][r] = scale * sum over c of x[order[p]][c] a[ad[p]][r][c], 0 without an adapter; ht, where given, the same as
+// [R][ldt]; two such products in one launch
 struct AdaptDown {
-  const void* x;
-  int64_t ldx;
-  int32_t vec_x, T, C, R, n_ad;
-  const int32_t* order;
+  struct Part {
+    const void* x;
+    int64_t ldx;
+    int32_t vec_x, C;
+    const int32_t* order;
+    const void* a;
+    float* h;
+    float* ht;
+  };
+  int32_t T, R, n_ad, ldt, parts;
+  int32_t by_token;  // rows of h are tokens
   const int32_t* ad;
-  const void* a;
+  const int32_t* n_runs;  // not adapt_few: the order's runs, nullptr: adapter 0 for all
+  const AdaptChunk* runs;
   const float* scale;
-  float* h;
-  float* ht;
-  int32_t ldt;
+  Part part[2];
 };
 hipError_t launch_adapt_down(const AdaptDown& a, int dtype, hipStream_t st);
-// out[e] = sum over e's positions of v[p][r] m[p][c]: [n][R][C], or with `rows` [n][C][R]
+// out[e] = sum over e's positions of v[p][r] m[p][c]: [n][R][C], or with `rows` [n][C][R]; out NULL: not wanted
 struct AdaptOuter {
-  const void* m;
-  int64_t ldm;
-  int32_t vec_m, T, C, R, n_ad, rows;
-  const int32_t* order;  // rows of m, nullptr: m's rows are positions
-  const float* v;
-  const float* vt;
-  int32_t ldt;
-  AdaptTable table;
-  float* part;  // [kAdaptSlots][R][C]
-  void* out;
+  struct Part {
+    const void* m;
+    int64_t ldm;
+    int32_t vec_m, C, rows;
+    const int32_t* order;  // rows of m, nullptr: m's rows are positions
+    const float* v;
+    const float* vt;
+    float* part;  // [kAdaptSlots][R][C]
+    void* out;
+  };
+  int32_t T, R, n_ad, ldt;
+  AdaptOrder order;
+  Part part[2];
 };
 hipError_t launch_adapt_outer(const AdaptOuter& a, int dtype, hipStream_t st);
-// out [n][Q][M] = in [n][M][Q] transposed, for the adapters that tokens have
-hipError_t launch_adapt_transpose(const void* in, int n, int M, int Q, int elem, const int32_t* offsets, void* out,
-                                  hipStream_t st);
+// out [n][Q][M] = in [n][M][Q] transposed, for the adapters that tokens have; out NULL: not wanted
+struct AdaptTranspose {
+  struct Part {
+    const void* in;
+    int32_t M, Q;
+    void* out;
+  };
+  int32_t n_ad;
+  const int32_t* offsets;
+  Part part[2];
+};
+hipError_t launch_adapt_transpose(const AdaptTranspose& a, int elem, hipStream_t st);
 
 // ------------------------------------------------------------ gradients' norm (k_clip.hip)
 int64_t clip_chunks(const moe_grad* g, int count);

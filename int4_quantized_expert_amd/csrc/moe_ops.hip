@@ -193,7 +193,7 @@ int32_t moe_linear(const moe_linear_config* cfg, const uint8_t* codes, const flo
 
 size_t moe_linear_adapted_workspace_bytes(const moe_linear_config* cfg, const moe_adapters* adapters, int32_t max_tokens) {
   if (check_linear(cfg) != MOE_OK || check_adapters(adapters) != MOE_OK || !tokens_ok(max_tokens)) return 0;
-  return adapted_ws_bytes(*cfg, adapters ? adapters->rank : 0, max_tokens);
+  return adapted_ws_bytes(*cfg, adapters, max_tokens);
 }
 
 int32_t moe_linear_adapted(const moe_linear_config* cfg, const uint8_t* codes, const float* scales, const float* bias,
@@ -211,7 +211,7 @@ int32_t moe_linear_adapted(const moe_linear_config* cfg, const uint8_t* codes, c
   if (!elem_aligned(x, dtype) || !elem_aligned(residual, dtype) || !elem_aligned(y, dtype) || !elem_aligned(pre, dtype))
     return MOE_E_ARG;
   if ((rc = check_adapter_arrays(adapters, ids))) return rc;
-  if ((rc = check_space(ws, ws_bytes, adapted_ws_bytes(*cfg, adapters ? adapters->rank : 0, T)))) return rc;
+  if ((rc = check_space(ws, ws_bytes, adapted_ws_bytes(*cfg, adapters, T)))) return rc;
   return done(launch_linear_adapted(*cfg, codes, scales, bias, adapters, ids, x, ldx, T, dtype, residual, ldr, y, ldy, pre,
                                     ldp, ws, stream));
 }
