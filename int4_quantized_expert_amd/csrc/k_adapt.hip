@@ -1,5 +1,7 @@
 // k_adapt.hip — low-rank adapters beside a product over weight codes: the first half s (A x) of what a token's adapter adds,
 // the order of the tokens by adapter, and the gradients of A and B.
+#include <algorithm>
+
 #include "linear_types.h"
 
 namespace moe {
@@ -145,7 +147,7 @@ __device__ __forceinline__ int adapter_of(const AdaptDown& a, int p) {
 }
 __device__ __forceinline__ void put_h(const AdaptDown& a, const AdaptDown::Part& d, int p, int r, float v) {
   d.h[(size_t)p * a.R + r] = v;
-  if (d.ht) d.ht[(size_t)r * a.ldt + p] = v;
+  if (d.ht) d.ht[((size_t)(p >> 3) * a.R + r) * 8 + (p & 7)] = v;
 }
 
 // Few tokens: a workgroup takes a token and 4 rows of its A; its lanes share the columns, all loads in flight at once.
@@ -188,49 +190,40 @@ __global__ __launch_bounds__(256) void k_adapt_dot(AdaptDown a) {
   }
 }
 
-// More: a run of up to 16 positions of one adapter and 16 RF rows a workgroup. Eight wavefronts share the columns; a lane
-// takes 32 bytes of its row at a time, so that four lanes read whole cache lines, and the next columns are on their way
-// while these are multiplied. fp32 is multiplied in fp32, the others in their type, which is exact.
+// More: a run of up to 16 positions of one adapter and 16 RF rows a workgroup; its wavefronts share the columns, each with
+// the loads of several steps (128 bytes of every row) in flight. Eight neighbouring lanes load a row's 128 bytes; the
+// operands, a row a lane, come from LDS: loaded in the operands' order, where neighbouring lanes are in different rows, a
+// load takes four times as long (14 us for any number of runs up to 128, rows of 6144 bf16). fp32 is multiplied in fp32,
+// the others in their type, which is exact.
 constexpr int kDownWaves = 8;
 template <class TX>
-struct Pair {  // 32 bytes: 16 elements (fp32: 8)
-  u4v v[2];
-};
-template <class TX>
-__device__ __forceinline__ Pair<TX> load_pair(const TX* p, bool vec) {
-  Pair<TX> d;
-  if (vec) {
-    d.v[0] = reinterpret_cast<const u4v*>(p)[0];
-    d.v[1] = reinterpret_cast<const u4v*>(p)[1];
-  } else {
-    TX t[32 / sizeof(TX)];
+__device__ __forceinline__ u4v load_16(const TX* p, bool vec) {
+  if (vec) return *reinterpret_cast<const u4v*>(p);
+  TX t[16 / sizeof(TX)];
 #pragma unroll
-    for (int i = 0; i < (int)(32 / sizeof(TX)); ++i) t[i] = p[i];
-    __builtin_memcpy(&d, t, 32);
-  }
-  return d;
+  for (int i = 0; i < (int)(16 / sizeof(TX)); ++i) t[i] = p[i];
+  return __builtin_bit_cast(u4v, t);
 }
 template <class TX>
-__device__ __forceinline__ f4 mul_pair(const Pair<TX>& x, const Pair<TX>& w, f4 c) {
+__device__ __forceinline__ f4 mul_16(const u4v& x, const u4v& w, f4 c) {
+  if constexpr (std::is_same<TX, float>::value) {
+    const f4 xv = __builtin_bit_cast(f4, x), wv = __builtin_bit_cast(f4, w);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if constexpr (std::is_same<TX, float>::value) {
-      const f4 xv = __builtin_bit_cast(f4, x.v[h]), wv = __builtin_bit_cast(f4, w.v[h]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(xv[j], wv[j], c, 0, 0, 0);
-    } else if constexpr (std::is_same<TX, bf16_t>::value) {
-      c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, x.v[h]), __builtin_bit_cast(b8, w.v[h]), c, 0, 0, 0);
-    } else {
-      c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, x.v[h]), __builtin_bit_cast(h8, w.v[h]), c, 0, 0, 0);
-    }
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(xv[j], wv[j], c, 0, 0, 0);
+    return c;
+  } else if constexpr (std::is_same<TX, bf16_t>::value) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, x), __builtin_bit_cast(b8, w), c, 0, 0, 0);
+  } else {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, x), __builtin_bit_cast(h8, w), c, 0, 0, 0);
   }
-  return c;
 }
 
 template <class TX, int RF>
-__global__ __launch_bounds__(64 * kDownWaves, 2) void k_adapt_down(AdaptDown a) {
-  __shared__ float s_sum[kDownWaves][16][16 * RF + 4];
-  constexpr int kLane = 32 / sizeof(TX), kStep = 4 * kLane, U = RF == 1 ? 4 : 2;  // columns of a lane, of a step; steps ahead
+__global__ __launch_bounds__(64 * kDownWaves, 4) void k_adapt_down(AdaptDown a) {
+  constexpr int kChunk = 16 / sizeof(TX), kStep = 8 * kChunk, U = RF == 1 ? 4 : 3;  // columns; steps at once
+  constexpr int kSum = 16 * RF + 4;
+  // a wavefront's rows of a step, [1 + RF][16][128 bytes], later the sums, [wavefronts][16][kSum]
+  __shared__ __align__(16) char s_mem[std::max<size_t>((size_t)kDownWaves * (1 + RF) * 2048, sizeof(float) * kDownWaves * 16 * kSum)];
   const AdaptDown::Part& d = a.part[blockIdx.z];
   AdaptChunk run{0, (int)blockIdx.x * 16, min((int)blockIdx.x * 16 + 16, a.T), 0};  // one adapter for all
   if (a.runs) {
@@ -238,59 +231,73 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_adapt_down(AdaptDown a) 
     run = a.runs[blockIdx.x];
   }
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, g = lane >> 4;
-  const int p = min(run.p0 + i, run.p1 - 1), r0 = blockIdx.y * 16 * RF, rows = min(16 * RF, a.R - r0);
-  const TX* x = static_cast<const TX*>(d.x) + (size_t)(d.order ? d.order[p] : p) * d.ldx + g * kLane;
+  const int r0 = blockIdx.y * 16 * RF, rows = min(16 * RF, a.R - r0);
   const int steps = (d.C + kStep - 1) / kStep, per = (steps + kDownWaves - 1) / kDownWaves;
   const int s0 = min(wave * per, steps), s1 = min(s0 + per, steps);
-  const TX* w[RF];
+  // lane: row lane / 8 (and 8 more), chunk lane % 8, which goes to place chunk ^ row % 8, so that no two lanes that read
+  // at a time meet in a bank
+  const int chunk = (lane & 7) ^ (lane >> 3);
+  const TX* x[2];
+  const TX* w[RF][2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int q = 8 * k + (lane >> 3), p = min(run.p0 + q, run.p1 - 1);
+    x[k] = static_cast<const TX*>(d.x) + (size_t)(d.order ? d.order[p] : p) * d.ldx + chunk * kChunk;
+#pragma unroll
+    for (int f = 0; f < RF; ++f)
+      w[f][k] = static_cast<const TX*>(d.a) + ((size_t)run.e * a.R + r0 + min(16 * f + q, rows - 1)) * d.C + chunk * kChunk;
+  }
   f4 acc[RF];
 #pragma unroll
-  for (int f = 0; f < RF; ++f) {
-    w[f] = static_cast<const TX*>(d.a) + ((size_t)run.e * a.R + r0 + min(16 * f + i, rows - 1)) * d.C + g * kLane;
-    acc[f] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-  Pair<TX> xn[U], wn[RF][U];
-  auto fetch = [&](int s) __attribute__((always_inline)) {
+  for (int f = 0; f < RF; ++f) acc[f] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+  u4v* s_row = reinterpret_cast<u4v*>(s_mem) + wave * (1 + RF) * 128;
+  for (int s = s0; s < s1; s += U) {
+    u4v xv[U][2], wv[U][RF][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool in = s + u < s1 && (s + u) * kStep + g * kLane < d.C;  // 16-bit columns may end at half a step
-      xn[u] = Pair<TX>{};
+      const int at = min(s + u, s1 - 1) * kStep, c = at + chunk * kChunk < d.C ? at : -chunk * kChunk;  // they may end at half a step
 #pragma unroll
-      for (int f = 0; f < RF; ++f) wn[f][u] = Pair<TX>{};
-      if (in) {
-        xn[u] = load_pair(x + (s + u) * kStep, d.vec_x);
+      for (int k = 0; k < 2; ++k) {
+        xv[u][k] = load_16(x[k] + c, d.vec_x);
 #pragma unroll
-        for (int f = 0; f < RF; ++f) wn[f][u] = load_pair(w[f] + (s + u) * kStep, true);
+        for (int f = 0; f < RF; ++f) wv[u][f][k] = load_16(w[f][k] + c, true);
       }
     }
-  };
-  fetch(s0);
-  for (int s = s0; s < s1; s += U) {
-    Pair<TX> xc[U], wc[RF][U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      xc[u] = xn[u];
+      if (s + u >= s1) break;
 #pragma unroll
-      for (int f = 0; f < RF; ++f) wc[f][u] = wn[f][u];
+      for (int k = 0; k < 2; ++k) {
+        s_row[64 * k + lane] = xv[u][k];
+#pragma unroll
+        for (int f = 0; f < RF; ++f) s_row[128 * (1 + f) + 64 * k + lane] = wv[u][f][k];
+      }
+      wave_sync();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if ((s + u) * kStep + 4 * h * kChunk >= d.C) break;
+        const int from = i * 8 + ((4 * h + g) ^ (i & 7));
+        const u4v xf = s_row[from];
+#pragma unroll
+        for (int f = 0; f < RF; ++f) acc[f] = mul_16<TX>(xf, s_row[128 * (1 + f) + from], acc[f]);
+      }
+      wave_sync();
     }
-    fetch(s + U);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int f = 0; f < RF; ++f) acc[f] = mul_pair<TX>(xc[u], wc[f][u], acc[f]);
   }
   // sum j of a lane: position 4 g + j, row l % 16
+  __syncthreads();
+  float* s_sum = reinterpret_cast<float*>(s_mem);
 #pragma unroll
   for (int f = 0; f < RF; ++f)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s_sum[wave][4 * g + j][16 * f + i] = acc[f][j];
+    for (int j = 0; j < 4; ++j) s_sum[(wave * 16 + 4 * g + j) * kSum + 16 * f + i] = acc[f][j];
   __syncthreads();
   const float scale = a.scale[run.e];
   for (int k = tid; k < (run.p1 - run.p0) * rows; k += 64 * kDownWaves) {
     const int q = k / rows, r = k % rows, at = run.p0 + q;
-    float v = s_sum[0][q][r];
+    float v = s_sum[q * kSum + r];
 #pragma unroll
-    for (int u = 1; u < kDownWaves; ++u) v += s_sum[u][q][r];
+    for (int u = 1; u < kDownWaves; ++u) v += s_sum[(u * 16 + q) * kSum + r];
     put_h(a, d, a.by_token && d.order ? d.order[at] : at, r0 + r, scale * v);
   }
 }
@@ -300,7 +307,8 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_adapt_down(AdaptDown a) 
 // 128 columns and a run of positions, a workgroup four of them; both gradients in one launch. Positions are what is
 // summed over, and neither m nor v has neighbouring ones in memory: a lane loads 8 columns of each of 8 positions and
 // exchanges halves of words between two positions, which gives the operands of 8 products (column l + j of every eight
-// columns in product j). v is read transposed. As in the product's epilogue v has two bf16 parts, bf16 m one and fp16 m
+// columns in product j). v comes with eight
+// positions of a row next to each other. As in the product's epilogue v has two bf16 parts, bf16 m one and fp16 m
 // two. fp32 is multiplied as it is, 4 columns a lane.
 __device__ __forceinline__ size_t outer_at(const AdaptOuter& a, const AdaptOuter::Part& d, int e, int r, int c) {
   return d.rows ? ((size_t)e * d.C + c) * a.R + r : ((size_t)e * a.R + r) * d.C + c;
@@ -319,7 +327,8 @@ __device__ __forceinline__ void outer_16(const AdaptOuter& a, const AdaptOuter::
     for (int k = 0; k < 8; ++k) acc[f][k] = f4{0.0f, 0.0f, 0.0f, 0.0f};
   const float* vt[RF];
 #pragma unroll
-  for (int f = 0; f < RF; ++f) vt[f] = d.vt + (size_t)min(r0 + 16 * f + i, a.R - 1) * a.ldt;
+  for (int f = 0; f < RF; ++f) vt[f] = d.vt + (size_t)min(r0 + 16 * f + i, a.R - 1) * 8;
+  const int begin = ch.p0 & ~7, last = (ch.p1 - 1) & ~7;
   Granule<TX> mn[8];
   f8v vn[RF];
   int row[8];  // rows of m two steps ahead
@@ -338,9 +347,8 @@ __device__ __forceinline__ void outer_16(const AdaptOuter& a, const AdaptOuter::
       if (in && t0 + j >= ch.p0 && t0 + j < ch.p1) load8(static_cast<const TX*>(d.m) + (size_t)row[j] * d.ldm + c0, d.vec_m, mn[j]);
     }
 #pragma unroll
-    for (int f = 0; f < RF; ++f) vn[f] = *reinterpret_cast<const f8v*>(vt[f] + min(t0, a.ldt - 8));
+    for (int f = 0; f < RF; ++f) vn[f] = *reinterpret_cast<const f8v*>(vt[f] + (size_t)min(t0, last) * a.R);
   };
-  const int begin = ch.p0 & ~7;
   rows_of(begin);
   fetch(begin);
   rows_of(begin + 32);

@@ -6,6 +6,13 @@
 
 namespace moe {
 
+namespace {
+size_t slim_bytes(int N, int K, int64_t T) {
+  const SlimPlan s = slim_plan(N, K / 32, slim_frags(T), T);
+  return s.parts > 1 ? (size_t)s.parts * T * N * 4 : 0;
+}
+}  // namespace
+
 // for any number of tokens up to T
 size_t linear_ws_bytes(const moe_linear_config& c, int64_t T) {
   size_t b = is_slim(T, c.rows) ? 256 : linear_plan(c.cols, T).total;

@@ -235,7 +235,6 @@ __global__ __launch_bounds__(256) void k_group_scales(const float* __restrict__ 
 struct GradPlan {
   LinearPlan z;
   size_t mul, gs, dz, order, ad, offsets, slot0, n_chunks, runs, chunks, h, ht, u, ut, at, bt, part, part_a, total;
-  int ldt;
 };
 GradPlan grad_plan(const moe_linear_config& c, const moe_adapters* ad, int64_t T) {
   GradPlan p;
@@ -249,7 +248,6 @@ GradPlan grad_plan(const moe_linear_config& c, const moe_adapters* ad, int64_t T
   const size_t groups = c.group_size > 0 ? c.cols / c.group_size : 0;
   p.mul = take(groups ? (size_t)c.rows * 4 : 0);
   p.gs = take(groups * c.rows * 4);
-  p.ldt = (int)((T + 7) & ~7);
   if (ad) {
     const size_t R = ad->rank, n = ad->n_adapters, N = c.rows, K = c.cols;
     p.dz = take(c.act != MOE_ACT_NONE ? T * N * 4 : 0);
@@ -261,9 +259,9 @@ GradPlan grad_plan(const moe_linear_config& c, const moe_adapters* ad, int64_t T
     p.runs = take(sizeof(AdaptChunk) * (size_t)adapt_max_runs(T, (int)n));
     p.chunks = take(sizeof(AdaptChunk) * (size_t)adapt_max_chunks(T, (int)n));
     p.h = take(T * R * 4);
-    p.ht = take(p.ldt * R * 4);
+    p.ht = take((T + 7) / 8 * 8 * R * 4);
     p.u = take(T * R * 4);
-    p.ut = take(p.ldt * R * 4);
+    p.ut = take((T + 7) / 8 * 8 * R * 4);
     p.at = take(n * R * K * 4);
     p.bt = take(n * R * N * 4);
     p.part = take((size_t)kAdaptSlots * R * N * 4);
@@ -342,12 +340,12 @@ hipError_t run(const moe_linear_config& c, const uint8_t* codes, const float* sc
     const int32_t* m_order = keep ? nullptr : a.order;
     MOE_TRY(launch_adapt_transpose({a.n_ad, order.offsets, {{ad->b, N, a.R, w + p.bt}, {ad->a, a.R, K, dx ? w + p.at : nullptr}}},
                                    elem, st));
-    AdaptDown down{T, a.R, a.n_ad, p.ldt, db ? 2 : 1, 0, a.ad, order.n_runs, order.runs, ad->scale, {}};
+    AdaptDown down{T, a.R, a.n_ad, db ? 2 : 1, 0, a.ad, order.n_runs, order.runs, ad->scale, {}};
     down.part[0] = {m, ldm, vec(m, ldm), N, m_order, w + p.bt, f32(p.u), f32(p.ut)};
     down.part[1] = {x, ldx, vec(x, ldx), K, a.order, ad->a, f32(p.h), f32(p.ht)};
     MOE_TRY(launch_adapt_down(down, dtype, st));
     if (da || db) {
-      AdaptOuter outer{T, a.R, a.n_ad, p.ldt, order, {}};
+      AdaptOuter outer{T, a.R, a.n_ad, order, {}};
       outer.part[0] = {m, ldm, vec(m, ldm), N, 1, m_order, f32(p.h), f32(p.ht), f32(p.part), db};
       outer.part[1] = {x, ldx, vec(x, ldx), K, 0, a.order, f32(p.u), f32(p.ut), f32(p.part_a), da};
       MOE_TRY(launch_adapt_outer(outer, dtype, st));

@@ -89,13 +89,6 @@ constexpr size_t tile_lds() {
                            (size_t)(KW / 2) * RW * 8 * 1024, (size_t)16 * kOutRow * 4});
 }
 
-// Orders a wavefront's LDS writes before its later reads of other lanes' data.
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // ------------------------------------------------------------ adapters of a fragment
 // Column that the sums' position j of a fragment stands for: transposed int8 codes keep the order of a row's bytes, in
 // each eight the even elements and then the odd ones.
@@ -1036,11 +1029,6 @@ SlimPlan slim_plan(int N, int nb, int nt, int64_t T) {
   const int per = std::min((quads + parts - 1) / parts, most);
   parts = (quads + per - 1) / per;
   return {per * 4, parts};
-}
-
-size_t slim_bytes(int N, int K, int64_t T) {
-  const SlimPlan s = slim_plan(N, K / 32, slim_frags(T), T);
-  return s.parts > 1 ? (size_t)s.parts * T * N * 4 : 0;
 }
 
 template <class TX, int TOK, int F, int W, int GSH>

@@ -61,8 +61,8 @@ struct AdaptOrder {
 hipError_t launch_adapt_order(const int32_t* ids, int T, int n_ad, const AdaptOrder& out, hipStream_t st);
 // Whether s (A x) takes a workgroup for a token and four rows (no order needed), or one for a run of 16 positions.
 inline bool adapt_few(int64_t T, int R) { return T * R <= 4096; }
-// h[p][r] = scale * sum over c of x[order[p]][c] a[ad[p]][r][c], 0 without an adapter; ht, where given, the same as
-// [R][ldt]; two such products in one launch
+// h[p][r] = scale * sum over c of x[order[p]][c] a[ad[p]][r][c] for positions with an adapter; ht, where given, the same as
+// [T / 8][R][8]; two such products in one launch
 struct AdaptDown {
   struct Part {
     const void* x;
@@ -73,7 +73,7 @@ struct AdaptDown {
     float* h;
     float* ht;
   };
-  int32_t T, R, n_ad, ldt, parts;
+  int32_t T, R, n_ad, parts;
   int32_t by_token;  // rows of h are tokens
   const int32_t* ad;
   const int32_t* n_runs;  // not adapt_few: the order's runs, nullptr: adapter 0 for all
@@ -94,7 +94,7 @@ struct AdaptOuter {
     float* part;  // [kAdaptSlots][R][C]
     void* out;
   };
-  int32_t T, R, n_ad, ldt;
+  int32_t T, R, n_ad;
   AdaptOrder order;
   Part part[2];
 };
