@@ -8,7 +8,7 @@ namespace moe {
 
 namespace {
 
-typedef float f4 __attribute__((ext_vector_type(4)));
+typedef f4v f4;
 
 // ------------------------------------------------------------ order by adapter
 // Positions: the tokens of adapter 0, of adapter 1, ..., those without one; ascending tokens in each. One workgroup: each

@@ -7,6 +7,7 @@
 namespace moe {
 
 namespace {
+int slim_frags(int64_t T) { return T <= 16 ? 1 : 2; }
 size_t slim_bytes(int N, int K, int64_t T) {
   const SlimPlan s = slim_plan(N, K / 32, slim_frags(T), T);
   return s.parts > 1 ? (size_t)s.parts * T * N * 4 : 0;

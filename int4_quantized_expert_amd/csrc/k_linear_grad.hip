@@ -234,7 +234,7 @@ __global__ __launch_bounds__(256) void k_group_scales(const float* __restrict__ 
 // ------------------------------------------------------------ the whole
 struct GradPlan {
   LinearPlan z;
-  size_t mul, gs, dz, order, ad, offsets, slot0, n_chunks, runs, chunks, h, ht, u, ut, at, bt, part, part_a, total;
+  size_t mul, gs, sums, dz, order, ad, offsets, slot0, n_chunks, runs, chunks, h, ht, u, ut, at, bt, part, part_a, total;
 };
 GradPlan grad_plan(const moe_linear_config& c, const moe_adapters* ad, int64_t T) {
   GradPlan p;
@@ -248,6 +248,7 @@ GradPlan grad_plan(const moe_linear_config& c, const moe_adapters* ad, int64_t T
   const size_t groups = c.group_size > 0 ? c.cols / c.group_size : 0;
   p.mul = take(groups ? (size_t)c.rows * 4 : 0);
   p.gs = take(groups * c.rows * 4);
+  p.sums = take(tile_sums_bytes(c.cols, c.rows / 64, T));
   if (ad) {
     const size_t R = ad->rank, n = ad->n_adapters, N = c.rows, K = c.cols;
     p.dz = take(c.act != MOE_ACT_NONE ? T * N * 4 : 0);
@@ -355,7 +356,7 @@ hipError_t run(const moe_linear_config& c, const uint8_t* codes, const float* sc
       a.ab = w + p.at;
     }
   }
-  if (dx) tiles_launch<TX>(a, c.weight_bits == 8 ? 8 : 4, st);
+  if (dx) tiles_launch<TX>(a, c.weight_bits == 8 ? 8 : 4, f32(p.sums), st);
 #undef MOE_TRY
   return hipGetLastError();
 }

@@ -175,8 +175,10 @@ __device__ __forceinline__ void adapter_frags(const LinearArgs& a, int p0, const
 
 // KW groups of RW wavefronts: a group's wavefronts take 64 rows each, from wavefront tile wt0 on, the groups share the
 // columns.
+// Transposed: part `part` of `parts` of the sum goes to `sums` [tokens of the tile][256 columns] where there are several.
 template <class TX, int TT, int W, int GSH, int RW, int KW>
-__device__ __forceinline__ void tile_run(const LinearArgs& a, int wt0, int t0, char* s_mem) {
+__device__ __forceinline__ void tile_run(const LinearArgs& a, int wt0, int t0, char* s_mem, int part = 0, int parts = 1,
+                                         float* sums = nullptr) {
   constexpr int NX = std::is_same<TX, float>::value ? 2 : 1;
   constexpr int kStep = NX * TT * 2048;  // halfs of a step: [NX][TT][2 blocks][4 slices][32][8]
   // values that are equal in a wavefront are made so for the compiler: addresses are then a scalar base and a lane's
@@ -186,7 +188,9 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int wt0, int t0, c
   const int lane = threadIdx.x & 63, wave = wv % RW, r = lane & 31, g = lane >> 5;
   const int kw = wv / RW, tid = threadIdx.x % kLanes;
   auto s_x = reinterpret_cast<_Float16(*)[kStep]>(s_mem) + kw * 2;
-  const int steps = (a.nbp / 2 + KW - 1) / KW, p0 = min(kw * steps, a.nbp / 2), p1 = min(p0 + steps, a.nbp / 2);
+  const int from = kTransposed ? (int)((int64_t)(a.nbp / 2) * part / parts) : 0;
+  const int to = kTransposed ? (int)((int64_t)(a.nbp / 2) * (part + 1) / parts) : a.nbp / 2;
+  const int steps = (to - from + KW - 1) / KW, p0 = min(from + kw * steps, to), p1 = min(p0 + steps, to);
   const int cols = a.half ? a.half / 32 : (a.N + 63) / 64;  // wavefront tiles over the outputs
   const int wtc = min(wt0 + wave, cols - 1);
   int first[2];  // first weight row (transposed: column) of a fragment
@@ -491,7 +495,7 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int wt0, int t0, c
       for (int f = 0; f < 2; ++f)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[tt][f][i] *= rs[f];
-      if (a.h && kw == 0 && t0 + 32 * tt < a.T) {
+      if (a.h && kw == 0 && part == 0 && t0 + 32 * tt < a.T) {
         adapter_frags<TX>(a, t0 + 32 * tt, row, lane, d);
 #pragma unroll
         for (int f = 0; f < 2; ++f) acc[tt][f] += d[f];
@@ -510,7 +514,12 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int wt0, int t0, c
       __syncthreads();
       for (int k = threadIdx.x; k < 16 * quads; k += kLanes * KW) {
         const int tk = k / quads, c = k % quads * 4, t = t0 + 32 * tt + 16 * hh + tk;
-        if (t < a.T && col0 + c < out)
+        if (kTransposed && sums) {
+          f4v v = *reinterpret_cast<const f4v*>(s_out + tk * kOutRow + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = ldexpf(v[i], t < a.T ? -a.sh[t] : 0);
+          *reinterpret_cast<f4v*>(sums + (size_t)(32 * tt + 16 * hh + tk) * 256 + c) = v;
+        } else if (t < a.T && col0 + c < out)
           finish4<TX>(a, token_of(a, t), col0 + c, -a.sh[t], s_out + tk * kOutRow + c,
                       s_out + tk * kOutRow + 32 * RW + c);
       }
@@ -525,13 +534,18 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int wt0, int t0, c
 constexpr int kTileRowGroup = 8, kDies = 8;
 template <class TX, int GSH>
 constexpr int base_frags() {  // 128 tokens need too many registers with two halves of them or a second set of sums
-  return std::is_same<TX, float>::value || (GSH >= 0 && !kTransposed) ? 2 : 4;
+  return std::is_same<TX, float>::value || GSH == 0 || (GSH > 0 && !kTransposed) ? 2 : 4;
 }
 
+// Transposed: the sum over the rows in n parts, [n][tiles of the launch][32 * BT tokens][256 columns], added by k_linear_add.
+struct TileParts {
+  int32_t n;
+  float* sums;
+};
 template <class TX, int TT, int W, int GSH, int RW, int KW>
 __global__ __launch_bounds__(64 * RW * KW, RW * KW == 16 ? 4 : 2) void k_linear_tile(LinearArgs a, int row_tiles,
                                                                                      int tok_tiles, int first,
-                                                                                     int count) {
+                                                                                     int count, TileParts parts) {
   constexpr int BT = base_frags<TX, GSH>(), kToks = BT / TT, kRows = 4 / RW;  // the cut of a tile
   __shared__ __align__(16) char s_mem[tile_lds<TX, TT, W, RW, KW>()];
   const int n = count * kToks * kRows, d = blockIdx.x % kDies, q = n / kDies, m = n % kDies;
@@ -540,7 +554,14 @@ __global__ __launch_bounds__(64 * RW * KW, RW * KW == 16 ? 4 : 2) void k_linear_
   const int rows_in = min(kTileRowGroup, row_tiles - group * kTileRowGroup);
   const int t0 = in_group / rows_in * 32 * BT + k % kToks * 32 * TT;
   const int wt0 = (group * kTileRowGroup + in_group % rows_in) * 4 + k / kToks % kRows * RW;
-  if (t0 < a.T && wt0 * (a.half ? 32 : 64) < (a.half ? a.half : a.N)) tile_run<TX, TT, W, GSH, RW, KW>(a, wt0, t0, s_mem);
+  if (t0 >= a.T || wt0 * (a.half ? 32 : 64) >= (a.half ? a.half : a.N)) return;
+  if constexpr (kTransposed) {
+    const int part = blockIdx.y;
+    float* sums = parts.n > 1 ? parts.sums + ((size_t)(part * count + id - first) * 32 * BT + t0 % (32 * BT)) * 256 : nullptr;
+    tile_run<TX, TT, W, GSH, RW, KW>(a, wt0, t0, s_mem, part, parts.n, sums);
+  } else {
+    tile_run<TX, TT, W, GSH, RW, KW>(a, wt0, t0, s_mem);
+  }
 }
 
 #if !MOE_TRANSPOSED
@@ -555,8 +576,6 @@ __global__ __launch_bounds__(64 * RW * KW, RW * KW == 16 ? 4 : 2) void k_linear_
 // Activations are converted in LDS, order [blocks][4 slices][tokens][8], each token multiplied by a power of two of its
 // own. Their loads are issued ahead of the codes' (loads return in order) and stay in registers while the largest is
 // found.
-typedef float f4v __attribute__((ext_vector_type(4)));
-
 __device__ __forceinline__ void transpose4(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
   auto s = __builtin_amdgcn_permlane32_swap(a, c, false, false);
   a = s[0], c = s[1];
@@ -1015,7 +1034,6 @@ bool tiny_fits(int64_t T, int K, int size) {
   return T <= kTinyTokens && per * 16 * tok <= tiny_rounds(size) * 64 &&
          kTinyWaves * per * 256 * tok * (size == 4 ? 2 : 1) <= 64 << 10;
 }
-int slim_frags(int64_t T) { return T <= 16 ? 1 : 2; }
 
 // Columns are cut so that about kSlimGroups workgroups run, in parts of whole quads of blocks that the lanes' rounds
 // cover.
@@ -1078,31 +1096,30 @@ void few_tokens(const LinearArgs& a, float* ws, hipStream_t st) {
 // tiles of group scales 384 of them 88 / 87, 192 52.7 / 63.9, 96 39.1 / 50.9, 48 25.6 / 38.5, of fp32 111 / 119, 77 / 75,
 // 42 / 74, 30 / 40.
 constexpr int kUnits = 256;
+#if !MOE_TRANSPOSED
 template <class TX, int W, int GSH>
-void tile_launch(const LinearArgs& a, hipStream_t st) {
-  // transposed fp32: the codes' LDS leaves room for half as many column groups
-  constexpr int BT = base_frags<TX, GSH>(),
-                KQ = GSH >= 0 || (kTransposed && std::is_same<TX, float>::value) ? 2 : 4;
+void tile_launch(const LinearArgs& a, float*, hipStream_t st) {
+  constexpr int BT = base_frags<TX, GSH>(), KQ = GSH >= 0 ? 2 : 4;
   const int row_tiles = (a.N + 255) / 256, tok_tiles = (a.T + 32 * BT - 1) / (32 * BT);
   const int tiles = row_tiles * tok_tiles;
   for (int at = 0, left; (left = tiles - at) > 0;) {
     if constexpr (BT == 4) {
       if (left >= 2 * kUnits) {
         const int n = left / (2 * kUnits) * (2 * kUnits);
-        k_linear_tile<TX, 4, W, GSH, 4, 1><<<n, 256, 0, st>>>(a, row_tiles, tok_tiles, at, n);
+        k_linear_tile<TX, 4, W, GSH, 4, 1><<<n, 256, 0, st>>>(a, row_tiles, tok_tiles, at, n, {});
         at += n;
       } else if (left > kUnits / 2) {
         const int n = std::min(left, kUnits);
-        k_linear_tile<TX, 4, W, GSH, 4, 2><<<n, 512, 0, st>>>(a, row_tiles, tok_tiles, at, n);
+        k_linear_tile<TX, 4, W, GSH, 4, 2><<<n, 512, 0, st>>>(a, row_tiles, tok_tiles, at, n, {});
         at += n;
       } else if (left > kUnits / 4) {
-        k_linear_tile<TX, 2, W, GSH, 4, 2><<<2 * left, 512, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+        k_linear_tile<TX, 2, W, GSH, 4, 2><<<2 * left, 512, 0, st>>>(a, row_tiles, tok_tiles, at, left, {});
         at += left;
       } else if (left > kUnits / 8) {
-        k_linear_tile<TX, 1, W, GSH, 4, 4><<<4 * left, 1024, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+        k_linear_tile<TX, 1, W, GSH, 4, 4><<<4 * left, 1024, 0, st>>>(a, row_tiles, tok_tiles, at, left, {});
         at += left;
       } else {
-        k_linear_tile<TX, 1, W, GSH, 2, 8><<<8 * left, 1024, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+        k_linear_tile<TX, 1, W, GSH, 2, 8><<<8 * left, 1024, 0, st>>>(a, row_tiles, tok_tiles, at, left, {});
         at += left;
       }
     } else {
@@ -1114,27 +1131,84 @@ void tile_launch(const LinearArgs& a, hipStream_t st) {
         // 281 / 282; 176 210 / 216; 400 190 / 220)
         const int over = left % (2 * kUnits);
         n = over > kUnits / 2 ? left : left - over;
-        k_linear_tile<TX, kWhole ? 2 : 1, W, GSH, 4, 1><<<n, 256, 0, st>>>(a, row_tiles, tok_tiles, at, n);
+        k_linear_tile<TX, kWhole ? 2 : 1, W, GSH, 4, 1><<<n, 256, 0, st>>>(a, row_tiles, tok_tiles, at, n, {});
       } else if (left > kUnits) {
-        k_linear_tile<TX, 1, W, GSH, 4, 1><<<2 * left, 256, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+        k_linear_tile<TX, 1, W, GSH, 4, 1><<<2 * left, 256, 0, st>>>(a, row_tiles, tok_tiles, at, left, {});
       } else if (left > kUnits / 2) {
-        k_linear_tile<TX, 2, W, GSH, 4, 2><<<left, 512, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+        k_linear_tile<TX, 2, W, GSH, 4, 2><<<left, 512, 0, st>>>(a, row_tiles, tok_tiles, at, left, {});
       } else if (left > kUnits / 4) {
-        k_linear_tile<TX, 1, W, GSH, 4, KQ><<<2 * left, 256 * KQ, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+        k_linear_tile<TX, 1, W, GSH, 4, KQ><<<2 * left, 256 * KQ, 0, st>>>(a, row_tiles, tok_tiles, at, left, {});
       } else {
-        k_linear_tile<TX, 1, W, GSH, 2, 2 * KQ><<<4 * left, 256 * KQ, 0, st>>>(a, row_tiles, tok_tiles, at, left);
+        k_linear_tile<TX, 1, W, GSH, 2, 2 * KQ><<<4 * left, 256 * KQ, 0, st>>>(a, row_tiles, tok_tiles, at, left, {});
       }
       at += n;
     }
   }
 }
+#else
+// Adds the parts in ascending order and finishes: a workgroup takes 4 tokens of a tile, a lane 4 columns.
+template <class TX, int BT>
+__global__ __launch_bounds__(256) void k_linear_add(LinearArgs a, int row_tiles, int tok_tiles, int first, int count,
+                                                    TileParts parts) {
+  const int id = first + blockIdx.x / (8 * BT), tk = blockIdx.x % (8 * BT) * 4 + (threadIdx.x >> 6);
+  const int group = id / (kTileRowGroup * tok_tiles), in_group = id - group * kTileRowGroup * tok_tiles;
+  const int rows_in = min(kTileRowGroup, row_tiles - group * kTileRowGroup);
+  const int t = in_group / rows_in * 32 * BT + tk, c = (threadIdx.x & 63) * 4;
+  const int col = (group * kTileRowGroup + in_group % rows_in) * 256 + c;
+  if (t >= a.T || col >= a.N) return;
+  const float* p = parts.sums + ((size_t)(id - first) * 32 * BT + tk) * 256 + c;
+  const size_t step = (size_t)count * 32 * BT * 256;
+  f4v v = *reinterpret_cast<const f4v*>(p);
+#pragma unroll 8
+  for (int k = 1; k < parts.n; ++k) v += *reinterpret_cast<const f4v*>(p + k * step);
+  const float w[4] = {v[0], v[1], v[2], v[3]};
+  finish4<TX>(a, token_of(a, t), col, 0, w, w);
+}
+
+// As many tiles as fill the card twice over run in workgroups of four wavefronts, up to 256 of the rest with eight that share
+// the rows summed over; what is left then, up to 128, is cut into parts of the sum, so that 256 workgroups run again.
+constexpr int kMinSteps = 4;  // of a part
+inline int tile_parts(int left, int steps) { return std::max(1, std::min(kUnits / left, steps / kMinSteps)); }
+template <class TX, int W, int GSH>
+void tile_launch(const LinearArgs& a, float* sums, hipStream_t st) {
+  constexpr int BT = base_frags<TX, GSH>();
+  const int row_tiles = (a.N + 255) / 256, tok_tiles = (a.T + 32 * BT - 1) / (32 * BT);
+  const int tiles = row_tiles * tok_tiles;
+  for (int at = 0, left; (left = tiles - at) > 0;) {
+    if (left >= 2 * kUnits) {
+      const int n = left / (2 * kUnits) * (2 * kUnits);
+      k_linear_tile<TX, BT, W, GSH, 4, 1><<<n, 256, 0, st>>>(a, row_tiles, tok_tiles, at, n, {1, nullptr});
+      at += n;
+    } else if (left > kUnits / 2) {
+      const int n = std::min(left, kUnits);
+      k_linear_tile<TX, BT, W, GSH, 4, 2><<<n, 512, 0, st>>>(a, row_tiles, tok_tiles, at, n, {1, nullptr});
+      at += n;
+    } else {
+      const TileParts p{tile_parts(left, a.nbp / 2), sums};
+      if (BT == 4 && a.T > 64)
+        k_linear_tile<TX, BT, W, GSH, 4, 2><<<dim3(left, p.n), 512, 0, st>>>(a, row_tiles, tok_tiles, at, left, p);
+      else if (a.T > 32)
+        k_linear_tile<TX, 2, W, GSH, 4, 2><<<dim3(left * BT / 2, p.n), 512, 0, st>>>(a, row_tiles, tok_tiles, at, left, p);
+      else
+        k_linear_tile<TX, 1, W, GSH, 4, 2><<<dim3(left * BT, p.n), 512, 0, st>>>(a, row_tiles, tok_tiles, at, left, p);
+      if (p.n > 1) k_linear_add<TX, BT><<<left * 8 * BT, 256, 0, st>>>(a, row_tiles, tok_tiles, at, left, p);
+      at += left;
+    }
+  }
+}
+// of the parts' sums, for any number of tokens up to T
+inline size_t tile_sums_bytes(int N, int steps, int64_t T) {
+  const int64_t tiles = (int64_t)((N + 255) / 256) * ((T + 63) / 64);  // the smaller tiles
+  return (size_t)std::min<int64_t>(kUnits, tiles * std::max(1, steps / kMinSteps)) * 128 * 256 * 4;
+}
+#endif
 
 template <class TX>
-void tiles_launch(const LinearArgs& a, int bits, hipStream_t st) {
-  if (bits == 8) tile_launch<TX, 8, -1>(a, st);
-  else if (a.gshift < 0) tile_launch<TX, 4, -1>(a, st);
-  else if (a.gshift == 0) tile_launch<TX, 4, 0>(a, st);
-  else tile_launch<TX, 4, 1>(a, st);
+void tiles_launch(const LinearArgs& a, int bits, float* sums, hipStream_t st) {
+  if (bits == 8) tile_launch<TX, 8, -1>(a, sums, st);
+  else if (a.gshift < 0) tile_launch<TX, 4, -1>(a, sums, st);
+  else if (a.gshift == 0) tile_launch<TX, 4, 0>(a, sums, st);
+  else tile_launch<TX, 4, 1>(a, sums, st);
 }
 
 #if !MOE_TRANSPOSED
@@ -1155,7 +1229,7 @@ void linear_launch(const LinearArgs& a, int bits, void* ws, hipStream_t st) {
     return;
   }
   k_linear_x<TX><<<(a.T + 31) / 32 * 4, 8 * kPrepLanes, 0, st>>>(a);
-  tiles_launch<TX>(a, bits, st);
+  tiles_launch<TX>(a, bits, nullptr, st);
 }
 
 LinearArgs linear_args(const moe_linear_config& c, const uint8_t* codes, const float* scales, const float* bias,
