@@ -151,6 +151,7 @@ __device__ __forceinline__ void put_h(const AdaptDown& a, const AdaptDown::Part&
 }
 
 // Few tokens: a workgroup takes a token and 4 rows of its A; its lanes share the columns, all loads in flight at once.
+// across: A lies as [C][R].
 template <class TX>
 __global__ __launch_bounds__(256) void k_adapt_dot(AdaptDown a) {
   __shared__ float s_sum[4][4];
@@ -160,9 +161,22 @@ __global__ __launch_bounds__(256) void k_adapt_dot(AdaptDown a) {
   float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (e >= 0) {
     const TX* x = static_cast<const TX*>(d.x) + (size_t)(d.order ? d.order[p] : p) * d.ldx;
+    if (d.across) {
+      struct alignas(4 * sizeof(TX)) Four {
+        TX v[4];
+      };
+      const TX* b = static_cast<const TX*>(d.a) + (size_t)e * a.R * d.C + r0;
+#pragma unroll 8
+      for (int c = tid; c < d.C; c += 256) {
+        const float xv = to_f32<TX>(x[c]);
+        const Four w = *reinterpret_cast<const Four*>(b + (size_t)c * a.R);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = fmaf(xv, to_f32<TX>(w.v[i]), v[i]);
+      }
+    }
     const TX* w = static_cast<const TX*>(d.a) + ((size_t)e * a.R + r0) * d.C;
 #pragma unroll 4
-    for (int g = tid; g < d.C / 8; g += 256) {
+    for (int g = tid; g < d.C / 8 && !d.across; g += 256) {
       Granule<TX> xg, wg[4];
       load8(x + g * 8, d.vec_x, xg);
 #pragma unroll
@@ -314,9 +328,13 @@ __device__ __forceinline__ size_t outer_at(const AdaptOuter& a, const AdaptOuter
   return d.rows ? ((size_t)e * d.C + c) * a.R + r : ((size_t)e * a.R + r) * d.C + c;
 }
 
-template <class TX, int RF>
-__device__ __forceinline__ void outer_16(const AdaptOuter& a, const AdaptOuter::Part& d, const AdaptChunk& ch, int c_wave,
-                                         int r0) {
+// FEW: positions are tokens, at most 64, and those that count are bits of `mine`.
+template <class TX, int RF, bool FEW>
+__device__ __forceinline__ void outer_16(const AdaptOuter& a, const AdaptOuter::Part& d, const AdaptChunk& ch, uint64_t mine,
+                                         int c_wave, int r0) {
+  auto counts = [&](int t) __attribute__((always_inline)) {
+    return t >= ch.p0 && t < ch.p1 && (!FEW || (mine >> t & 1));
+  };
   constexpr int MP = std::is_same<TX, bf16_t>::value ? 1 : 2;  // parts of m
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4, c0 = c_wave + 8 * i;
   const bool in = c0 < d.C;
@@ -328,14 +346,14 @@ __device__ __forceinline__ void outer_16(const AdaptOuter& a, const AdaptOuter::
   const float* vt[RF];
 #pragma unroll
   for (int f = 0; f < RF; ++f) vt[f] = d.vt + (size_t)min(r0 + 16 * f + i, a.R - 1) * 8;
-  const int begin = ch.p0 & ~7, last = (ch.p1 - 1) & ~7;
+  const int begin = ch.p0 & ~7, last = max(ch.p1 - 1, 0) & ~7;
   Granule<TX> mn[8];
   f8v vn[RF];
   int row[8];  // rows of m two steps ahead
   auto rows_of = [&](int p) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int t = min(max(p + 8 * g + j, ch.p0), ch.p1 - 1);
+      const int t = max(min(p + 8 * g + j, ch.p1 - 1), ch.p0);
       row[j] = d.order ? d.order[t] : t;
     }
   };
@@ -344,7 +362,7 @@ __device__ __forceinline__ void outer_16(const AdaptOuter& a, const AdaptOuter::
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       mn[j] = Granule<TX>{};
-      if (in && t0 + j >= ch.p0 && t0 + j < ch.p1) load8(static_cast<const TX*>(d.m) + (size_t)row[j] * d.ldm + c0, d.vec_m, mn[j]);
+      if (in && counts(t0 + j)) load8(static_cast<const TX*>(d.m) + (size_t)row[j] * d.ldm + c0, d.vec_m, mn[j]);
     }
 #pragma unroll
     for (int f = 0; f < RF; ++f) vn[f] = *reinterpret_cast<const f8v*>(vt[f] + (size_t)min(t0, last) * a.R);
@@ -362,7 +380,7 @@ __device__ __forceinline__ void outer_16(const AdaptOuter& a, const AdaptOuter::
     for (int f = 0; f < RF; ++f) {
       f8v v = vn[f];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = t0 + j >= ch.p0 && t0 + j < ch.p1 ? v[j] : 0.0f;
+      for (int j = 0; j < 8; ++j) v[j] = counts(t0 + j) ? v[j] : 0.0f;
       split_bf16(v, vh[f], vl[f]);
     }
     fetch(p + 32);
@@ -430,9 +448,9 @@ __device__ __forceinline__ void outer_16(const AdaptOuter& a, const AdaptOuter::
   }
 }
 
-template <int RF>
-__device__ __forceinline__ void outer_32(const AdaptOuter& a, const AdaptOuter::Part& d, const AdaptChunk& ch, int c_wave,
-                                         int r0) {
+template <int RF, bool FEW>
+__device__ __forceinline__ void outer_32(const AdaptOuter& a, const AdaptOuter::Part& d, const AdaptChunk& ch, uint64_t mine,
+                                         int c_wave, int r0) {
   constexpr int U = 4;  // steps of four positions
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4, c0 = c_wave + 4 * i;
   const bool in = c0 < d.C;
@@ -446,7 +464,7 @@ __device__ __forceinline__ void outer_32(const AdaptOuter& a, const AdaptOuter::
   auto rows_of = [&](int p) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int t = min(p + 4 * u + g, ch.p1 - 1);
+      const int t = max(min(p + 4 * u + g, ch.p1 - 1), ch.p0);
       row[u] = d.order ? d.order[t] : t;
     }
   };
@@ -457,7 +475,7 @@ __device__ __forceinline__ void outer_32(const AdaptOuter& a, const AdaptOuter::
       mn[u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int f = 0; f < RF; ++f) vn[f][u] = 0.0f;
-      if (t < ch.p1) {
+      if (t < ch.p1 && (!FEW || (mine >> t & 1))) {
         if (in) {
           const float* q = static_cast<const float*>(d.m) + (size_t)row[u] * d.ldm + c0;
           if (d.vec_m) mn[u] = *reinterpret_cast<const f4*>(q);
@@ -510,12 +528,20 @@ __device__ __forceinline__ void outer_32(const AdaptOuter& a, const AdaptOuter::
 
 // Workgroups in x: the columns of the first gradient, then of the second. In y: runs of positions, then adapters, whose
 // gradients are zeros where they have no tokens.
-template <class TX, int RF>
+template <class TX, int RF, bool FEW>
 __global__ __launch_bounds__(256, 2) void k_adapt_outer(AdaptOuter a, int x0, int runs) {
   constexpr int kCols = std::is_same<TX, float>::value ? 64 : 128;
   const bool second = (int)blockIdx.x >= x0;
   const AdaptOuter::Part& d = a.part[second];
   const int c = ((blockIdx.x - (second ? x0 : 0)) * 4 + (threadIdx.x >> 6)) * kCols, r0 = blockIdx.z * 16 * RF;
+  if constexpr (FEW) {  // an adapter each; without tokens its sums are zeros
+    const int lane = threadIdx.x & 63;
+    const uint64_t mine = __ballot(lane < a.T && (a.ids ? a.ids[min(lane, a.T - 1)] : 0) == (int)blockIdx.y);
+    const AdaptChunk ch{(int)blockIdx.y, 0, mine ? a.T : 0, -1};
+    if constexpr (std::is_same<TX, float>::value) outer_32<RF, true>(a, d, ch, mine, c, r0);
+    else outer_16<TX, RF, true>(a, d, ch, mine, c, r0);
+    return;
+  }
   if ((int)blockIdx.y >= runs) {
     const int e = blockIdx.y - runs;
     if (a.order.offsets[e + 1] != a.order.offsets[e]) return;
@@ -528,8 +554,8 @@ __global__ __launch_bounds__(256, 2) void k_adapt_outer(AdaptOuter a, int x0, in
   }
   if ((int)blockIdx.y >= *a.order.n_chunks) return;
   const AdaptChunk ch = a.order.chunks[blockIdx.y];
-  if constexpr (std::is_same<TX, float>::value) outer_32<RF>(a, d, ch, c, r0);
-  else outer_16<TX, RF>(a, d, ch, c, r0);
+  if constexpr (std::is_same<TX, float>::value) outer_32<RF, false>(a, d, ch, 0, c, r0);
+  else outer_16<TX, RF, false>(a, d, ch, 0, c, r0);
 }
 
 // Adapters of several runs: their partial sums in ascending order.
@@ -583,7 +609,7 @@ __global__ __launch_bounds__(256) void k_adapt_transpose(AdaptTranspose a, int x
 
 template <class TX>
 void down_launch(const AdaptDown& a, hipStream_t st) {
-  if (adapt_few(a.T, a.R)) {
+  if (a.few) {
     k_adapt_dot<TX><<<dim3(a.T, a.R / 4, a.parts), 256, 0, st>>>(a);
     return;
   }
@@ -597,10 +623,15 @@ template <class TX>
 void outer_launch(const AdaptOuter& a, hipStream_t st) {
   const int per = std::is_same<TX, float>::value ? 256 : 512, len = adapt_chunk_len(a.T);
   auto cols = [&](int k, int w) { return a.part[k].out ? (a.part[k].C + w - 1) / w : 0; };
+  const int x = cols(0, per) + cols(1, per);
+  if (!a.order.order) {
+    if (a.R <= 16) k_adapt_outer<TX, 1, true><<<dim3(x, a.n_ad), 256, 0, st>>>(a, cols(0, per), 0);
+    else k_adapt_outer<TX, 2, true><<<dim3(x, a.n_ad, (a.R + 31) / 32), 256, 0, st>>>(a, cols(0, per), 0);
+    return;
+  }
   const int runs = (int)adapt_max_chunks(a.T, a.n_ad);
-  const dim3 grid(cols(0, per) + cols(1, per), runs + a.n_ad, 1);
-  if (a.R <= 16) k_adapt_outer<TX, 1><<<grid, 256, 0, st>>>(a, cols(0, per), runs);
-  else k_adapt_outer<TX, 2><<<dim3(grid.x, grid.y, (a.R + 31) / 32), 256, 0, st>>>(a, cols(0, per), runs);
+  if (a.R <= 16) k_adapt_outer<TX, 1, false><<<dim3(x, runs + a.n_ad), 256, 0, st>>>(a, cols(0, per), runs);
+  else k_adapt_outer<TX, 2, false><<<dim3(x, runs + a.n_ad, (a.R + 31) / 32), 256, 0, st>>>(a, cols(0, per), runs);
   if (a.T > len)
     k_adapt_join<TX><<<dim3(cols(0, 256) + cols(1, 256), a.n_ad, a.R / 8), 256, 0, st>>>(a, cols(0, 256), len);
 }

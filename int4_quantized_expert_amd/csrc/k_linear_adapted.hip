@@ -35,7 +35,7 @@ hipError_t run(LinearArgs& a, int bits, const moe_adapters* ad, const int32_t* i
     a.R = ad->rank;
     a.ad = ids;
     AdaptDown d{};
-    d.T = a.T, d.R = a.R, d.n_ad = a.n_ad, d.parts = 1, d.by_token = few;
+    d.T = a.T, d.R = a.R, d.n_ad = a.n_ad, d.parts = 1, d.by_token = few, d.few = adapt_few(a.T, a.R);
     d.scale = ad->scale;
     const bool sorted = ids && !(few && adapt_few(a.T, a.R));
     const AdaptOrder o{reinterpret_cast<int32_t*>(w + p.order), reinterpret_cast<int32_t*>(w + p.ad),
@@ -47,7 +47,7 @@ hipError_t run(LinearArgs& a, int bits, const moe_adapters* ad, const int32_t* i
       if (!few) a.order = o.order, a.ad = o.ad;
     }
     d.ad = sorted ? o.ad : ids;
-    d.part[0] = {a.x, a.ldx, a.vec_x, a.K, sorted ? o.order : nullptr, ad->a, reinterpret_cast<float*>(w + p.h), nullptr};
+    d.part[0] = {a.x, a.ldx, a.vec_x, a.K, sorted ? o.order : nullptr, ad->a, 0, reinterpret_cast<float*>(w + p.h), nullptr};
     const hipError_t e = launch_adapt_down(d, dtype, st);
     if (e != hipSuccess) return e;
   }

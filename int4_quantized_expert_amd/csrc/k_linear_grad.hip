@@ -231,6 +231,167 @@ __global__ __launch_bounds__(256) void k_group_scales(const float* __restrict__ 
   }
 }
 
+// ------------------------------------------------------------ few tokens
+// Reading the codes is what counts: a wavefront takes 64 columns and a part of the rows for all tokens, with the codes of
+// kAhead steps (64 rows) in flight and the activations of the next one; no wavefront waits for another. The parts' sums
+// [part][T][N] are added by k_few_add, with the adapters' part and the residual.
+constexpr int kFewGroups = 384;  // workgroups wanted
+template <class TX, int TT, int W, int GSH>
+__global__ __launch_bounds__(256, 2) void k_linear_few(LinearArgs a, int parts, float* __restrict__ sums) {
+  constexpr int NX = std::is_same<TX, float>::value ? 2 : 1, GF = GSH < 0 ? 0 : GSH == 0 ? 2 : 1, WP = GF > 0 && NX == 2 ? 2 : 1;
+  constexpr int kAhead = WP == 2 ? 1 : W == 8 || GF > 0 ? 2 : 4;
+  __shared__ __align__(16) uint32_t s_mem[4][128 * W];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 31, g = lane >> 5;
+  const int col = (blockIdx.x * 4 + wave) * 64;
+  if (col >= a.N) return;  // all of a wavefront; there is no barrier
+  uint32_t* s_w = s_mem[wave];
+  const int first[2] = {col, min(col + 32, a.N - 32)}, groups = GSH >= 0 ? a.N / 32 >> a.gshift : 0;
+  const int steps = a.nbp / 2, p0 = steps * blockIdx.y / parts, p1 = steps * (blockIdx.y + 1) / parts;
+  const size_t step_bytes = (size_t)(a.N / 32) * kTileBlock<W>, low = a.xl - a.xh;
+  const uint8_t* src[2];
+  const _Float16* gsrc[2];
+#pragma unroll
+  for (int f = 0; f < 2; ++f) {
+    src[f] = a.codes + (size_t)(first[f] / 32) * kTileBlock<W> + (size_t)lane * (4 * W);
+    gsrc[f] = GF > 0 ? a.gs + (size_t)(first[f] / 32 >> a.gshift) * 64 + 16 * g : nullptr;
+  }
+  uint32_t wn[kAhead][2][W];
+  h8 gn[kAhead][GF ? GF : 1][WP][2][2];
+  auto fetch_w = [&](int p, uint32_t (&w)[2][W], h8 (&gs)[GF ? GF : 1][WP][2][2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int i = 0; i < W / 4; ++i) {
+        const u4v v = __builtin_nontemporal_load(reinterpret_cast<const u4v*>(src[f] + (size_t)p * step_bytes) + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[f][4 * i + j] = v[j];
+      }
+#pragma unroll
+    for (int f = 0; f < GF; ++f)
+#pragma unroll
+      for (int v = 0; v < WP; ++v)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            gs[f][v][h][m] = *reinterpret_cast<const h8*>(gsrc[f] + v * a.gs_low + (size_t)p * groups * 64 + h * 32 + m * 8);
+  };
+  f16v acc[TT][2];
+#pragma unroll
+  for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[tt][f][i] = 0.0f;
+  auto step = [&](int p, uint32_t (&w)[2][W], h8 (&gs)[GF ? GF : 1][WP][2][2]) __attribute__((always_inline)) {
+    h8 xf[NX][TT][2][2], wf[2][2][2 * WP];
+#pragma unroll
+    for (int n = 0; n < NX; ++n)
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            xf[n][tt][h][m] = *reinterpret_cast<const h8*>(a.xh + n * low + (size_t)tt * a.nbp * 1024 + (size_t)p * 2048 +
+                                                           (h * 4 + 2 * g + m) * 256 + r * 8);
+    unpack_transposed<W, WP, GF>(s_w, w, gs, wf);
+    fetch_w(min(p + kAhead, p1 - 1), w, gs);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+          for (int n = 0; n < NX; ++n)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              acc[tt][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xf[n][tt][h][m], wf[h][m][f], acc[tt][f], 0, 0, 0);
+              if constexpr (WP == 2)
+                if (n == 0)
+                  acc[tt][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xf[n][tt][h][m], wf[h][m][2 + f], acc[tt][f], 0, 0, 0);
+            }
+  };
+  if (p0 < p1) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) fetch_w(min(p0 + k, p1 - 1), wn[k], gn[k]);
+    for (int p = p0; p < p1; p += kAhead)
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (p + k < p1) step(p + k, wn[k], gn[k]);
+  }
+  const int rc = column_at<W>(r);
+#pragma unroll
+  for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int t = 32 * tt + 8 * (i >> 2) + 4 * g + (i & 3);
+        if (t < a.T && col + 32 * f < a.N) sums[((size_t)blockIdx.y * a.T + t) * a.N + first[f] + rc] = acc[tt][f][i];
+      }
+}
+
+// A workgroup takes a token and 1024 columns, a lane four. ab: A of the adapters as it is, [n][R][N].
+template <class TX>
+__global__ __launch_bounds__(256) void k_few_add(LinearArgs a, int parts, const float* __restrict__ sums) {
+  const int t = blockIdx.y, col = blockIdx.x * 1024 + threadIdx.x * 4;
+  if (col >= a.N) return;
+  const size_t step = (size_t)a.T * a.N;
+  const float* p = sums + (size_t)t * a.N + col;
+  f4v v = *reinterpret_cast<const f4v*>(p);
+#pragma unroll 8
+  for (int k = 1; k < parts; ++k) v += *reinterpret_cast<const f4v*>(p + k * step);
+  const int sh = a.sh[t], id = a.h ? adapter_of(a, t) : -1;
+  float w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = ldexpf(v[i], -sh);
+  if (id >= 0) {
+    struct alignas(4 * sizeof(TX)) Four {
+      TX v[4];
+    };
+    const TX* b = static_cast<const TX*>(a.ab) + (size_t)id * a.R * a.N + col;
+    const float* h = a.h + (size_t)t * a.R;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+    for (int r = 0; r < a.R; ++r) {
+      const Four q = *reinterpret_cast<const Four*>(b + (size_t)r * a.N);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = fmaf(h[r], to_f32<TX>(q.v[i]), s[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] += s[i];
+  }
+  finish4<TX>(a, t, col, 0, w, w);
+}
+
+// by the columns alone, so that the sums of fewer tokens are no larger; with 33 to 64 tokens half as many, twice as long
+inline int few_parts(int N, int steps, bool two) {
+  return std::max(1, std::min((two ? kFewGroups / 2 : kFewGroups) / ((N + 255) / 256), steps / (two ? 4 : 2)));
+}
+inline size_t few_bytes(int N, int steps, int64_t T) {
+  const int64_t t = std::min<int64_t>(T, kAdaptFewTokens);
+  size_t b = (size_t)few_parts(N, steps, false) * std::min<int64_t>(t, 32) * N * 4;
+  if (t > 32) b = std::max(b, (size_t)few_parts(N, steps, true) * t * N * 4);
+  return b;
+}
+template <class TX, int W, int GSH>
+void few_form(const LinearArgs& a, float* sums, hipStream_t st) {
+  const int parts = few_parts(a.N, a.nbp / 2, a.T > 32);
+  const dim3 grid((a.N + 255) / 256, parts);
+  if (a.T <= 32) k_linear_few<TX, 1, W, GSH><<<grid, 256, 0, st>>>(a, parts, sums);
+  else k_linear_few<TX, 2, W, GSH><<<grid, 256, 0, st>>>(a, parts, sums);
+  k_few_add<TX><<<dim3((a.N + 1023) / 1024, a.T), 256, 0, st>>>(a, parts, sums);
+}
+template <class TX>
+void few_launch(const LinearArgs& a, int bits, float* sums, hipStream_t st) {
+  if (bits == 8) few_form<TX, 8, -1>(a, sums, st);
+  else if (a.gshift < 0) few_form<TX, 4, -1>(a, sums, st);
+  else if (a.gshift == 0) few_form<TX, 4, 0>(a, sums, st);
+  else few_form<TX, 4, 1>(a, sums, st);
+}
+
 // ------------------------------------------------------------ the whole
 struct GradPlan {
   LinearPlan z;
@@ -248,7 +409,7 @@ GradPlan grad_plan(const moe_linear_config& c, const moe_adapters* ad, int64_t T
   const size_t groups = c.group_size > 0 ? c.cols / c.group_size : 0;
   p.mul = take(groups ? (size_t)c.rows * 4 : 0);
   p.gs = take(groups * c.rows * 4);
-  p.sums = take(tile_sums_bytes(c.cols, c.rows / 64, T));
+  p.sums = take(std::max(tile_sums_bytes(c.cols, c.rows / 64, T), few_bytes(c.cols, c.rows / 64, T)));
   if (ad) {
     const size_t R = ad->rank, n = ad->n_adapters, N = c.rows, K = c.cols;
     p.dz = take(c.act != MOE_ACT_NONE ? T * N * 4 : 0);
@@ -309,14 +470,18 @@ hipError_t run(const moe_linear_config& c, const uint8_t* codes, const float* sc
   a.sh = i32(p.z.sh);
 
   AdaptOrder order{};
+  const bool few = T <= kAdaptFewTokens;  // positions are tokens
   if (ad) {
+    a.ad = ids;
+    a.n_ad = ad->n_adapters;
+    a.R = ad->rank;
+  }
+  if (ad && !few) {
     order = AdaptOrder{i32(p.order), i32(p.ad), i32(p.n_chunks) + 1, reinterpret_cast<AdaptChunk*>(w + p.runs),
                        i32(p.offsets), i32(p.slot0), i32(p.n_chunks), reinterpret_cast<AdaptChunk*>(w + p.chunks)};
     MOE_TRY(launch_adapt_order(ids, T, ad->n_adapters, order, st));
     a.order = i32(p.order);
     a.ad = i32(p.ad);
-    a.n_ad = ad->n_adapters;
-    a.R = ad->rank;
   }
   const bool keep = ad && c.act != MOE_ACT_NONE;
   const float* mul = scales;
@@ -339,24 +504,28 @@ hipError_t run(const moe_linear_config& c, const uint8_t* codes, const float* sc
     const void* m = keep ? w + p.dz : dy;  // dz, by position or by token
     const int64_t ldm = keep ? N : ldd;
     const int32_t* m_order = keep ? nullptr : a.order;
-    MOE_TRY(launch_adapt_transpose({a.n_ad, order.offsets, {{ad->b, N, a.R, w + p.bt}, {ad->a, a.R, K, dx ? w + p.at : nullptr}}},
-                                   elem, st));
-    AdaptDown down{T, a.R, a.n_ad, db ? 2 : 1, 0, a.ad, order.n_runs, order.runs, ad->scale, {}};
-    down.part[0] = {m, ldm, vec(m, ldm), N, m_order, w + p.bt, f32(p.u), f32(p.ut)};
-    down.part[1] = {x, ldx, vec(x, ldx), K, a.order, ad->a, f32(p.h), f32(p.ht)};
+    // few: A and B as they are
+    if (!few)
+      MOE_TRY(launch_adapt_transpose(
+          {a.n_ad, order.offsets, {{ad->b, N, a.R, w + p.bt}, {ad->a, a.R, K, dx ? w + p.at : nullptr}}}, elem, st));
+    AdaptDown down{T, a.R, a.n_ad, db ? 2 : 1, few || adapt_few(T, a.R), 0, a.ad, order.n_runs, order.runs, ad->scale, {}};
+    down.part[0] = {m, ldm, vec(m, ldm), N, m_order, few ? ad->b : w + p.bt, few, f32(p.u), f32(p.ut)};
+    down.part[1] = {x, ldx, vec(x, ldx), K, a.order, ad->a, 0, f32(p.h), f32(p.ht)};
     MOE_TRY(launch_adapt_down(down, dtype, st));
     if (da || db) {
-      AdaptOuter outer{T, a.R, a.n_ad, order, {}};
+      AdaptOuter outer{T, a.R, a.n_ad, ids, order, {}};
       outer.part[0] = {m, ldm, vec(m, ldm), N, 1, m_order, f32(p.h), f32(p.ht), f32(p.part), db};
       outer.part[1] = {x, ldx, vec(x, ldx), K, 0, a.order, f32(p.u), f32(p.ut), f32(p.part_a), da};
       MOE_TRY(launch_adapt_outer(outer, dtype, st));
     }
     if (dx) {
       a.h = f32(p.u);
-      a.ab = w + p.at;
+      a.ab = few ? ad->a : w + p.at;
     }
   }
-  if (dx) tiles_launch<TX>(a, c.weight_bits == 8 ? 8 : 4, f32(p.sums), st);
+  const int bits = c.weight_bits == 8 ? 8 : 4;
+  if (dx && few) few_launch<TX>(a, bits, f32(p.sums), st);
+  else if (dx) tiles_launch<TX>(a, bits, f32(p.sums), st);
 #undef MOE_TRY
   return hipGetLastError();
 }

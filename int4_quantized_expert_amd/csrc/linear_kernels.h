@@ -173,6 +173,54 @@ __device__ __forceinline__ void adapter_frags(const LinearArgs& a, int p0, const
   }
 }
 
+// Transposed codes of a step: each lane holds its row's codes of two fragments of 32 columns and needs a column's codes of
+// the rows it multiplies. They go through LDS (s_w, [2][64 rows][4 * W bytes]) and are read back transposed, in each group
+// of 16 lanes the codes of 16 columns and 16 rows (int8: 8 rows). GF: fragments with group scales of their own, 0 without
+// them; WP: parts of a scaled code.
+template <int W, int WP, int GF>
+__device__ __forceinline__ void unpack_transposed(uint32_t* s_w, const uint32_t (&wn)[2][W], const h8 (&gn)[GF ? GF : 1][WP][2][2],
+                                                  h8 (&d)[2][2][2 * WP]) {
+  typedef int i2v __attribute__((ext_vector_type(2)));
+  typedef __attribute__((address_space(3))) i2v* lds2;
+  const int lane = threadIdx.x & 63, g = lane >> 5, q = lane & 15, ch = lane >> 4 & 1;
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i)
+      *reinterpret_cast<u4v*>(s_w + f * 64 * W + lane * W + 4 * i) =
+          u4v{wn[f][4 * i], wn[f][4 * i + 1], wn[f][4 * i + 2], wn[f][4 * i + 3]};
+  wave_sync();
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (W == 4) {
+        const i2v v = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds2)(s_w + f * 256 + (32 * h + 16 * g + q) * 4 + ch * 2));
+        d[h][0][f] = codes_h8((uint32_t)v[0]);
+        d[h][1][f] = codes_h8((uint32_t)v[1]);
+      } else {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const i2v v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+              (lds2)(s_w + f * 512 + (32 * h + 16 * g + 8 * m + (q >> 1)) * 8 + ch * 4 + (q & 1) * 2));
+          d[h][m][f] = codes_h8(__builtin_amdgcn_perm(v[1], v[0], 0x06040200u), __builtin_amdgcn_perm(v[1], v[0], 0x07050301u));
+        }
+      }
+    }
+  if constexpr (GF > 0)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const h8 q8 = d[h][m][f];
+          d[h][m][f] = q8 * gn[f & (GF - 1)][0][h][m];
+          if constexpr (WP == 2) d[h][m][2 + f] = q8 * gn[f & (GF - 1)][1][h][m];
+        }
+  wave_sync();
+}
+
 // KW groups of RW wavefronts: a group's wavefronts take 64 rows each, from wavefront tile wt0 on, the groups share the
 // columns.
 // Transposed: part `part` of `parts` of the sum goes to `sums` [tokens of the tile][256 columns] where there are several.
@@ -284,48 +332,7 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int wt0, int t0, c
   };
   auto unpack = [&](h8 (&d)[2][2][2 * kWP], float (&ds)[2][kScales]) __attribute__((always_inline)) {
     if constexpr (kTransposed) {
-      // Each lane holds a row's codes of 32 columns and needs a column's codes of the rows it multiplies: through LDS,
-      // read back transposed, in each group of 16 lanes the codes of 16 columns and 16 rows (int8: 8 rows).
-#pragma unroll
-      for (int f = 0; f < 2; ++f)
-#pragma unroll
-        for (int i = 0; i < W / 4; ++i)
-          *reinterpret_cast<u4v*>(s_w + f * 64 * W + lane * W + 4 * i) =
-              u4v{wn[f][4 * i], wn[f][4 * i + 1], wn[f][4 * i + 2], wn[f][4 * i + 3]};
-      wave_sync();
-      typedef int i2v __attribute__((ext_vector_type(2)));
-      typedef __attribute__((address_space(3))) i2v* lds2;
-      const int q = lane & 15, ch = lane >> 4 & 1;
-#pragma unroll
-      for (int f = 0; f < 2; ++f)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if constexpr (W == 4) {
-            const i2v v = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds2)(s_w + f * 256 + (32 * h + 16 * g + q) * 4 + ch * 2));
-            d[h][0][f] = codes_h8((uint32_t)v[0]);
-            d[h][1][f] = codes_h8((uint32_t)v[1]);
-          } else {
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              const i2v v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                  (lds2)(s_w + f * 512 + (32 * h + 16 * g + 8 * m + (q >> 1)) * 8 + ch * 4 + (q & 1) * 2));
-              d[h][m][f] = codes_h8(__builtin_amdgcn_perm(v[1], v[0], 0x06040200u),
-                                    __builtin_amdgcn_perm(v[1], v[0], 0x07050301u));
-            }
-          }
-        }
-      if constexpr (kGroupFrags > 0)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-              const h8 q8 = d[h][m][f];
-              d[h][m][f] = q8 * gn[f & (kGroupFrags - 1)][0][h][m];
-              if constexpr (kWP == 2) d[h][m][2 + f] = q8 * gn[f & (kGroupFrags - 1)][1][h][m];
-            }
-      wave_sync();
+      unpack_transposed<W, kWP, kGroupFrags>(s_w, wn, gn, d);
       return;
     }
 #pragma unroll
@@ -1185,12 +1192,7 @@ void tile_launch(const LinearArgs& a, float* sums, hipStream_t st) {
       at += n;
     } else {
       const TileParts p{tile_parts(left, a.nbp / 2), sums};
-      if (BT == 4 && a.T > 64)
-        k_linear_tile<TX, BT, W, GSH, 4, 2><<<dim3(left, p.n), 512, 0, st>>>(a, row_tiles, tok_tiles, at, left, p);
-      else if (a.T > 32)
-        k_linear_tile<TX, 2, W, GSH, 4, 2><<<dim3(left * BT / 2, p.n), 512, 0, st>>>(a, row_tiles, tok_tiles, at, left, p);
-      else
-        k_linear_tile<TX, 1, W, GSH, 4, 2><<<dim3(left * BT, p.n), 512, 0, st>>>(a, row_tiles, tok_tiles, at, left, p);
+      k_linear_tile<TX, BT, W, GSH, 4, 2><<<dim3(left, p.n), 512, 0, st>>>(a, row_tiles, tok_tiles, at, left, p);
       if (p.n > 1) k_linear_add<TX, BT><<<left * 8 * BT, 256, 0, st>>>(a, row_tiles, tok_tiles, at, left, p);
       at += left;
     }

@@ -59,8 +59,10 @@ struct AdaptOrder {
   AdaptChunk* chunks;
 };
 hipError_t launch_adapt_order(const int32_t* ids, int T, int n_ad, const AdaptOrder& out, hipStream_t st);
-// Whether s (A x) takes a workgroup for a token and four rows (no order needed), or one for a run of 16 positions.
+// Whether s (A x) takes a workgroup for a token and four rows (no order needed) rather than one for a run of 16 positions.
 inline bool adapt_few(int64_t T, int R) { return T * R <= 4096; }
+// Tokens of a backward pass that needs no order: its products and sums look for their adapters' tokens themselves.
+constexpr int kAdaptFewTokens = 64;
 // h[p][r] = scale * sum over c of x[order[p]][c] a[ad[p]][r][c] for positions with an adapter; ht, where given, the same as
 // [T / 8][R][8]; two such products in one launch
 struct AdaptDown {
@@ -70,13 +72,15 @@ struct AdaptDown {
     int32_t vec_x, C;
     const int32_t* order;
     const void* a;
+    int32_t across;  // (few) a lies as [C][R]
     float* h;
     float* ht;
   };
   int32_t T, R, n_ad, parts;
+  int32_t few;       // a workgroup for a token and four rows, with ad; else one for each of the order's runs
   int32_t by_token;  // rows of h are tokens
   const int32_t* ad;
-  const int32_t* n_runs;  // not adapt_few: the order's runs, nullptr: adapter 0 for all
+  const int32_t* n_runs;  // nullptr: adapter 0 for all
   const AdaptChunk* runs;
   const float* scale;
   Part part[2];
@@ -95,7 +99,8 @@ struct AdaptOuter {
     void* out;
   };
   int32_t T, R, n_ad;
-  AdaptOrder order;
+  const int32_t* ids;  // without an order: adapter of a token
+  AdaptOrder order;    // order.order nullptr: positions are tokens, at most kAdaptFewTokens
   Part part[2];
 };
 hipError_t launch_adapt_outer(const AdaptOuter& a, int dtype, hipStream_t st);
