@@ -233,20 +233,22 @@ __global__ __launch_bounds__(256) void k_group_scales(const float* __restrict__ 
 
 // ------------------------------------------------------------ few tokens
 // Reading the codes is what counts: a wavefront takes 64 columns and a part of the rows for all tokens, with the codes of
-// kAhead steps (64 rows) in flight and the activations of the next one; no wavefront waits for another. The parts' sums
+// kAhead steps (64 rows) in flight; it waits for no other before the sum of the workgroup's four. The parts' sums
 // [part][T][N] are added by k_few_add, with the adapters' part and the residual.
-constexpr int kFewGroups = 384;  // workgroups wanted
+constexpr int kFewGroups = 512;  // workgroups wanted
+constexpr int kFewWaves = 4;
 template <class TX, int TT, int W, int GSH>
 __global__ __launch_bounds__(256, 2) void k_linear_few(LinearArgs a, int parts, float* __restrict__ sums) {
   constexpr int NX = std::is_same<TX, float>::value ? 2 : 1, GF = GSH < 0 ? 0 : GSH == 0 ? 2 : 1, WP = GF > 0 && NX == 2 ? 2 : 1;
-  constexpr int kAhead = WP == 2 ? 1 : W == 8 || GF > 0 ? 2 : 4;
-  __shared__ __align__(16) uint32_t s_mem[4][128 * W];
+  constexpr int kAhead = WP == 2 ? 1 : W == 8 || GF > 0 ? 2 : 3;
+  // [wavefronts][128 * W] codes, then [wavefronts][32 * TT][64] sums
+  __shared__ __align__(16) uint32_t s_mem[kFewWaves * std::max(128 * W, 2048 * TT)];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 31, g = lane >> 5;
-  const int col = (blockIdx.x * 4 + wave) * 64;
-  if (col >= a.N) return;  // all of a wavefront; there is no barrier
-  uint32_t* s_w = s_mem[wave];
+  const int col = blockIdx.x * 64;
+  uint32_t* s_w = s_mem + wave * 128 * W;
   const int first[2] = {col, min(col + 32, a.N - 32)}, groups = GSH >= 0 ? a.N / 32 >> a.gshift : 0;
-  const int steps = a.nbp / 2, p0 = steps * blockIdx.y / parts, p1 = steps * (blockIdx.y + 1) / parts;
+  const int64_t steps = a.nbp / 2, k0 = blockIdx.y * kFewWaves + wave;
+  const int p0 = (int)(steps * k0 / (parts * kFewWaves)), p1 = (int)(steps * (k0 + 1) / (parts * kFewWaves));
   const size_t step_bytes = (size_t)(a.N / 32) * kTileBlock<W>, low = a.xl - a.xh;
   const uint8_t* src[2];
   const _Float16* gsrc[2];
@@ -321,16 +323,24 @@ __global__ __launch_bounds__(256, 2) void k_linear_few(LinearArgs a, int parts, 
       for (int k = 0; k < kAhead; ++k)
         if (p + k < p1) step(p + k, wn[k], gn[k]);
   }
-  const int rc = column_at<W>(r);
+  __syncthreads();
+  float* s_sum = reinterpret_cast<float*>(s_mem);
 #pragma unroll
   for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
     for (int f = 0; f < 2; ++f)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int t = 32 * tt + 8 * (i >> 2) + 4 * g + (i & 3);
-        if (t < a.T && col + 32 * f < a.N) sums[((size_t)blockIdx.y * a.T + t) * a.N + first[f] + rc] = acc[tt][f][i];
-      }
+      for (int i = 0; i < 16; ++i) s_sum[((wave * TT + tt) * 32 + 16 * f + i) * 64 + lane] = acc[tt][f][i];
+  __syncthreads();
+  const int rc = column_at<W>(r);
+  for (int k = wave; k < 32 * TT; k += kFewWaves) {  // sum i of fragment f and tokens tt, of all lanes
+    const int tt = k >> 5, f = k >> 4 & 1, i = k & 15;
+    const int t = 32 * tt + 8 * (i >> 2) + 4 * g + (i & 3);
+    float v = s_sum[k * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) v += s_sum[(w * 32 * TT + k) * 64 + lane];
+    if (t < a.T && col + 32 * f < a.N) sums[((size_t)blockIdx.y * a.T + t) * a.N + first[f] + rc] = v;
+  }
 }
 
 // A workgroup takes a token and 1024 columns, a lane four. ab: A of the adapters as it is, [n][R][N].
@@ -366,20 +376,17 @@ __global__ __launch_bounds__(256) void k_few_add(LinearArgs a, int parts, const 
   finish4<TX>(a, t, col, 0, w, w);
 }
 
-// by the columns alone, so that the sums of fewer tokens are no larger; with 33 to 64 tokens half as many, twice as long
-inline int few_parts(int N, int steps, bool two) {
-  return std::max(1, std::min((two ? kFewGroups / 2 : kFewGroups) / ((N + 255) / 256), steps / (two ? 4 : 2)));
+// by the columns alone, so that the sums of fewer tokens are no larger
+inline int few_parts(int N, int steps) {
+  return std::max(1, std::min(kFewGroups / ((N + 63) / 64), steps / (2 * kFewWaves)));
 }
 inline size_t few_bytes(int N, int steps, int64_t T) {
-  const int64_t t = std::min<int64_t>(T, kAdaptFewTokens);
-  size_t b = (size_t)few_parts(N, steps, false) * std::min<int64_t>(t, 32) * N * 4;
-  if (t > 32) b = std::max(b, (size_t)few_parts(N, steps, true) * t * N * 4);
-  return b;
+  return (size_t)few_parts(N, steps) * std::min<int64_t>(T, kAdaptFewTokens) * N * 4;
 }
 template <class TX, int W, int GSH>
 void few_form(const LinearArgs& a, float* sums, hipStream_t st) {
-  const int parts = few_parts(a.N, a.nbp / 2, a.T > 32);
-  const dim3 grid((a.N + 255) / 256, parts);
+  const int parts = few_parts(a.N, a.nbp / 2);
+  const dim3 grid((a.N + 63) / 64, parts);
   if (a.T <= 32) k_linear_few<TX, 1, W, GSH><<<grid, 256, 0, st>>>(a, parts, sums);
   else k_linear_few<TX, 2, W, GSH><<<grid, 256, 0, st>>>(a, parts, sums);
   k_few_add<TX><<<dim3((a.N + 1023) / 1024, a.T), 256, 0, st>>>(a, parts, sums);
