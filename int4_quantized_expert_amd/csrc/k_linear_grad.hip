@@ -3,8 +3,8 @@
 // W^T dz runs in the product's tiles, summing over the weight rows. Row scales are multiplied into dz, in fp32 before its
 // one rounding to fp16 (relative 2^-12; fp32 gradients keep two halves, 2^-23). Group scales differ along a row: the power
 // of two of a row's largest is multiplied into dz, without loss, what is left of them, at most 1, into the codes, as fp16
-// (relative 2^-11, or 2^-25 of the row's largest for scales that are less than 2^-14 of it; fp32 gradients keep two parts,
-// 2^-19). dz is kept in the call's type for the adapters' sums, as autograd would hand it on.
+// (relative 2^-11, or 2^-25 of the row's largest for scales that are less than 2^-14 of it; fp16 and fp32 gradients keep
+// two parts, 2^-19). dz is kept in the call's type for the adapters' sums, as autograd would hand it on.
 #define MOE_ADAPTED 1
 #define MOE_TRANSPOSED 1
 #include "linear_kernels.h"
@@ -239,7 +239,7 @@ constexpr int kFewGroups = 512;  // workgroups wanted
 constexpr int kFewWaves = 4;
 template <class TX, int TT, int W, int GSH>
 __global__ __launch_bounds__(256, 2) void k_linear_few(LinearArgs a, int parts, float* __restrict__ sums) {
-  constexpr int NX = std::is_same<TX, float>::value ? 2 : 1, GF = GSH < 0 ? 0 : GSH == 0 ? 2 : 1, WP = GF > 0 && NX == 2 ? 2 : 1;
+  constexpr int NX = std::is_same<TX, float>::value ? 2 : 1, GF = GSH < 0 ? 0 : GSH == 0 ? 2 : 1, WP = GF > 0 ? scaled_parts<TX>() : 1;
   constexpr int kAhead = WP == 2 ? 1 : W == 8 || GF > 0 ? 2 : 3;
   // [wavefronts][128 * W] codes, then [wavefronts][32 * TT][64] sums
   __shared__ __align__(16) uint32_t s_mem[kFewWaves * std::max(128 * W, 2048 * TT)];
@@ -497,7 +497,7 @@ hipError_t run(const moe_linear_config& c, const uint8_t* codes, const float* sc
     a.gs = reinterpret_cast<_Float16*>(w + p.gs);
     a.gs_low = (int64_t)N * groups;
     k_group_scales<<<N / 64, 256, 0, st>>>(scales, groups, f32(p.mul), reinterpret_cast<_Float16*>(w + p.gs), a.gs_low,
-                                           elem == 4);
+                                           scaled_parts<TX>() == 2);
     mul = f32(p.mul);
   }
   if (dx || keep) {

@@ -173,6 +173,14 @@ __device__ __forceinline__ void adapter_frags(const LinearArgs& a, int p0, const
   }
 }
 
+// Parts of a code times what is left of its group scale: for bf16 one fp16 rounding of either is far below the result's own;
+// fp16 and fp32 keep the rest of the scale as a second part (fp16 with one: 4.0e-4 off in the 2-norm where the result's
+// rounding alone is 2.1e-4).
+template <class TX>
+constexpr int scaled_parts() {
+  return std::is_same<TX, bf16_t>::value ? 1 : 2;
+}
+
 // Transposed codes of a step: each lane holds its row's codes of two fragments of 32 columns and needs a column's codes of
 // the rows it multiplies. They go through LDS (s_w, [2][64 rows][4 * W bytes]) and are read back transposed, in each group
 // of 16 lanes the codes of 16 columns and 16 rows (int8: 8 rows). GF: fragments with group scales of their own, 0 without
@@ -267,7 +275,7 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int wt0, int t0, c
 #pragma unroll
     for (int f = 0; f < 2; ++f) gsrc[f] = a.gs + (size_t)(first[f] / 32 >> a.gshift) * 64 + 16 * g;
   constexpr int kGroupFrags = !kTransposed || GSH < 0 ? 0 : GSH == 0 ? 2 : 1;  // fragments with scales of their own
-  constexpr int kWP = kGroupFrags > 0 && NX == 2 ? 2 : 1;                      // parts of a scaled code
+  constexpr int kWP = kGroupFrags > 0 ? scaled_parts<TX>() : 1;                // parts of a scaled code
   h8 gn[kGroupFrags ? kGroupFrags : 1][kWP][2][2];  // the next step's group scales
   const uint32_t off0 = r * (4 * W), off1 = off0 + g * (uint32_t)kTileBlock<W>;
   // this workgroup's [2 blocks][4 slices][32][8] chunks, 16 bytes a lane
@@ -541,7 +549,7 @@ __device__ __forceinline__ void tile_run(const LinearArgs& a, int wt0, int t0, c
 constexpr int kTileRowGroup = 8, kDies = 8;
 template <class TX, int GSH>
 constexpr int base_frags() {  // 128 tokens need too many registers with two halves of them or a second set of sums
-  return std::is_same<TX, float>::value || GSH == 0 || (GSH > 0 && !kTransposed) ? 2 : 4;
+  return std::is_same<TX, float>::value || GSH == 0 || (GSH > 0 && !(kTransposed && std::is_same<TX, bf16_t>::value)) ? 2 : 4;
 }
 
 // Transposed: the sum over the rows in n parts, [n][tiles of the launch][32 * BT tokens][256 columns], added by k_linear_add.
