@@ -317,8 +317,8 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_adapt_down(AdaptDown a) 
 }
 
 // ------------------------------------------------------------ gradients of A and B
-// out[r][c] = sum over an adapter's positions of v[p][r] m[p][c]; a wavefront takes 32 rows r (fewer where R is less) by
-// 128 columns and a run of positions, a workgroup four of them; both gradients in one launch. Positions are what is
+// out[r][c] = sum over an adapter's positions of v[p][r] m[p][c]; a workgroup takes 32 rows r (fewer where R is less) by
+// 128 columns and a run of positions, of which each of its four wavefronts takes a part; both gradients in one launch. Positions are what is
 // summed over, and neither m nor v has neighbouring ones in memory: a lane loads 8 columns of each of 8 positions and
 // exchanges halves of words between two positions, which gives the operands of 8 products (column l + j of every eight
 // columns in product j). v comes with eight
@@ -328,15 +328,22 @@ __device__ __forceinline__ size_t outer_at(const AdaptOuter& a, const AdaptOuter
   return d.rows ? ((size_t)e * d.C + c) * a.R + r : ((size_t)e * a.R + r) * d.C + c;
 }
 
+// The positions of a run that this one of four wavefronts takes, cut at multiples of 8.
+__device__ __forceinline__ void wave_part(const AdaptChunk& ch, int& w0, int& w1) {
+  const int wave = threadIdx.x >> 6, begin = ch.p0 & ~7, per = ((ch.p1 - begin + 31) / 32) * 8;
+  w0 = max(min(begin + wave * per, ch.p1), ch.p0);
+  w1 = max(min(begin + (wave + 1) * per, ch.p1), ch.p0);
+}
+
 // FEW: positions are tokens, at most 64, and those that count are bits of `mine`.
 template <class TX, int RF, bool FEW>
 __device__ __forceinline__ void outer_16(const AdaptOuter& a, const AdaptOuter::Part& d, const AdaptChunk& ch, uint64_t mine,
-                                         int c_wave, int r0) {
-  auto counts = [&](int t) __attribute__((always_inline)) {
-    return t >= ch.p0 && t < ch.p1 && (!FEW || (mine >> t & 1));
-  };
+                                         int c_group, int r0, float* s_sum) {
+  int w0, w1;  // this wavefront's positions
+  wave_part(ch, w0, w1);
+  auto counts = [&](int t) __attribute__((always_inline)) { return t >= w0 && t < w1 && (!FEW || (mine >> t & 1)); };
   constexpr int MP = std::is_same<TX, bf16_t>::value ? 1 : 2;  // parts of m
-  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4, c0 = c_wave + 8 * i;
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4, c0 = c_group + 8 * i;
   const bool in = c0 < d.C;
   f4 acc[RF][8];
 #pragma unroll
@@ -346,14 +353,14 @@ __device__ __forceinline__ void outer_16(const AdaptOuter& a, const AdaptOuter::
   const float* vt[RF];
 #pragma unroll
   for (int f = 0; f < RF; ++f) vt[f] = d.vt + (size_t)min(r0 + 16 * f + i, a.R - 1) * 8;
-  const int begin = ch.p0 & ~7, last = max(ch.p1 - 1, 0) & ~7;
+  const int begin = w0 & ~7, last = max(w1 - 1, 0) & ~7;
   Granule<TX> mn[8];
   f8v vn[RF];
   int row[8];  // rows of m two steps ahead
   auto rows_of = [&](int p) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int t = max(min(p + 8 * g + j, ch.p1 - 1), ch.p0);
+      const int t = max(min(p + 8 * g + j, w1 - 1), 0);
       row[j] = d.order ? d.order[t] : t;
     }
   };
@@ -370,7 +377,7 @@ __device__ __forceinline__ void outer_16(const AdaptOuter& a, const AdaptOuter::
   rows_of(begin);
   fetch(begin);
   rows_of(begin + 32);
-  for (int p = begin; p < ch.p1; p += 32) {
+  for (int p = begin; p < w1; p += 32) {
     Granule<TX> m[8];
     b8 vh[RF], vl[RF];
     const int t0 = p + 8 * g;
@@ -410,6 +417,21 @@ __device__ __forceinline__ void outer_16(const AdaptOuter& a, const AdaptOuter::
         }
       }
   }
+  // the wavefronts' sums through LDS, [wavefront][f][k][j][lane]
+  const int wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int f = 0; f < RF; ++f)
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s_sum[(((wave * RF + f) * 8 + k) * 4 + j) * 64 + lane] = acc[f][k][j];
+  __syncthreads();
+  auto total = [&](int f, int k, int j) __attribute__((always_inline)) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) v += s_sum[(((w * RF + f) * 8 + k) * 4 + j) * 64 + lane];
+    return v;
+  };
   if (!in) return;
   struct alignas(16) Eight {
     TX v[8];
@@ -421,28 +443,28 @@ __device__ __forceinline__ void outer_16(const AdaptOuter& a, const AdaptOuter::
   for (int f = 0; f < RF; ++f) {
     const int r = r0 + 16 * f + 4 * g;  // and three more
     if (r >= a.R) continue;
-    if (ch.slot >= 0) {
+    if (d.rows && ch.slot < 0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f4* o = reinterpret_cast<f4*>(d.part + ((size_t)ch.slot * a.R + r + j) * d.C + c0);
-        o[0] = f4{acc[f][0][j], acc[f][1][j], acc[f][2][j], acc[f][3][j]};
-        o[1] = f4{acc[f][4][j], acc[f][5][j], acc[f][6][j], acc[f][7][j]};
-      }
-    } else if (d.rows) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int kk = 0; kk < 2; ++kk) {
+        const int k = 2 * wave + kk;
         Quad4 o;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o.v[j] = from_f32<TX>(acc[f][k][j]);
+        for (int j = 0; j < 4; ++j) o.v[j] = from_f32<TX>(total(f, k, j));
         *reinterpret_cast<Quad4*>(static_cast<TX*>(d.out) + outer_at(a, d, ch.e, r, c0 + k)) = o;
       }
     } else {
+      float v[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int k = 0; k < 8; ++k) v[k] = total(f, k, wave);
+      if (ch.slot >= 0) {
+        f4* o = reinterpret_cast<f4*>(d.part + ((size_t)ch.slot * a.R + r + wave) * d.C + c0);
+        o[0] = f4{v[0], v[1], v[2], v[3]};
+        o[1] = f4{v[4], v[5], v[6], v[7]};
+      } else {
         Eight o;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o.v[k] = from_f32<TX>(acc[f][k][j]);
-        *reinterpret_cast<Eight*>(static_cast<TX*>(d.out) + outer_at(a, d, ch.e, r + j, c0)) = o;
+        for (int k = 0; k < 8; ++k) o.v[k] = from_f32<TX>(v[k]);
+        *reinterpret_cast<Eight*>(static_cast<TX*>(d.out) + outer_at(a, d, ch.e, r + wave, c0)) = o;
       }
     }
   }
@@ -450,9 +472,11 @@ __device__ __forceinline__ void outer_16(const AdaptOuter& a, const AdaptOuter::
 
 template <int RF, bool FEW>
 __device__ __forceinline__ void outer_32(const AdaptOuter& a, const AdaptOuter::Part& d, const AdaptChunk& ch, uint64_t mine,
-                                         int c_wave, int r0) {
+                                         int c_group, int r0, float* s_sum) {
   constexpr int U = 4;  // steps of four positions
-  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4, c0 = c_wave + 4 * i;
+  int w0, w1;
+  wave_part(ch, w0, w1);
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4, c0 = c_group + 4 * i;
   const bool in = c0 < d.C;
   f4 acc[RF][4], mn[U];
   float vn[RF][U];
@@ -464,7 +488,7 @@ __device__ __forceinline__ void outer_32(const AdaptOuter& a, const AdaptOuter::
   auto rows_of = [&](int p) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int t = max(min(p + 4 * u + g, ch.p1 - 1), ch.p0);
+      const int t = max(min(p + 4 * u + g, w1 - 1), 0);
       row[u] = d.order ? d.order[t] : t;
     }
   };
@@ -475,7 +499,7 @@ __device__ __forceinline__ void outer_32(const AdaptOuter& a, const AdaptOuter::
       mn[u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int f = 0; f < RF; ++f) vn[f][u] = 0.0f;
-      if (t < ch.p1 && (!FEW || (mine >> t & 1))) {
+      if (t < w1 && (!FEW || (mine >> t & 1))) {
         if (in) {
           const float* q = static_cast<const float*>(d.m) + (size_t)row[u] * d.ldm + c0;
           if (d.vec_m) mn[u] = *reinterpret_cast<const f4*>(q);
@@ -486,10 +510,10 @@ __device__ __forceinline__ void outer_32(const AdaptOuter& a, const AdaptOuter::
       }
     }
   };
-  rows_of(ch.p0);
-  fetch(ch.p0);
-  rows_of(ch.p0 + 4 * U);
-  for (int p = ch.p0; p < ch.p1; p += 4 * U) {
+  rows_of(w0);
+  fetch(w0);
+  rows_of(w0 + 4 * U);
+  for (int p = w0; p < w1; p += 4 * U) {
     f4 m[U];
     float v[RF][U];
 #pragma unroll
@@ -507,22 +531,33 @@ __device__ __forceinline__ void outer_32(const AdaptOuter& a, const AdaptOuter::
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[f][k] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[f][u], m[u][k], acc[f][k], 0, 0, 0);
   }
+  const int wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int f = 0; f < RF; ++f)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s_sum[(((wave * RF + f) * 4 + k) * 4 + j) * 64 + lane] = acc[f][k][j];
+  __syncthreads();
+  auto total = [&](int f, int k, int j) __attribute__((always_inline)) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) v += s_sum[(((w * RF + f) * 4 + k) * 4 + j) * 64 + lane];
+    return v;
+  };
   if (!in) return;
 #pragma unroll
   for (int f = 0; f < RF; ++f) {
     const int r = r0 + 16 * f + 4 * g;
     if (r >= a.R) continue;
     float* out = static_cast<float*>(d.out);
-    if (ch.slot < 0 && d.rows) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) *reinterpret_cast<f4*>(out + outer_at(a, d, ch.e, r, c0 + k)) = acc[f][k];
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<f4*>(ch.slot >= 0 ? d.part + ((size_t)ch.slot * a.R + r + j) * d.C + c0
-                                            : out + outer_at(a, d, ch.e, r + j, c0)) =
-            f4{acc[f][0][j], acc[f][1][j], acc[f][2][j], acc[f][3][j]};
-    }
+    if (ch.slot < 0 && d.rows)
+      *reinterpret_cast<f4*>(out + outer_at(a, d, ch.e, r, c0 + wave)) =
+          f4{total(f, wave, 0), total(f, wave, 1), total(f, wave, 2), total(f, wave, 3)};
+    else
+      *reinterpret_cast<f4*>(ch.slot >= 0 ? d.part + ((size_t)ch.slot * a.R + r + wave) * d.C + c0
+                                          : out + outer_at(a, d, ch.e, r + wave, c0)) =
+          f4{total(f, 0, wave), total(f, 1, wave), total(f, 2, wave), total(f, 3, wave)};
   }
 }
 
@@ -531,22 +566,23 @@ __device__ __forceinline__ void outer_32(const AdaptOuter& a, const AdaptOuter::
 template <class TX, int RF, bool FEW>
 __global__ __launch_bounds__(256, 2) void k_adapt_outer(AdaptOuter a, int x0, int runs) {
   constexpr int kCols = std::is_same<TX, float>::value ? 64 : 128;
+  __shared__ __align__(16) float s_sum[4 * RF * 16 * kCols];
   const bool second = (int)blockIdx.x >= x0;
   const AdaptOuter::Part& d = a.part[second];
-  const int c = ((blockIdx.x - (second ? x0 : 0)) * 4 + (threadIdx.x >> 6)) * kCols, r0 = blockIdx.z * 16 * RF;
+  const int c = (blockIdx.x - (second ? x0 : 0)) * kCols, r0 = blockIdx.z * 16 * RF;
   if constexpr (FEW) {  // an adapter each; without tokens its sums are zeros
     const int lane = threadIdx.x & 63;
     const uint64_t mine = __ballot(lane < a.T && (a.ids ? a.ids[min(lane, a.T - 1)] : 0) == (int)blockIdx.y);
     const AdaptChunk ch{(int)blockIdx.y, 0, mine ? a.T : 0, -1};
-    if constexpr (std::is_same<TX, float>::value) outer_32<RF, true>(a, d, ch, mine, c, r0);
-    else outer_16<TX, RF, true>(a, d, ch, mine, c, r0);
+    if constexpr (std::is_same<TX, float>::value) outer_32<RF, true>(a, d, ch, mine, c, r0, s_sum);
+    else outer_16<TX, RF, true>(a, d, ch, mine, c, r0, s_sum);
     return;
   }
   if ((int)blockIdx.y >= runs) {
     const int e = blockIdx.y - runs;
     if (a.order.offsets[e + 1] != a.order.offsets[e]) return;
     const int rows = min(16 * RF, a.R - r0);
-    for (int k = threadIdx.x & 63; k < rows * kCols; k += 64) {
+    for (int k = threadIdx.x; k < rows * kCols; k += 256) {
       const int r = d.rows ? k % rows : k / kCols, cc = c + (d.rows ? k / rows : k % kCols);
       if (cc < d.C) static_cast<TX*>(d.out)[outer_at(a, d, e, r0 + r, cc)] = from_f32<TX>(0.0f);
     }
@@ -554,8 +590,8 @@ __global__ __launch_bounds__(256, 2) void k_adapt_outer(AdaptOuter a, int x0, in
   }
   if ((int)blockIdx.y >= *a.order.n_chunks) return;
   const AdaptChunk ch = a.order.chunks[blockIdx.y];
-  if constexpr (std::is_same<TX, float>::value) outer_32<RF, false>(a, d, ch, 0, c, r0);
-  else outer_16<TX, RF, false>(a, d, ch, 0, c, r0);
+  if constexpr (std::is_same<TX, float>::value) outer_32<RF, false>(a, d, ch, 0, c, r0, s_sum);
+  else outer_16<TX, RF, false>(a, d, ch, 0, c, r0, s_sum);
 }
 
 // Adapters of several runs: their partial sums in ascending order.
@@ -621,7 +657,7 @@ void down_launch(const AdaptDown& a, hipStream_t st) {
 }
 template <class TX>
 void outer_launch(const AdaptOuter& a, hipStream_t st) {
-  const int per = std::is_same<TX, float>::value ? 256 : 512, len = adapt_chunk_len(a.T);
+  const int per = std::is_same<TX, float>::value ? 64 : 128, len = adapt_chunk_len(a.T);
   auto cols = [&](int k, int w) { return a.part[k].out ? (a.part[k].C + w - 1) / w : 0; };
   const int x = cols(0, per) + cols(1, per);
   if (!a.order.order) {

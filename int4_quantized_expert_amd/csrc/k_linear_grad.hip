@@ -156,7 +156,8 @@ __global__ __launch_bounds__(1024) void k_linear_dz(DzArgs d) {
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 16; ++i) m = max(m, s_max[i][tk]);
-  const int sh = scale_shift(m);
+  // at most 2^100, so that the adapters' part, which takes the same power of two, stays in range beside the smallest scales
+  const int sh = min(scale_shift(m), 100);
   const bool finite = m < 0x7F800000u;
   if (in && g0 == 0) a.sh[p] = sh;
   const size_t base = (size_t)(p >> 5) * a.nbp * 1024 + (size_t)(p & 31) * 8;

@@ -54,6 +54,22 @@ def test_whole_numbers_are_exact(T, N, K, Rk, n, how, bits, group, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,N,K,Rk,n", [(2000, 64, 96, 8, 1024), (6000, 64, 64, 16, 3), (2500, 640, 64, 24, 1024),
+                                        (500, 1024, 96, 8, 4), (500, 1024, 96, 8, 5), (70, 8192, 32, 128, 33)])
+def test_many_tokens_and_adapters_of_whole_numbers(T, N, K, Rk, n, dtype):
+    """Few rows for many tokens, 1024 adapters, tokens with and without an order."""
+    rng = np.random.default_rng(T + N)
+    q, s, codes, scales = H.weights(rng, N, K, 4, 0, whole=True)
+    ad, a, b, sc = H.adapters(rng, n, Rk, N, K, dtype, whole=True)
+    ids, i = H.ids_of(rng, T, n, "mix")
+    x, x64 = H.matrix(rng, T, K, dtype, whole=4)
+    y, _ = _call(moe.LinearConfig(N, K), codes, scales, ad, ids, x, dtype=dtype)
+    rows = np.sort(rng.permutation(T)[:400])
+    want = x64[rows] @ R.weights(q, s).T + R.low_rank(x64[rows], a, b, sc, R.chosen(i, n, T)[rows], False)[0]
+    assert torch.equal(y.cpu()[rows], torch.from_numpy(want.astype(np.float32)).to(DT[dtype]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("act", list(ACT))
 @pytest.mark.parametrize("T,N,K,bits,group,Rk,n,how", [(1, 256, 544, 4, 0, 16, 4, "mix"), (5, 64, 256, 4, 32, 8, 2, "mix"),
                                                        (31, 192, 96, 8, 0, 24, 3, "runs"), (140, 4096, 320, 4, 64, 48, 5, "mix"),

@@ -97,6 +97,70 @@ def test_against_64_bits(T, N, K, bits, group, Rk, n, how, act, dtype):
         assert ok.all(), (name, g.double().cpu().numpy()[~ok][:4], v[~ok][:4], err[~ok][:4])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,N,K,Rk,n,how", [(64, 128, 288, 16, 70, "mix"), (65, 128, 288, 16, 70, "mix"), (64, 64, 96, 128, 1, "all"),
+                                            (2500, 64, 224, 8, 1024, "mix"), (4500, 128, 96, 24, 3, "runs"),
+                                            (9000, 64, 160, 8, 2, "runs"), (1024, 64, 16384, 16, 2, "runs")])
+def test_many_tokens_and_adapters_of_whole_numbers(T, N, K, Rk, n, how, dtype):
+    """The borders between the forms for few and many tokens, adapters' sums in one run and in several, 1024 adapters."""
+    rng = np.random.default_rng(T + N + K)
+    q, s, codes, scales = H.weights(rng, N, K, 4, 0, whole=True)
+    a, b = (torch.from_numpy((rng.integers(-1, 2, sh) * (rng.random(sh) < 0.2)).astype(np.float32)).to(DT[dtype])
+            for sh in ((n, Rk, K), (n, N, Rk)))
+    sc = torch.from_numpy(rng.choice([0.5, 1.0], n).astype(np.float32))
+    ad = moe.Adapters(a.to(DEV), b.to(DEV), sc.to(DEV))
+    ids, i = H.ids_of(rng, T, n, how)
+    x, x64 = H.matrix(rng, T, K, dtype, whole=1)
+    dy, dy64 = H.matrix(rng, T, N, dtype, whole=1)
+    got = _call(moe.LinearConfig(N, K), codes, scales, dy, ad, ids, x, dtype=dtype)
+    want = R.backward(q, s, x64, a.double().numpy(), b.double().numpy(), sc.double().numpy(), i, dy64, None, dtype)
+    for g, (v, _) in zip(got, want):
+        assert np.abs(v).max() < 2 ** 20
+        assert torch.equal(g.cpu(), torch.from_numpy(v.astype(np.float32)).to(DT[dtype]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [3, 100])
+@pytest.mark.parametrize("size", [2.0 ** -110, 2.0 ** -40, 2.0 ** 40])
+def test_scales_far_from_one(size, T, dtype):
+    """Row scales of 2^-110 leave the adapters' part as it is; others are exact powers of two of the same sums."""
+    rng = np.random.default_rng(T)
+    N, K, n = 128, 96, 2
+    q, s, codes, scales = H.weights(rng, N, K, 4, 0, whole=True)
+    scales.mul_(size)
+    ad, a, b, sc = H.adapters(rng, n, 8, N, K, dtype)
+    ids, i = H.ids_of(rng, T, n, "one")
+    x, x64 = H.matrix(rng, T, K, dtype)
+    dy, dy64 = H.matrix(rng, T, N, dtype)
+    got = _call(moe.LinearConfig(N, K), codes, scales, dy, ad, ids, x, dtype=dtype)
+    want = R.backward(q, s * size, x64, a, b, sc, i, dy64, None, dtype)
+    for g, (v, err) in zip(got, want):
+        assert R.within(g.double().cpu().numpy(), v, err, dtype).all()
+
+
+def test_two_streams_with_a_workspace_each():
+    rng = np.random.default_rng(8)
+    T, N, K, n = 300, 256, 192, 3
+    _, _, codes, scales = H.weights(rng, N, K, 4, 0)
+    ad, *_ = H.adapters(rng, n, 16, N, K, "bf16")
+    cfg = moe.LinearConfig(N, K)
+    x = [H.matrix(rng, T, K, "bf16")[0] for _ in range(2)]
+    dy = [H.matrix(rng, T, N, "bf16")[0] for _ in range(2)]
+    ids = [H.ids_of(rng, T, n, "mix")[0] for _ in range(2)]
+    want = [_call(cfg, codes, scales, dy[k], ad, ids[k], x[k], dtype="bf16") for k in range(2)]
+    got = [[torch.empty_like(t) for t in want[k]] for k in range(2)]
+    ws = [H.space(moe.moe_linear_backward_workspace_bytes(cfg, ad, T)) for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for k in range(2):
+            moe.moe_linear_backward(cfg, codes, scales, dy[k], got[k][0], ws[k], adapters=ad, ids=ids[k], x=x[k],
+                                    d_a=got[k][1], d_b=got[k][2], stream=streams[k])
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert all(torch.equal(p, q) for p, q in zip(got[k], want[k]))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_parts_alone_and_equal_calls(dtype):
     """Each gradient alone is what all of them together give, and a call gives the same bits again."""
