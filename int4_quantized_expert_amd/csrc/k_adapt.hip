@@ -356,20 +356,29 @@ __device__ __forceinline__ void outer_16(const AdaptOuter& a, const AdaptOuter::
   const int begin = w0 & ~7, last = max(w1 - 1, 0) & ~7;
   Granule<TX> mn[8];
   f8v vn[RF];
-  int row[8];  // rows of m two steps ahead
+  // Rows of m two steps ahead. Positions outside the part take the row of its first: v is 0 there, and what that row holds
+  // is in the sum anyway, so that the loads need no conditions.
+  int row[8];
+  const int any = min(w0, max(w1 - 1, 0)), row0 = !FEW && d.order ? d.order[any] : any;
+  const TX* m_col = static_cast<const TX*>(d.m) + min(c0, d.C - 8);
   auto rows_of = [&](int p) __attribute__((always_inline)) {
+    const int t0 = p + 8 * g;
+    if (!FEW && d.order) {
+      const i4v* o = reinterpret_cast<const i4v*>(d.order + max(min(t0, last), begin));
+      const i4v lo = o[0], hi = o[1];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int t = max(min(p + 8 * g + j, w1 - 1), 0);
-      row[j] = d.order ? d.order[t] : t;
+      for (int j = 0; j < 8; ++j) row[j] = counts(t0 + j) ? (j < 4 ? lo[j & 3] : hi[j & 3]) : row0;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) row[j] = counts(t0 + j) ? t0 + j : row0;
     }
   };
   auto fetch = [&](int p) __attribute__((always_inline)) {
     const int t0 = p + 8 * g;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      mn[j] = Granule<TX>{};
-      if (in && counts(t0 + j)) load8(static_cast<const TX*>(d.m) + (size_t)row[j] * d.ldm + c0, d.vec_m, mn[j]);
+      if constexpr (FEW) mn[j] = Granule<TX>{};
+      if (!FEW || counts(t0 + j)) load8(m_col + (size_t)row[j] * d.ldm, d.vec_m, mn[j]);
     }
 #pragma unroll
     for (int f = 0; f < RF; ++f) vn[f] = *reinterpret_cast<const f8v*>(vt[f] + (size_t)min(t0, last) * a.R);
@@ -485,28 +494,29 @@ __device__ __forceinline__ void outer_32(const AdaptOuter& a, const AdaptOuter::
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[f][k] = f4{0.0f, 0.0f, 0.0f, 0.0f};
   int row[U];
+  const float* m_col = static_cast<const float*>(d.m) + min(c0, d.C - 4);
   auto rows_of = [&](int p) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int t = max(min(p + 4 * u + g, w1 - 1), 0);
-      row[u] = d.order ? d.order[t] : t;
+      row[u] = !FEW && d.order ? d.order[t] : t;
     }
   };
   auto fetch = [&](int p) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int t = p + 4 * u + g;
-      mn[u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+      const bool own = t < w1 && (!FEW || (mine >> t & 1));
+      if constexpr (FEW) mn[u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (!FEW || own) {  // positions behind the part: its last one's row, times 0
+        const float* q = m_col + (size_t)row[u] * d.ldm;
+        if (d.vec_m) mn[u] = *reinterpret_cast<const f4*>(q);
+        else mn[u] = f4{q[0], q[1], q[2], q[3]};
+      }
 #pragma unroll
-      for (int f = 0; f < RF; ++f) vn[f][u] = 0.0f;
-      if (t < w1 && (!FEW || (mine >> t & 1))) {
-        if (in) {
-          const float* q = static_cast<const float*>(d.m) + (size_t)row[u] * d.ldm + c0;
-          if (d.vec_m) mn[u] = *reinterpret_cast<const f4*>(q);
-          else mn[u] = f4{q[0], q[1], q[2], q[3]};
-        }
-#pragma unroll
-        for (int f = 0; f < RF; ++f) vn[f][u] = d.v[(size_t)t * a.R + min(r0 + 16 * f + i, a.R - 1)];
+      for (int f = 0; f < RF; ++f) {
+        const float v = d.v[(size_t)max(min(t, w1 - 1), 0) * a.R + min(r0 + 16 * f + i, a.R - 1)];
+        vn[f][u] = own ? v : 0.0f;
       }
     }
   };
