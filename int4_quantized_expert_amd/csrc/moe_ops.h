@@ -44,7 +44,7 @@ struct AdaptChunk {
 // Runs of 16 positions for the products, and chunks for the gradients' sums over tokens: T positions make at most 16 of
 // the latter, and adapters of several chunks have at most kAdaptSlots together (count > len gives at most 2 count / len).
 constexpr int kAdaptSlots = 32;
-inline int adapt_chunk_len(int64_t T) { return T <= 4096 ? 256 : (int)((T + 511) / 512 * 32); }
+inline int adapt_chunk_len(int64_t T) { return T <= 1024 ? 256 : T <= 8192 ? 512 : (int)((T + 511) / 512 * 32); }
 inline int64_t adapt_max_chunks(int64_t T, int n) { return 16 + (T < n ? T : n); }
 inline int64_t adapt_max_runs(int64_t T, int n) { return T / 16 + (T < n ? T : n); }
 struct AdaptOrder {

@@ -54,14 +54,15 @@ def test_whole_numbers_are_exact(T, N, K, Rk, n, how, bits, group, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("T,N,K,Rk,n", [(2000, 64, 96, 8, 1024), (6000, 64, 64, 16, 3), (2500, 640, 64, 24, 1024),
-                                        (500, 1024, 96, 8, 4), (500, 1024, 96, 8, 5), (70, 8192, 32, 128, 33)])
-def test_many_tokens_and_adapters_of_whole_numbers(T, N, K, Rk, n, dtype):
+@pytest.mark.parametrize("T,N,K,Rk,n,how", [(2000, 64, 96, 8, 1024, "mix"), (6000, 64, 64, 16, 3, "mix"), (2500, 640, 64, 24, 1024, "mix"),
+                                            (500, 1024, 96, 8, 4, "mix"), (500, 1024, 96, 8, 5, "mix"), (70, 8192, 32, 128, 33, "mix"),
+                                            (100, 64, 96, 64, 1, "all"), (700, 1088, 96, 40, 2, "all")])
+def test_many_tokens_and_adapters_of_whole_numbers(T, N, K, Rk, n, how, dtype):
     """Few rows for many tokens, 1024 adapters, tokens with and without an order."""
     rng = np.random.default_rng(T + N)
     q, s, codes, scales = H.weights(rng, N, K, 4, 0, whole=True)
     ad, a, b, sc = H.adapters(rng, n, Rk, N, K, dtype, whole=True)
-    ids, i = H.ids_of(rng, T, n, "mix")
+    ids, i = H.ids_of(rng, T, n, how)
     x, x64 = H.matrix(rng, T, K, dtype, whole=4)
     y, _ = _call(moe.LinearConfig(N, K), codes, scales, ad, ids, x, dtype=dtype)
     rows = np.sort(rng.permutation(T)[:400])
@@ -170,6 +171,27 @@ def test_captured_and_replayed_on_changing_inputs(T, N):
         got = y.clone()
         want, _ = _call(cfg, codes, scales, ad, ids, x, dtype="bf16")
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T", [3, 70])
+def test_rows_far_apart(T):
+    """Rows whose offsets pass 2^31 elements, of the activations, the residual, the result and the values kept."""
+    rng = np.random.default_rng(T)
+    N, K = 8192, 64
+    far = (1 << 31) // (T - 1) // 8 * 8 + 64
+    _, _, codes, scales = H.weights(rng, N, K, 4, 0)
+    ad, *_ = H.adapters(rng, 2, 8, N, K, "bf16")
+    ids, _ = H.ids_of(rng, T, 2, "mix")
+    cfg = moe.LinearConfig(N, K, act=ACT["silu"])
+    x, _ = H.matrix(rng, T, K, "bf16")
+    res, _ = H.matrix(rng, T, N, "bf16")
+    y, z = _call(cfg, codes, scales, ad, ids, x, res=res, keep=True, dtype="bf16")
+    spread = [torch.empty((T - 1) * far + N, dtype=torch.bfloat16, device=DEV).as_strided((T, c), (far, 1)) for c in (K, N, N, N)]
+    spread[0].copy_(x)
+    spread[1].copy_(res)
+    ws = H.space(moe.moe_linear_adapted_workspace_bytes(cfg, ad, T))
+    moe.moe_linear_adapted(cfg, codes, scales, ad, ids, spread[0], spread[2], ws, residual=spread[1], pre=spread[3])
+    assert torch.equal(spread[2], y) and torch.equal(spread[3], z)
 
 
 def test_two_streams_with_a_workspace_each():

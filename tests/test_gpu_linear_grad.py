@@ -29,7 +29,7 @@ def _call(cfg, codes, scales, dy, ad=None, ids=None, x=None, z=None, res=None, d
     return dx, da, db
 
 
-SHAPES = [(1, 64, 32), (2, 128, 2080), (5, 320, 96), (16, 64, 160), (31, 512, 64), (33, 576, 224), (64, 192, 544),
+SHAPES = [(1, 64, 32), (100, 64, 32), (2, 128, 2080), (5, 320, 96), (16, 64, 160), (31, 512, 64), (33, 576, 224), (64, 192, 544),
           (129, 320, 1088), (200, 1088, 4160), (300, 128, 8192), (191, 704, 6080), (600, 64, 8128), (1024, 64, 16384)]
 
 
@@ -99,7 +99,7 @@ def test_against_64_bits(T, N, K, bits, group, Rk, n, how, act, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("T,N,K,Rk,n,how", [(64, 128, 288, 16, 70, "mix"), (65, 128, 288, 16, 70, "mix"), (64, 64, 96, 128, 1, "all"),
-                                            (2500, 64, 224, 8, 1024, "mix"), (4500, 128, 96, 24, 3, "runs"),
+                                            (2500, 64, 224, 8, 1024, "mix"), (4500, 128, 96, 24, 3, "runs"), (300, 128, 32, 16, 2, "all"),
                                             (9000, 64, 160, 8, 2, "runs"), (1024, 64, 16384, 16, 2, "runs")])
 def test_many_tokens_and_adapters_of_whole_numbers(T, N, K, Rk, n, how, dtype):
     """The borders between the forms for few and many tokens, adapters' sums in one run and in several, 1024 adapters."""
@@ -136,6 +136,30 @@ def test_scales_far_from_one(size, T, dtype):
     want = R.backward(q, s * size, x64, a, b, sc, i, dy64, None, dtype)
     for g, (v, err) in zip(got, want):
         assert R.within(g.double().cpu().numpy(), v, err, dtype).all()
+
+
+@pytest.mark.parametrize("T", [3, 70])
+def test_rows_far_apart(T):
+    """Rows whose offsets pass 2^31 elements, of every matrix of the call."""
+    rng = np.random.default_rng(T)
+    N, K = 128, 96
+    far = (1 << 31) // (T - 1) // 8 * 8 + 64
+    _, _, codes, scales = H.weights(rng, N, K, 4, 0)
+    ad, *_ = H.adapters(rng, 2, 8, N, K, "bf16")
+    ids, _ = H.ids_of(rng, T, 2, "mix")
+    cfg = moe.LinearConfig(N, K, act=ACT["silu"])
+    x, _ = H.matrix(rng, T, K, "bf16")
+    z, _ = H.matrix(rng, T, N, "bf16", spread=False)
+    dy, _ = H.matrix(rng, T, N, "bf16")
+    want = _call(cfg, codes, scales, dy, ad, ids, x, z, x, dtype="bf16")
+    sx, sz, sdy, sdx = (torch.empty((T - 1) * far + N, dtype=torch.bfloat16, device=DEV).as_strided((T, c), (far, 1))
+                        for c in (K, N, N, K))
+    for to, of in ((sx, x), (sz, z), (sdy, dy)):
+        to.copy_(of)
+    da, db = torch.empty_like(ad._keep[0]), torch.empty_like(ad._keep[1])
+    ws = H.space(moe.moe_linear_backward_workspace_bytes(cfg, ad, T))
+    moe.moe_linear_backward(cfg, codes, scales, sdy, sdx, ws, pre=sz, adapters=ad, ids=ids, x=sx, d_a=da, d_b=db, residual=sx)
+    assert all(torch.equal(p, q) for p, q in zip((sdx, da, db), want))
 
 
 def test_two_streams_with_a_workspace_each():
