@@ -38,9 +38,11 @@ hipError_t run(LinearArgs& a, int bits, const moe_adapters* ad, const int32_t* i
     AdaptDown d{};
     d.T = a.T, d.R = a.R, d.n_ad = a.n_ad, d.parts = 1, d.by_token = few, d.few = adapt_few(a.T, a.R);
     d.scale = ad->scale;
-    // few tokens, and not many of few adapters, do without an order: 32 neighbours then have at most kMixed of them
-    // (191 tokens, rank 8, four adapters, 6144 x 2048 int8: 29.0 us a call, 35.7)
-    const bool sorted = ids && !(adapt_few(a.T, a.R) && (few || a.n_ad <= kMixed));
+    // Few tokens do without an order, and so do any number of one adapter (2,048-token calls save 7 us of 70 to 310), where
+    // tokens that have none are computed with it and left out, and not many of a few adapters: 32 neighbours then have at
+    // most kMixed of them (191 tokens, rank 8, four adapters, 6144 x 2048 int8: 29.7 us a call, 35.7; 1,500 tokens of four
+    // adapters one by one would lose 7 to 14).
+    const bool sorted = ids && a.n_ad > 1 && !(adapt_few(a.T, a.R) && (few || a.n_ad <= kMixed));
     const AdaptOrder o{reinterpret_cast<int32_t*>(w + p.order), reinterpret_cast<int32_t*>(w + p.ad),
                        reinterpret_cast<int32_t*>(w + p.n_runs), reinterpret_cast<AdaptChunk*>(w + p.runs)};
     if (sorted) {

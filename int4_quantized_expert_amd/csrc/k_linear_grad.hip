@@ -102,7 +102,9 @@ __device__ __forceinline__ void hold(const f8v& w, uint32_t& m, Held<TX>& o) {
 
 // As k_linear_x, from dz: TOK positions a workgroup, the largest of a token first. kind: 0 no activation, 1 one row at a
 // time, 2 SwiGLU. A row's values stay in registers between the search for the largest and the conversion as far as they fit
-// (kRounds items of a lane), the rest is computed twice. One position a workgroup where there are few.
+// (kRounds items of a lane), the rest is computed twice. One position a workgroup where there are few. 2,048 tokens of 12288
+// rows, SwiGLU: 31 to 37 us for 125 MB (20 at the rate of a large read); a workgroup a compute unit, its reading, its
+// arithmetic and its writing one after the other. Written one position at a time, in pieces of 16 bytes, it takes 60.
 template <class TX, int KIND, int TOK>
 __global__ __launch_bounds__(1024) void k_linear_dz(DzArgs d) {
   constexpr int kLanes = 1024 / TOK, V = KIND == 2 ? 2 : 1;
@@ -235,7 +237,8 @@ __global__ __launch_bounds__(256) void k_group_scales(const float* __restrict__ 
 // ------------------------------------------------------------ few tokens
 // Reading the codes is what counts: a wavefront takes 64 columns and a part of the rows for all tokens, with the codes of
 // kAhead steps (64 rows) in flight; it waits for no other before the sum of the workgroup's four. The parts' sums
-// [part][T][N] are added by k_few_add, with the adapters' part and the residual.
+// [part][T][N] are added by k_few_add, with the adapters' part and the residual. 6144 x 6144 int4, bf16: 9.3 us for one
+// token, 11.6 for 32, 14.3 for 64 in two fragments, and 4 to add; 19 MB of codes take 3.0 to 4.0.
 constexpr int kFewGroups = 512;  // workgroups wanted
 constexpr int kFewWaves = 4;
 template <class TX, int TT, int W, int GSH>
