@@ -1182,6 +1182,9 @@ __global__ __launch_bounds__(256) void k_linear_add(LinearArgs a, int row_tiles,
 
 // As many tiles as fill the card twice over run in workgroups of four wavefronts, up to 256 of the rest with eight that share
 // the rows summed over; what is left then, up to 128, is cut into parts of the sum, so that 256 workgroups run again.
+// 2,048 tokens, 12288 rows x 6144 columns, bf16: 256 tiles 180 us, the other 128 in two parts 97 and 9 to add, 1.08 PFLOP/s of
+// matrix instructions while tiles run (128 as 256 tiles of half the tokens 128 us); bound as the product is, the codes' way
+// through LDS hides behind it.
 constexpr int kMinSteps = 4;  // of a part
 inline int tile_parts(int left, int steps) { return std::max(1, std::min(kUnits / left, steps / kMinSteps)); }
 template <class TX, int W, int GSH>
