@@ -438,8 +438,8 @@ size_t moe_linear_backward_workspace_bytes(const moe_linear_config* cfg, const m
  * NULL or dx itself: the gradients of several products of one x are added so. The gradient of the forward call's residual
  * is dy. The weights, the bias and the scales have none. dx overlaps no input but residual, d_a and d_b none.
  * W^T dz is summed in fp32 over one rounding of dz times its row's scale (2^-12 of each term, fp32 2^-23); group scales
- * cost 2^-10 more of each weight for bf16, 2^-19 for fp16 and fp32, and a scale below 2^-14 of its row's largest is taken
- * to 2^-25 of that one. A token whose dz holds an infinity or NaN
+ * cost 2^-10 more of each weight for bf16, 2^-19 for fp16 and fp32, and a scale below 2^-26 of its row's largest is taken
+ * to 2^-36 of that one. A token whose dz holds an infinity or NaN
  * has a dx of them, and so have the gradients of its adapter; others are not touched. Sums run in a fixed order: equal calls
  * give equal bits. Errors: MOE_E_NULL, MOE_E_SHAPE, MOE_E_ARG, MOE_E_WORKSPACE, MOE_E_HIP. */
 int32_t moe_linear_backward(const moe_linear_config* cfg, const uint8_t* codes, const float* scales,

@@ -2,9 +2,9 @@
 //   dx = W^T dz + s A^T (B^T dz),  dB = sum over tokens of dz (s A x)^T,  dA = sum over tokens of (s B^T dz) x^T.
 // W^T dz runs in the product's tiles, summing over the weight rows. Row scales are multiplied into dz, in fp32 before its
 // one rounding to fp16 (relative 2^-12; fp32 gradients keep two halves, 2^-23). Group scales differ along a row: the power
-// of two of a row's largest is multiplied into dz, without loss, what is left of them, at most 1, into the codes, as fp16
-// (relative 2^-11, or 2^-25 of the row's largest for scales that are less than 2^-14 of it; fp16 and fp32 gradients keep
-// two parts, 2^-19). dz is kept in the call's type for the adapters' sums, as autograd would hand it on.
+// of two of a row's largest is multiplied into dz, without loss, what is left of them, at most 2^12 (times a code of at
+// most 8 it fits fp16), into the codes, as fp16 (relative 2^-11, or 2^-36 of the row's largest for scales that are less than
+// 2^-26 of it; fp16 and fp32 gradients keep two parts, 2^-19). dz is kept in the call's type for the adapters' sums, as autograd would hand it on.
 #define MOE_ADAPTED 1
 #define MOE_TRANSPOSED 1
 #include "linear_kernels.h"
@@ -217,7 +217,8 @@ __global__ __launch_bounds__(256) void k_group_scales(const float* __restrict__ 
   s_max[wave][lane] = m;
   __syncthreads();
   m = fmaxf(fmaxf(s_max[0][lane], s_max[1][lane]), fmaxf(s_max[2][lane], s_max[3][lane]));
-  const int e = m > 0.0f && m < INFINITY ? __builtin_amdgcn_frexp_expf(m) : 0;  // m = f 2^e, f in [1/2, 1)
+  // m = f 2^(e + 12), f in [1/2, 1)
+  const int e = m > 0.0f && m < INFINITY ? __builtin_amdgcn_frexp_expf(m) - 12 : 0;
   if (wave == 0) mul[blockIdx.x * 64 + lane] = ldexpf(1.0f, e);
   // place of row l in the order of the codes: eight rows 0 4 1 5 2 6 3 7
   const int r = lane & 7, at = (lane & ~7) + (r < 4 ? 2 * r : 2 * (r - 4) + 1);

@@ -119,6 +119,28 @@ def test_many_tokens_and_adapters_of_whole_numbers(T, N, K, Rk, n, how, dtype):
         assert torch.equal(g.cpu(), torch.from_numpy(v.astype(np.float32)).to(DT[dtype]))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T", [3, 100])
+@pytest.mark.parametrize("group", [32, 64])
+def test_group_scales_far_apart(group, T, dtype):
+    """Scales of a row from 1 down to 2^-20 of it, rows of sizes from 2^-30 to 2^10, columns with small scales only."""
+    rng = np.random.default_rng(T + group)
+    N, K = 192, 256
+    q = rng.integers(-8, 8, (N, K)).astype(np.int8)
+    s = 2.0 ** rng.uniform(-20, 0, (N, K // group)) * 2.0 ** rng.uniform(-30, 10, (N, 1))
+    s[:, 1] = s.max(axis=1) * 2.0 ** -18
+    s = s.astype(np.float32)
+    u = (q & 15).astype(np.uint8)
+    codes = torch.empty(N * K // 2, dtype=torch.uint8, device=DEV)
+    moe.moe_tile_int4(torch.from_numpy(u[:, 0::2] | (u[:, 1::2] << 4)).to(DEV), codes)
+    scales = torch.empty(s.size, device=DEV)
+    moe.moe_tile_group_scales(torch.from_numpy(s).to(DEV), scales)
+    dy, dy64 = H.matrix(rng, T, N, dtype)
+    dx, _, _ = _call(moe.LinearConfig(N, K, 4, group), codes, scales, dy, dtype=dtype)
+    (v, err), _, _ = R.backward(q.astype(np.float64), s.astype(np.float64), None, None, None, None, None, dy64, None, dtype)
+    assert R.within(dx.double().cpu().numpy(), v, err, dtype).all()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T", [3, 100])
 @pytest.mark.parametrize("size", [2.0 ** -110, 2.0 ** -40, 2.0 ** 40])

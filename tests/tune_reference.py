@@ -116,9 +116,10 @@ def backward(q, s, x, a, b, sc, ids, dy, z, dtype, act="none", res=None):
     top = np.abs(dz) * np.abs(s).max(axis=1)[None, :]  # what the token's power of two is made for
     ex = (ez + (step + (N + 24) * UNIT) * np.abs(dz)) @ np.abs(w)
     ex = ex + 2.0 ** -38 * top.max(axis=1, keepdims=True) * np.abs(q).sum(axis=0)[None, :]
-    # group scales far below their row's largest: 2^-25 of that one
+    # group scales far below their row's largest: half a step of fp16's smallest, 2^-25, over the power of two that puts the
+    # largest in [2^11, 2^12)
     if s.shape[1] > 1:
-        ex = ex + 2.0 ** -25 * (top @ np.abs(q))
+        ex = ex + 2.0 ** -36 * (top @ np.abs(q))
     da = db = ea = eb = None
     if a is not None:
         n, R, K = a.shape
