@@ -71,6 +71,7 @@ __global__ __launch_bounds__(64 * kOrderWaves) void k_adapt_order(const int32_t*
     const bool in = t + lane < t1;
     const uint64_t m = same(e, in);
     if (in && lane == __builtin_ctzll(m)) s_at[wave][e] += (int)__popcll(m);
+    wave_sync();  // the next step's first lane of this adapter is another one
   };
 #pragma unroll
   for (int k = 0; k < kHeld; ++k)
@@ -99,12 +100,15 @@ __global__ __launch_bounds__(64 * kOrderWaves) void k_adapt_order(const int32_t*
   auto place = [&](int t, int e) __attribute__((always_inline)) {
     const bool in = t + lane < t1;
     const uint64_t m = same(e, in);
+    const int at = s_at[wave][e];  // e is at most n, of lanes without a token too
+    wave_sync();
     if (in) {
-      const int at = s_at[wave][e], p = at + (int)__popcll(m & below);
+      const int p = at + (int)__popcll(m & below);
       if (lane == __builtin_ctzll(m)) s_at[wave][e] = at + (int)__popcll(m);
       out.order[p] = t + lane;
       out.ad[p] = e < n ? e : -1;
     }
+    wave_sync();
   };
 #pragma unroll
   for (int k = 0; k < kHeld; ++k)

@@ -234,3 +234,18 @@ def test_binding_refuses_what_does_not_fit():
     for bad in ((a, b[:1], s), (a, b.float(), s), (a, b, s[:1]), (a[0], b, s), (a.transpose(1, 2), b, s), (a, b, s.double())):
         with pytest.raises(moe.ArgError):
             moe.Adapters(*bad)
+
+
+@pytest.mark.parametrize("T,n", [(4000, 2), (20000, 7), (20000, 64), (33000, 1024)])
+def test_order_of_many_steps_that_share_adapters(T, n):
+    """Every 64 tokens have adapters that the 64 before them had, found by other lanes: each count and position that a step
+    leaves in shared memory is the next one's. Whole numbers, so every token's result says whether its position was right."""
+    rng = np.random.default_rng(T + n)
+    N, K, Rk = 64, 32, 8
+    q, s, codes, scales = H.weights(rng, N, K, 4, 0, whole=True)
+    ad, a, b, sc = H.adapters(rng, n, Rk, N, K, "bf16", whole=True)
+    i = ((np.arange(T) * 5 + np.arange(T) // 64 * 3) % (n + 1)).astype(np.int32)  # n: no adapter
+    x, x64 = H.matrix(rng, T, K, "bf16", whole=4)
+    y, _ = _call(moe.LinearConfig(N, K), codes, scales, ad, torch.from_numpy(i).to(DEV), x, dtype="bf16")
+    want = x64 @ R.weights(q, s).T + R.low_rank(x64, a, b, sc, i, False)[0]
+    assert torch.equal(y.cpu(), torch.from_numpy(want.astype(np.float32)).to(torch.bfloat16))
