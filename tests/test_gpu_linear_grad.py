@@ -417,3 +417,31 @@ def test_a_training_step_of_a_gated_block():
     step(0.5 * total)
     for g, b in zip(grads, before):
         assert bool(((g.double() - 0.5 * b.double()).abs() <= (2.0 ** -8 + 2.0 ** -22) * b.double().abs()).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T", [3, 100, 1100])
+@pytest.mark.parametrize("size", [3e-3, 1e-5, 1e-8])
+@pytest.mark.parametrize("group", [32, 64])
+def test_rows_whose_group_scales_are_zero(group, size, T, dtype):
+    """A quarter of the rows, as padding and pruning leave them, and single groups of live rows: what their codes hold and
+    how large their dz is changes nothing, however small the live rows' scales are."""
+    rng = np.random.default_rng(T + group)
+    N, K = 256, 256
+    q = rng.integers(-8, 8, (N, K)).astype(np.int8)
+    s = (size * rng.uniform(0.3, 1.0, (N, K // group))).astype(np.float32)
+    dead = rng.permutation(N)[: N // 4]
+    s[dead] = 0.0
+    s[np.setdiff1d(np.arange(N), dead)[::5], 1] = 0.0
+    u = (q & 15).astype(np.uint8)
+    codes = torch.empty(N * K // 2, dtype=torch.uint8, device=DEV)
+    moe.moe_tile_int4(torch.from_numpy(u[:, 0::2] | (u[:, 1::2] << 4)).to(DEV), codes)
+    scales = torch.empty(s.size, device=DEV)
+    moe.moe_tile_group_scales(torch.from_numpy(s).to(DEV), scales)
+    dy, dy64 = H.matrix(rng, T, N, dtype, spread=False)
+    dy.mul_(1024)  # fp16 results stay above its smallest
+    dx, _, _ = _call(moe.LinearConfig(N, K, 4, group), codes, scales, dy, dtype=dtype)
+    rows = np.sort(rng.permutation(T)[:64])
+    (v, err), _, _ = R.backward(q.astype(np.float64), s.astype(np.float64), None, None, None, None, None, 1024 * dy64[rows], None,
+                                dtype)
+    assert R.within(dx.double().cpu().numpy()[rows], v, err, dtype).all()
