@@ -217,8 +217,8 @@ __global__ __launch_bounds__(256) void k_group_scales(const float* __restrict__ 
   s_max[wave][lane] = m;
   __syncthreads();
   m = fmaxf(fmaxf(s_max[0][lane], s_max[1][lane]), fmaxf(s_max[2][lane], s_max[3][lane]));
-  // m = f 2^(e + 12), f in [1/2, 1)
-  const int e = m > 0.0f && m < INFINITY ? __builtin_amdgcn_frexp_expf(m) - 12 : 0;
+  // m = f 2^(e + 12), f in [1/2, 1), but 2^e at least fp32's smallest number
+  const int e = m > 0.0f && m < INFINITY ? max(__builtin_amdgcn_frexp_expf(m) - 12, -149) : 0;
   // a row of zeros (padding, pruning) adds nothing, so its dz must not count for the token's power of two
   if (wave == 0) mul[blockIdx.x * 64 + lane] = m > 0.0f ? ldexpf(1.0f, e) : 0.0f;
   // place of row l in the order of the codes: eight rows 0 4 1 5 2 6 3 7

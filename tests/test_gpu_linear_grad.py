@@ -445,3 +445,24 @@ def test_rows_whose_group_scales_are_zero(group, size, T, dtype):
     (v, err), _, _ = R.backward(q.astype(np.float64), s.astype(np.float64), None, None, None, None, None, 1024 * dy64[rows], None,
                                 dtype)
     assert R.within(dx.double().cpu().numpy()[rows], v, err, dtype).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [3, 100])
+@pytest.mark.parametrize("size", [2.0 ** -130, 2.0 ** -141])
+def test_group_scales_below_the_normal_range(size, T, dtype):
+    """Rows whose largest group scale is a subnormal, with gradients that make up for it."""
+    rng = np.random.default_rng(T)
+    N, K, group = 128, 128, 32
+    q = rng.integers(-8, 8, (N, K)).astype(np.int8)
+    s = (size * rng.uniform(0.25, 1.0, (N, K // group))).astype(np.float32)
+    u = (q & 15).astype(np.uint8)
+    codes = torch.empty(N * K // 2, dtype=torch.uint8, device=DEV)
+    moe.moe_tile_int4(torch.from_numpy(u[:, 0::2] | (u[:, 1::2] << 4)).to(DEV), codes)
+    scales = torch.empty(s.size, device=DEV)
+    moe.moe_tile_group_scales(torch.from_numpy(s).to(DEV), scales)
+    dy, dy64 = H.matrix(rng, T, N, dtype, spread=False)
+    dy.mul_(2.0 ** 100)
+    dx, _, _ = _call(moe.LinearConfig(N, K, 4, group), codes, scales, dy, dtype=dtype)
+    (v, err), _, _ = R.backward(q.astype(np.float64), s.astype(np.float64), None, None, None, None, None, 2.0 ** 100 * dy64, None, dtype)
+    assert R.within(dx.double().cpu().numpy(), v, err, dtype).all()
