@@ -466,3 +466,22 @@ def test_group_scales_below_the_normal_range(size, T, dtype):
     dx, _, _ = _call(moe.LinearConfig(N, K, 4, group), codes, scales, dy, dtype=dtype)
     (v, err), _, _ = R.backward(q.astype(np.float64), s.astype(np.float64), None, None, None, None, None, 2.0 ** 100 * dy64, None, dtype)
     assert R.within(dx.double().cpu().numpy(), v, err, dtype).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [2, 100])
+def test_a_large_gradient_times_a_large_up_part_of_a_closed_gate(T, dtype):
+    """dy up is beyond fp32, its product with the gate's derivative is not."""
+    rng = np.random.default_rng(T)
+    N, K = 128, 64
+    q, s, codes, scales = H.weights(rng, N, K, 8, 0)
+    dy, z = rng.uniform(0.5, 1.0, (T, N // 2)) * 2.0 ** 84, np.empty((T, N))
+    z[:, : N // 2], z[:, N // 2:] = rng.uniform(-40.0, -30.0, (T, N // 2)), rng.uniform(0.5, 1.0, (T, N // 2)) * 2.0 ** 68
+    dy, z = (torch.from_numpy(v.astype(np.float32)).to(DT[dtype]) for v in (dy, z))
+    dx, _, _ = _call(moe.LinearConfig(N, K, 8, 0, ACT["swiglu"]), codes, scales, dy.to(DEV), z=z.to(DEV), dtype=dtype)
+    dy64, z64 = dy.double().numpy(), z.double().numpy()
+    dz, _ = R.grad_in(dy64, z64, "swiglu")
+    # exp in fp32 at 40 is off by 40 2^-24 of it beside the roundings; the derivative is (1 + gate) exp(gate) there
+    size = np.abs(dz) * 128 * R.UNIT
+    (v, err), _, _ = R.backward(q, s, None, None, None, None, None, dz, None, dtype)
+    assert R.within(dx.double().cpu().numpy(), v, err + size @ np.abs(R.weights(q, s)), dtype).all()
