@@ -138,8 +138,9 @@ __global__ __launch_bounds__(256) void k_clip_norm(const ClipEntry* __restrict__
   if (threadIdx.x == 0) sums[blockIdx.x] = s;
 }
 
+// out = g mant 2^exp, in this order: a factor below fp32's normal range loses nothing
 template <class T, bool LAST>
-__device__ __forceinline__ void scale_chunk(const ClipEntry& e, int64_t chunk, float factor) {
+__device__ __forceinline__ void scale_chunk(const ClipEntry& e, int64_t chunk, float mant, int exp) {
   constexpr int V = 16 / sizeof(T);
   Global<T>* out = (Global<T>*)(static_cast<T*>(e.out) - e.skip);
   const bool whole = (uintptr_t)out % 16 == 0;
@@ -148,7 +149,7 @@ __device__ __forceinline__ void scale_chunk(const ClipEntry& e, int64_t chunk, f
     T t[V];
     __builtin_memcpy(t, &d, 16);
 #pragma unroll
-    for (int i = 0; i < V; ++i) t[i] = from_f32<T>(to_f32<T>(t[i]) * factor);
+    for (int i = 0; i < V; ++i) t[i] = from_f32<T>(__builtin_amdgcn_ldexpf(to_f32<T>(t[i]) * mant, exp));
     if (whole && at >= e.skip && at + V <= end) {
       Global<u4v>* to = (Global<u4v>*)(out + at);
       if (LAST) __builtin_nontemporal_store(__builtin_bit_cast(u4v, t), to);
@@ -180,14 +181,16 @@ __global__ __launch_bounds__(256) void k_clip_scale(const ClipEntry* __restrict_
   const double n = sqrt(block_sum(s, s_wave));
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
   // an infinite or NaN norm leaves the gradients as they are
-  const float factor = n > (double)max_norm && (float)n < INFINITY ? (float)((double)max_norm / n) : 1.0f;
+  const double factor = n > (double)max_norm && (float)n < INFINITY ? (double)max_norm / n : 1.0;
+  const int exp = factor < 1.0 ? __builtin_amdgcn_frexp_exp(factor) : 0;
+  const float mant = factor < 1.0 ? (float)__builtin_amdgcn_frexp_mant(factor) : 1.0f;  // a copy is exact
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     const ClipEntry e = next;
     const int32_t who = owner[max(chunks - 1 - c - gridDim.x, (int64_t)0)];
-    if (factor != 1.0f || e.out != e.g) {
-      if (e.dtype == MOE_DTYPE_F32) scale_chunk<float, LAST>(e, chunks - 1 - c - e.first, factor);
-      else if (e.dtype == MOE_DTYPE_BF16) scale_chunk<bf16_t, LAST>(e, chunks - 1 - c - e.first, factor);
-      else scale_chunk<_Float16, LAST>(e, chunks - 1 - c - e.first, factor);
+    if (factor < 1.0 || e.out != e.g) {
+      if (e.dtype == MOE_DTYPE_F32) scale_chunk<float, LAST>(e, chunks - 1 - c - e.first, mant, exp);
+      else if (e.dtype == MOE_DTYPE_BF16) scale_chunk<bf16_t, LAST>(e, chunks - 1 - c - e.first, mant, exp);
+      else scale_chunk<_Float16, LAST>(e, chunks - 1 - c - e.first, mant, exp);
     }
     next = entries[who];
   }

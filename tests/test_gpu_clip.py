@@ -159,3 +159,31 @@ def test_binding_refuses_what_does_not_fit():
             moe.moe_grad_clip(table, 1.0, norm)
     with pytest.raises(moe.MoeError):
         moe.moe_grad_clip(table, 0.0, torch.zeros(1, device=DEV))
+
+
+@pytest.mark.parametrize("types", [["f32"], ["bf16"], ["f32", "bf16"]])
+@pytest.mark.parametrize("size,limit", [(1e30, 1e-6), (1e30, 1e-9), (1e30, 1e-14), (3e34, 1e-20)])
+@pytest.mark.parametrize("inplace", [True, False])
+def test_a_limit_far_below_the_norm(size, limit, types, inplace):
+    """The factor is below fp32's normal range, or below all of it; the clipped gradients are not."""
+    rng = np.random.default_rng(5)
+    sizes = [5000, 37, 9000]
+    _, grads = _tensors(rng, sizes, [types[i % len(types)] for i in range(3)], size)
+    out = grads if inplace else [torch.zeros_like(g) for g in grads]
+    before = [g.clone() for g in grads]
+    want = _norm(before)
+    norm = torch.zeros(1, device=DEV)
+    moe.moe_grad_clip(moe.GradTable(grads, out), limit, norm)
+    assert abs(float(norm) - want) <= 2.0 ** -23 * want
+    _check(before, out, want, limit)
+
+
+@pytest.mark.parametrize("types", [["f32"], ["bf16"], ["f16"]])
+def test_a_copy_keeps_the_smallest_numbers(types):
+    """Within the limit, to other arrays: every bit of values down to the types' smallest subnormals."""
+    rng = np.random.default_rng(6)
+    _, grads = _tensors(rng, [8000, 33], types * 2, {"f32": 1e-42, "bf16": 1e-39, "f16": 1e-7}[types[0]])
+    out = [torch.full_like(g, 9.0) for g in grads]
+    norm = torch.zeros(1, device=DEV)
+    moe.moe_grad_clip(moe.GradTable(grads, out), 1.0, norm)
+    assert all(torch.equal(a, b) for a, b in zip(out, grads)) and all(bool((g != 0).any()) for g in grads)
