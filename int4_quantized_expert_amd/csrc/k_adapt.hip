@@ -158,6 +158,43 @@ __device__ __forceinline__ void put_h(const AdaptDown& a, const AdaptDown::Part&
 // Few tokens: a workgroup takes a token and 4 rows of its A; its lanes share the columns, all loads in flight at once.
 // across: A lies as [C][R]. One token of 6144 columns, rank 16: 3.4 us, 191 of 2048, rank 8: 4.0; a launch and its loads.
 template <class TX>
+struct alignas(4 * sizeof(TX)) Four {
+  TX v[4];
+};
+// a lane's share of the sums of rows r0 .. r0 + 3; TM: the type of x
+template <class TX, class TM>
+__device__ __forceinline__ void dot_rows(const AdaptDown& a, const AdaptDown::Part& d, int p, int e, int r0, float (&v)[4]) {
+  const int tid = threadIdx.x;
+  const TM* x = static_cast<const TM*>(d.x) + (size_t)(d.order ? d.order[p] : p) * d.ldx;
+  if (d.across) {
+    const TX* b = static_cast<const TX*>(d.a) + (size_t)e * a.R * d.C + r0;
+#pragma unroll 8
+    for (int c = tid; c < d.C; c += 256) {
+      const float xv = to_f32<TM>(x[c]);
+      const Four<TX> w = *reinterpret_cast<const Four<TX>*>(b + (size_t)c * a.R);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = fmaf(xv, to_f32<TX>(w.v[i]), v[i]);
+    }
+  }
+  const TX* w = static_cast<const TX*>(d.a) + ((size_t)e * a.R + r0) * d.C;
+#pragma unroll 4
+  for (int g = tid; g < d.C / 8 && !d.across; g += 256) {
+    Granule<TM> xg;
+    Granule<TX> wg[4];
+    load8(x + g * 8, d.vec_x, xg);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load8(w + (size_t)i * d.C + g * 8, true, wg[i]);
+    const f8v xv = granule_f32<TM>(xg);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f8v wv = granule_f32<TX>(wg[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i] = fmaf(xv[j], wv[j], v[i]);
+    }
+  }
+}
+
+template <class TX>
 __global__ __launch_bounds__(256) void k_adapt_dot(AdaptDown a) {
   __shared__ float s_sum[4][4];
   const AdaptDown::Part& d = a.part[blockIdx.z];
@@ -165,35 +202,8 @@ __global__ __launch_bounds__(256) void k_adapt_dot(AdaptDown a) {
   const int e = adapter_of(a, p);
   float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (e >= 0) {
-    const TX* x = static_cast<const TX*>(d.x) + (size_t)(d.order ? d.order[p] : p) * d.ldx;
-    if (d.across) {
-      struct alignas(4 * sizeof(TX)) Four {
-        TX v[4];
-      };
-      const TX* b = static_cast<const TX*>(d.a) + (size_t)e * a.R * d.C + r0;
-#pragma unroll 8
-      for (int c = tid; c < d.C; c += 256) {
-        const float xv = to_f32<TX>(x[c]);
-        const Four w = *reinterpret_cast<const Four*>(b + (size_t)c * a.R);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = fmaf(xv, to_f32<TX>(w.v[i]), v[i]);
-      }
-    }
-    const TX* w = static_cast<const TX*>(d.a) + ((size_t)e * a.R + r0) * d.C;
-#pragma unroll 4
-    for (int g = tid; g < d.C / 8 && !d.across; g += 256) {
-      Granule<TX> xg, wg[4];
-      load8(x + g * 8, d.vec_x, xg);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) load8(w + (size_t)i * d.C + g * 8, true, wg[i]);
-      const f8v xv = granule_f32<TX>(xg);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f8v wv = granule_f32<TX>(wg[i]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i] = fmaf(xv[j], wv[j], v[i]);
-      }
-    }
+    if (!std::is_same<TX, float>::value && d.f32) dot_rows<TX, float>(a, d, p, e, r0, v);
+    else dot_rows<TX, TX>(a, d, p, e, r0, v);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -214,7 +224,7 @@ __global__ __launch_bounds__(256) void k_adapt_dot(AdaptDown a) {
 // operands, a row a lane, come from LDS: loaded in the operands' order, where neighbouring lanes are in different rows, a
 // load takes four times as long (14 us for any number of runs up to 128, rows of 6144 bf16; 8 us so where they are in the
 // caches and 11 where not, 2,048 tokens of rank 32 14 to 15.5). Latency bounds it: run, token, row, columns are loaded one
-// after the other. fp32 is multiplied in fp32, the others in their type, which is exact.
+// after the other. fp32 is multiplied in fp32 (by 16-bit A or B too, for a kept dz), the others in their type, which is exact.
 constexpr int kDownWaves = 8;
 template <class TX>
 __device__ __forceinline__ u4v load_16(const TX* p, bool vec) {
@@ -238,18 +248,24 @@ __device__ __forceinline__ f4 mul_16(const u4v& x, const u4v& w, f4 c) {
   }
 }
 
-template <class TX, int RF>
-__global__ __launch_bounds__(64 * kDownWaves, 4) void k_adapt_down(AdaptDown a) {
-  constexpr int kChunk = 16 / sizeof(TX), kStep = 8 * kChunk, U = RF == 1 ? 4 : 3;  // columns; steps at once
+// as many elements as 16 bytes of TM hold, as TM
+template <class TX, class TM>
+__device__ __forceinline__ u4v load_as(const TX* p) {
+  if constexpr (std::is_same<TX, TM>::value) return load_16<TX>(p, true);
+  const Four<TX> q = *reinterpret_cast<const Four<TX>*>(p);
+  return __builtin_bit_cast(u4v, f4{to_f32<TX>(q.v[0]), to_f32<TX>(q.v[1]), to_f32<TX>(q.v[2]), to_f32<TX>(q.v[3])});
+}
+
+template <int RF>
+constexpr size_t down_lds() {
+  return std::max<size_t>((size_t)kDownWaves * (1 + RF) * 2048, sizeof(float) * kDownWaves * 16 * (16 * RF + 4));
+}
+// TM: the type of x, in which the products are taken; s_mem: a wavefront's rows of a step, [1 + RF][16][128 bytes], later the
+// sums, [wavefronts][16][kSum]
+template <class TX, class TM, int RF>
+__device__ __forceinline__ void down_run(const AdaptDown& a, const AdaptDown::Part& d, const AdaptChunk& run, char* s_mem) {
+  constexpr int kChunk = 16 / sizeof(TM), kStep = 8 * kChunk, U = RF == 1 ? 4 : 3;  // columns; steps at once
   constexpr int kSum = 16 * RF + 4;
-  // a wavefront's rows of a step, [1 + RF][16][128 bytes], later the sums, [wavefronts][16][kSum]
-  __shared__ __align__(16) char s_mem[std::max<size_t>((size_t)kDownWaves * (1 + RF) * 2048, sizeof(float) * kDownWaves * 16 * kSum)];
-  const AdaptDown::Part& d = a.part[blockIdx.z];
-  AdaptChunk run{0, (int)blockIdx.x * 16, min((int)blockIdx.x * 16 + 16, a.T), 0};  // the only adapter, whoever has it
-  if (a.runs) {
-    if ((int)blockIdx.x >= *a.n_runs) return;
-    run = a.runs[blockIdx.x];
-  }
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, g = lane >> 4;
   const int r0 = blockIdx.y * 16 * RF, rows = min(16 * RF, a.R - r0);
   const int steps = (d.C + kStep - 1) / kStep, per = (steps + kDownWaves - 1) / kDownWaves;
@@ -257,12 +273,12 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_adapt_down(AdaptDown a) 
   // lane: row lane / 8 (and 8 more), chunk lane % 8, which goes to place chunk ^ row % 8, so that no two lanes that read
   // at a time meet in a bank
   const int chunk = (lane & 7) ^ (lane >> 3);
-  const TX* x[2];
+  const TM* x[2];
   const TX* w[RF][2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int q = 8 * k + (lane >> 3), p = min(run.p0 + q, run.p1 - 1);
-    x[k] = static_cast<const TX*>(d.x) + (size_t)(d.order ? d.order[p] : p) * d.ldx + chunk * kChunk;
+    x[k] = static_cast<const TM*>(d.x) + (size_t)(d.order ? d.order[p] : p) * d.ldx + chunk * kChunk;
 #pragma unroll
     for (int f = 0; f < RF; ++f)
       w[f][k] = static_cast<const TX*>(d.a) + ((size_t)run.e * a.R + r0 + min(16 * f + q, rows - 1)) * d.C + chunk * kChunk;
@@ -280,7 +296,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_adapt_down(AdaptDown a) 
       for (int k = 0; k < 2; ++k) {
         xv[u][k] = load_16(x[k] + c, d.vec_x);
 #pragma unroll
-        for (int f = 0; f < RF; ++f) wv[u][f][k] = load_16(w[f][k] + c, true);
+        for (int f = 0; f < RF; ++f) wv[u][f][k] = load_as<TX, TM>(w[f][k] + c);
       }
     }
 #pragma unroll
@@ -299,7 +315,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_adapt_down(AdaptDown a) 
         const int from = i * 8 + ((4 * h + g) ^ (i & 7));
         const u4v xf = s_row[from];
 #pragma unroll
-        for (int f = 0; f < RF; ++f) acc[f] = mul_16<TX>(xf, s_row[128 * (1 + f) + from], acc[f]);
+        for (int f = 0; f < RF; ++f) acc[f] = mul_16<TM>(xf, s_row[128 * (1 + f) + from], acc[f]);
       }
       wave_sync();
     }
@@ -322,6 +338,19 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_adapt_down(AdaptDown a) 
   }
 }
 
+template <class TX, int RF>
+__global__ __launch_bounds__(64 * kDownWaves, 4) void k_adapt_down(AdaptDown a) {
+  __shared__ __align__(16) char s_mem[down_lds<RF>()];
+  const AdaptDown::Part& d = a.part[blockIdx.z];
+  AdaptChunk run{0, (int)blockIdx.x * 16, min((int)blockIdx.x * 16 + 16, a.T), 0};  // the only adapter, whoever has it
+  if (a.runs) {
+    if ((int)blockIdx.x >= *a.n_runs) return;
+    run = a.runs[blockIdx.x];
+  }
+  if (!std::is_same<TX, float>::value && d.f32) down_run<TX, float, RF>(a, d, run, s_mem);
+  else down_run<TX, TX, RF>(a, d, run, s_mem);
+}
+
 // ------------------------------------------------------------ gradients of A and B
 // out[r][c] = sum over an adapter's positions of v[p][r] m[p][c]; a workgroup takes 32 rows r (fewer where R is less) by
 // 128 columns and a run of positions, of which each of its four wavefronts takes a part; both gradients in one launch. Positions are what is
@@ -329,8 +358,8 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_adapt_down(AdaptDown a) 
 // exchanges halves of words between two positions, which gives the operands of 8 products (column l + j of every eight
 // columns in product j). v comes with eight
 // positions of a row next to each other. As in the product's epilogue v has two bf16 parts, bf16 m one and fp16 m
-// two. fp32 is multiplied as it is, 4 columns a lane. 2,000 tokens of four adapters, rank 32, 4096 and 6144 columns: 16.0 us
-// for 41 MB; two workgroups a compute unit fit the registers, and each waits for chunk, order and rows in turn.
+// two. fp32 (a kept dz too) is multiplied as it is, 4 columns a lane. 2,000 tokens of four adapters, rank 32, 4096 columns of
+// fp32 and 6144 of bf16: 20.4 us for 57 MB, 16.0 for 41 with both in bf16; two workgroups a compute unit fit the registers, and each waits for chunk, order and rows in turn.
 __device__ __forceinline__ size_t outer_at(const AdaptOuter& a, const AdaptOuter::Part& d, int e, int r, int c) {
   return d.rows ? ((size_t)e * d.C + c) * a.R + r : ((size_t)e * a.R + r) * d.C + c;
 }
@@ -486,7 +515,8 @@ __device__ __forceinline__ void outer_16(const AdaptOuter& a, const AdaptOuter::
   }
 }
 
-template <int RF, bool FEW>
+// m in fp32, multiplied as it is; TX: the type of the result.
+template <class TX, int RF, bool FEW>
 __device__ __forceinline__ void outer_32(const AdaptOuter& a, const AdaptOuter::Part& d, const AdaptChunk& ch, uint64_t mine,
                                          int c_group, int r0, float* s_sum) {
   constexpr int U = 4;  // steps of four positions
@@ -567,14 +597,36 @@ __device__ __forceinline__ void outer_32(const AdaptOuter& a, const AdaptOuter::
   for (int f = 0; f < RF; ++f) {
     const int r = r0 + 16 * f + 4 * g;
     if (r >= a.R) continue;
-    float* out = static_cast<float*>(d.out);
-    if (ch.slot < 0 && d.rows)
-      *reinterpret_cast<f4*>(out + outer_at(a, d, ch.e, r, c0 + wave)) =
-          f4{total(f, wave, 0), total(f, wave, 1), total(f, wave, 2), total(f, wave, 3)};
-    else
-      *reinterpret_cast<f4*>(ch.slot >= 0 ? d.part + ((size_t)ch.slot * a.R + r + wave) * d.C + c0
-                                          : out + outer_at(a, d, ch.e, r + wave, c0)) =
-          f4{total(f, 0, wave), total(f, 1, wave), total(f, 2, wave), total(f, 3, wave)};
+    const bool rows = ch.slot < 0 && d.rows;  // four rows of a column, or four columns of a row
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = rows ? total(f, wave, k) : total(f, k, wave);
+    if (ch.slot >= 0) {
+      *reinterpret_cast<f4*>(d.part + ((size_t)ch.slot * a.R + r + wave) * d.C + c0) = f4{v[0], v[1], v[2], v[3]};
+    } else {
+      Four<TX> o;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o.v[k] = from_f32<TX>(v[k]);
+      const size_t at = rows ? outer_at(a, d, ch.e, r, c0 + wave) : outer_at(a, d, ch.e, r + wave, c0);
+      *reinterpret_cast<Four<TX>*>(static_cast<TX*>(d.out) + at) = o;
+    }
+  }
+}
+
+// columns of a workgroup
+template <class TX>
+constexpr int outer_cols(bool f32) {
+  return f32 || std::is_same<TX, float>::value ? 64 : 128;
+}
+template <class TX, int RF, bool FEW>
+__device__ __forceinline__ void outer_run(const AdaptOuter& a, const AdaptOuter::Part& d, const AdaptChunk& ch, uint64_t mine,
+                                          int c, int r0, float* s_sum) {
+  if constexpr (std::is_same<TX, float>::value) {
+    outer_32<TX, RF, FEW>(a, d, ch, mine, c, r0, s_sum);
+  } else if (d.f32) {
+    outer_32<TX, RF, FEW>(a, d, ch, mine, c, r0, s_sum);
+  } else {
+    outer_16<TX, RF, FEW>(a, d, ch, mine, c, r0, s_sum);
   }
 }
 
@@ -582,33 +634,30 @@ __device__ __forceinline__ void outer_32(const AdaptOuter& a, const AdaptOuter::
 // gradients are zeros where they have no tokens.
 template <class TX, int RF, bool FEW>
 __global__ __launch_bounds__(256, 2) void k_adapt_outer(AdaptOuter a, int x0, int runs) {
-  constexpr int kCols = std::is_same<TX, float>::value ? 64 : 128;
-  __shared__ __align__(16) float s_sum[4 * RF * 16 * kCols];
+  __shared__ __align__(16) float s_sum[4 * RF * 16 * outer_cols<TX>(false)];
   const bool second = (int)blockIdx.x >= x0;
   const AdaptOuter::Part& d = a.part[second];
-  const int c = (blockIdx.x - (second ? x0 : 0)) * kCols, r0 = blockIdx.z * 16 * RF;
+  const int cols = outer_cols<TX>(d.f32), c = (blockIdx.x - (second ? x0 : 0)) * cols, r0 = blockIdx.z * 16 * RF;
   if constexpr (FEW) {  // an adapter each; without tokens its sums are zeros
     const int lane = threadIdx.x & 63;
     const uint64_t mine = __ballot(lane < a.T && (a.ids ? a.ids[min(lane, a.T - 1)] : 0) == (int)blockIdx.y);
     const AdaptChunk ch{(int)blockIdx.y, 0, mine ? a.T : 0, -1};
-    if constexpr (std::is_same<TX, float>::value) outer_32<RF, true>(a, d, ch, mine, c, r0, s_sum);
-    else outer_16<TX, RF, true>(a, d, ch, mine, c, r0, s_sum);
+    outer_run<TX, RF, true>(a, d, ch, mine, c, r0, s_sum);
     return;
   }
   if ((int)blockIdx.y >= runs) {
     const int e = blockIdx.y - runs;
     if (a.order.offsets[e + 1] != a.order.offsets[e]) return;
     const int rows = min(16 * RF, a.R - r0);
-    for (int k = threadIdx.x; k < rows * kCols; k += 256) {
-      const int r = d.rows ? k % rows : k / kCols, cc = c + (d.rows ? k / rows : k % kCols);
+    for (int k = threadIdx.x; k < rows * cols; k += 256) {
+      const int r = d.rows ? k % rows : k / cols, cc = c + (d.rows ? k / rows : k % cols);
       if (cc < d.C) static_cast<TX*>(d.out)[outer_at(a, d, e, r0 + r, cc)] = from_f32<TX>(0.0f);
     }
     return;
   }
   if ((int)blockIdx.y >= *a.order.n_chunks) return;
   const AdaptChunk ch = a.order.chunks[blockIdx.y];
-  if constexpr (std::is_same<TX, float>::value) outer_32<RF, false>(a, d, ch, 0, c, r0, s_sum);
-  else outer_16<TX, RF, false>(a, d, ch, 0, c, r0, s_sum);
+  outer_run<TX, RF, false>(a, d, ch, 0, c, r0, s_sum);
 }
 
 // Adapters of several runs: their partial sums in ascending order.
@@ -674,17 +723,17 @@ void down_launch(const AdaptDown& a, hipStream_t st) {
 }
 template <class TX>
 void outer_launch(const AdaptOuter& a, hipStream_t st) {
-  const int per = std::is_same<TX, float>::value ? 64 : 128, len = adapt_chunk_len(a.T);
+  const int len = adapt_chunk_len(a.T);
   auto cols = [&](int k, int w) { return a.part[k].out ? (a.part[k].C + w - 1) / w : 0; };
-  const int x = cols(0, per) + cols(1, per);
+  const int x0 = cols(0, outer_cols<TX>(a.part[0].f32)), x = x0 + cols(1, outer_cols<TX>(a.part[1].f32));
   if (!a.order.order) {
-    if (a.R <= 16) k_adapt_outer<TX, 1, true><<<dim3(x, a.n_ad), 256, 0, st>>>(a, cols(0, per), 0);
-    else k_adapt_outer<TX, 2, true><<<dim3(x, a.n_ad, (a.R + 31) / 32), 256, 0, st>>>(a, cols(0, per), 0);
+    if (a.R <= 16) k_adapt_outer<TX, 1, true><<<dim3(x, a.n_ad), 256, 0, st>>>(a, x0, 0);
+    else k_adapt_outer<TX, 2, true><<<dim3(x, a.n_ad, (a.R + 31) / 32), 256, 0, st>>>(a, x0, 0);
     return;
   }
   const int runs = (int)adapt_max_chunks(a.T, a.n_ad);
-  if (a.R <= 16) k_adapt_outer<TX, 1, false><<<dim3(x, runs + a.n_ad), 256, 0, st>>>(a, cols(0, per), runs);
-  else k_adapt_outer<TX, 2, false><<<dim3(x, runs + a.n_ad, (a.R + 31) / 32), 256, 0, st>>>(a, cols(0, per), runs);
+  if (a.R <= 16) k_adapt_outer<TX, 1, false><<<dim3(x, runs + a.n_ad), 256, 0, st>>>(a, x0, runs);
+  else k_adapt_outer<TX, 2, false><<<dim3(x, runs + a.n_ad, (a.R + 31) / 32), 256, 0, st>>>(a, x0, runs);
   if (a.T > len)
     k_adapt_join<TX><<<dim3(cols(0, 256) + cols(1, 256), a.n_ad, a.R / 8), 256, 0, st>>>(a, cols(0, 256), len);
 }

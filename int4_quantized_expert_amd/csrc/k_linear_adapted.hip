@@ -52,7 +52,7 @@ hipError_t run(LinearArgs& a, int bits, const moe_adapters* ad, const int32_t* i
       if (!few) a.order = o.order, a.ad = o.ad;
     }
     d.ad = sorted ? o.ad : ids;
-    d.part[0] = {a.x, a.ldx, a.vec_x, a.K, sorted ? o.order : nullptr, ad->a, 0, reinterpret_cast<float*>(w + p.h), nullptr};
+    d.part[0] = {a.x, a.ldx, 0, a.vec_x, a.K, sorted ? o.order : nullptr, ad->a, 0, reinterpret_cast<float*>(w + p.h), nullptr};
     const hipError_t e = launch_adapt_down(d, dtype, st);
     if (e != hipSuccess) return e;
   }

@@ -67,9 +67,9 @@ constexpr int kAdaptFewTokens = 64;
 // [T / 8][R][8]; two such products in one launch
 struct AdaptDown {
   struct Part {
-    const void* x;
+    const void* x;  // of the call's type, or fp32
     int64_t ldx;
-    int32_t vec_x, C;
+    int32_t f32, vec_x, C;
     const int32_t* order;
     const void* a;
     int32_t across;  // (few) a lies as [C][R]
@@ -89,9 +89,9 @@ hipError_t launch_adapt_down(const AdaptDown& a, int dtype, hipStream_t st);
 // out[e] = sum over e's positions of v[p][r] m[p][c]: [n][R][C], or with `rows` [n][C][R]; out NULL: not wanted
 struct AdaptOuter {
   struct Part {
-    const void* m;
+    const void* m;  // of the call's type, or fp32
     int64_t ldm;
-    int32_t vec_m, C, rows;
+    int32_t f32, vec_m, C, rows;
     const int32_t* order;  // rows of m, nullptr: m's rows are positions
     const float* v;
     const float* vt;

@@ -485,3 +485,74 @@ def test_a_large_gradient_times_a_large_up_part_of_a_closed_gate(T, dtype):
     size = np.abs(dz) * 128 * R.UNIT
     (v, err), _, _ = R.backward(q, s, None, None, None, None, None, dz, None, dtype)
     assert R.within(dx.double().cpu().numpy(), v, err + size @ np.abs(R.weights(q, s)), dtype).all()
+
+
+def _unrounded(q, s, x64, a, b, sc, i, dy64, z64, dtype, act):
+    """R.backward's results and bounds for adapters' sums over dz as it is: a few fp32 roundings of the derivative, none to the
+    type."""
+    dz, size = R.grad_in(dy64, z64, act)
+    dx, (da, ea), (db, eb) = R.backward(q, s, x64, a, b, sc, i, dz, None, dtype)
+    ez = 32 * R.UNIT * size
+    ex = dx[1] + ez @ np.abs(R.weights(q, s))
+    at = R.chosen(i, a.shape[0], dy64.shape[0])
+    for e in np.unique(at[at >= 0]):
+        t = np.nonzero(at == e)[0]
+        eu = ez[t] @ np.abs(b[e]) * abs(sc[e])
+        ea[e] += eu.T @ np.abs(x64[t])
+        eb[e] += ez[t].T @ np.abs(x64[t] @ a[e].T * sc[e])
+        ex[t] += eu @ np.abs(a[e])
+    return (dx[0], ex), (da, ea), (db, eb)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("act", ["silu", "swiglu"])
+@pytest.mark.parametrize("T,N,K,Rk,n,how", [(5, 256, 96, 16, 2, "mix"), (40, 128, 160, 8, 3, "mix"), (64, 192, 64, 128, 2, "one"),
+                                            (300, 448, 288, 16, 3, "runs"), (700, 320, 96, 40, 2, "one"), (2100, 128, 64, 24, 5, "mix")])
+def test_adapters_gradients_are_rounded_once(T, N, K, Rk, n, how, act, dtype):
+    """Between the activation's derivative and the adapters' sums nothing is rounded to the type: each gradient is off by its
+    own rounding and by what fp32 sums and 16 bits of scale (A x) and scale (B^T dz) leave."""
+    rng = np.random.default_rng(T + N + Rk)
+    q, s, codes, scales = H.weights(rng, N, K, 4, 0)
+    ad, a, b, sc = H.adapters(rng, n, Rk, N, K, dtype)
+    ids, i = H.ids_of(rng, T, n, how)
+    x, x64 = H.matrix(rng, T, K, dtype, pad=3)
+    dy, dy64 = H.matrix(rng, T, N // 2 if act == "swiglu" else N, dtype, pad=1)
+    z, z64 = H.matrix(rng, T, N, dtype, pad=8, spread=False)
+    got = _call(moe.LinearConfig(N, K, 4, 0, ACT[act]), codes, scales, dy, ad, ids, x, z, dtype=dtype)
+    want = _unrounded(q, s, x64, a, b, sc, i, dy64, z64, dtype, act)
+    for name, g, (v, err) in zip(("dx", "da", "db"), got, want):
+        assert R.within(g.double().cpu().numpy(), v, err, dtype).all(), name
+
+
+@pytest.mark.parametrize("T", [3, 40, 300, 1100])
+@pytest.mark.parametrize("big", [True, False])
+def test_half_precision_dz_outside_its_range(big, T):
+    """fp16 calls whose dz is beyond 65504, or below 2^-24: with adapters dx is finite as it is without, and the gradients are
+    the formula's."""
+    rng = np.random.default_rng(T)
+    N, K, n, Rk = 128, 96, 3, 8
+    half = lambda v: torch.from_numpy(v.astype(np.float32)).half()  # noqa: E731
+    q, s, codes, scales = H.weights(rng, N, K, 4, 0)
+    a, b = rng.normal(0, 1 / np.sqrt(K), (n, Rk, K)), rng.normal(0, 1e-4 if big else 1.0, (n, N, Rk))
+    x, dy, z = rng.normal(0, 1e-3 if big else 1e4, (T, K)), rng.normal(0, 500 if big else 3e-6, (T, N // 2)), rng.normal(0, 1, (T, N))
+    z[:, N // 2:] *= 500 if big else 3e-3
+    z[:, : N // 2] += 2 if big else -5
+    a, b, x, dy, z = (half(v) for v in (a, b, x, dy, z))
+    sc = torch.from_numpy(rng.uniform(0.5, 2.0, n).astype(np.float32))
+    scale = 2.0 ** (-10 if big else 10)
+    scales.mul_(scale)
+    ad = moe.Adapters(a.to(DEV), b.to(DEV), sc.to(DEV))
+    ids, i = H.ids_of(rng, T, n, "mix")
+    i[0] = 0
+    ids.copy_(torch.from_numpy(i))
+    args = (moe.LinearConfig(N, K, 4, 0, ACT["swiglu"]), codes, scales, dy.to(DEV))
+    f64 = [t.double().numpy() for t in (x, a, b, sc, dy, z)]
+    dz = np.abs(R.grad_in(f64[4], f64[5], "swiglu")[0])
+    assert dz.max() > 2 * 65504 if big else np.median(dz) < 2.0 ** -24
+    alone = _call(*args, z=z.to(DEV), dtype="f16")[0]
+    got = _call(*args, ad, ids, x.to(DEV), z.to(DEV), dtype="f16")
+    want = _unrounded(q, s * scale, *f64[:4], i, *f64[4:], "f16", "swiglu")
+    assert all(bool(torch.isfinite(t).all()) for t in (alone, *got))
+    for name, g, (v, err) in zip(("dx", "da", "db"), got, want):
+        assert np.abs(v).max() > 2.0 ** -16
+        assert R.within(g.double().cpu().numpy(), v, err, "f16").all(), name
