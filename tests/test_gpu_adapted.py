@@ -249,3 +249,29 @@ def test_order_of_many_steps_that_share_adapters(T, n):
     y, _ = _call(moe.LinearConfig(N, K), codes, scales, ad, torch.from_numpy(i).to(DEV), x, dtype="bf16")
     want = x64 @ R.weights(q, s).T + R.low_rank(x64, a, b, sc, i, False)[0]
     assert torch.equal(y.cpu(), torch.from_numpy(want.astype(np.float32)).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,N,K,Rk,how", [(64, 64, 96, 128, "mix"), (300, 2048, 160, 16, "mix"), (700, 1088, 96, 40, "runs"),
+                                          (1100, 4096, 64, 8, "mix"), (520, 128, 96, 8, "none")])
+def test_one_adapter_that_some_tokens_have(T, N, K, Rk, how, dtype):
+    """One adapter and ids with others beside it, which take no order: whole numbers, bit for bit; then an adapter of NaN and
+    infinity, which the tokens without it do not see."""
+    rng = np.random.default_rng(T + N)
+    q, s, codes, scales = H.weights(rng, N, K, 4, 0, whole=True)
+    ad, a, b, sc = H.adapters(rng, 1, Rk, N, K, dtype, whole=True)
+    i = rng.choice([0, -1, 1, 2 ** 31 - 1], T) if how == "mix" else H.ids_of(rng, T, 1, how)[1]
+    i = i.astype(np.int32)
+    ids = torch.from_numpy(i).to(DEV)
+    x, x64 = H.matrix(rng, T, K, dtype, whole=4)
+    cfg = moe.LinearConfig(N, K)
+    y, z = _call(cfg, codes, scales, ad, ids, x, keep=True, dtype=dtype)
+    want = x64 @ R.weights(q, s).T + R.low_rank(x64, a, b, sc, i, False)[0]
+    want = torch.from_numpy(want.astype(np.float32)).to(DT[dtype])
+    assert torch.equal(y.cpu(), want) and torch.equal(z.cpu(), want)
+    ta, tb, _ = ad._keep
+    ta[0, 1, 3], tb[0, ::2] = float("inf"), float("nan")
+    y, _ = _call(cfg, codes, scales, ad, ids, x, dtype=dtype)
+    own = torch.from_numpy(i == 0)
+    assert torch.equal(y.cpu()[~own], want[~own])
+    assert bool((~torch.isfinite(y.cpu()[own])).all())

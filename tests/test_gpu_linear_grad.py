@@ -556,3 +556,71 @@ def test_half_precision_dz_outside_its_range(big, T):
     for name, g, (v, err) in zip(("dx", "da", "db"), got, want):
         assert np.abs(v).max() > 2.0 ** -16
         assert R.within(g.double().cpu().numpy(), v, err, "f16").all(), name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("act", ["none", "silu", "swiglu"])
+@pytest.mark.parametrize("group", [0, 32])
+@pytest.mark.parametrize("T", [3, 33, 64, 300, 1100])
+def test_no_number_reaches_another_token_or_adapter(T, group, act, dtype):
+    """NaN and infinity in dy, in x and in an adapter, for few tokens and for many: other tokens' dx and other adapters'
+    gradients keep their bits; so do d_b's rows of an adapter whose token has an infinity in another row of dz."""
+    rng = np.random.default_rng(T)
+    N, K = 320, 160
+    _, _, codes, scales = H.weights(rng, N, K, 4, group)
+    ad, *_ = H.adapters(rng, 5, 16, N, K, dtype)
+    _, i = H.ids_of(rng, T, 5, "mix")
+    i[:3] = 1, -1, 3
+    ids = torch.from_numpy(i).to(DEV)
+    x, _ = H.matrix(rng, T, K, dtype)
+    dy, _ = H.matrix(rng, T, N // 2 if act == "swiglu" else N, dtype)
+    z, _ = H.matrix(rng, T, N, dtype, spread=False)
+    z = z.abs_().add_(0.5) if act != "none" else None  # no derivative of zero beside an infinity
+    cfg = moe.LinearConfig(N, K, 4, group, ACT[act])
+    clean = _call(cfg, codes, scales, dy, ad, ids, x, z, dtype=dtype)
+    dy[0, 5], dy[1, 9] = float("inf"), float("nan")  # tokens of adapter 1 and of none
+    x[2, 7] = float("nan")                           # a token of adapter 3: in its d_a and, by A x, its d_b
+    ad._keep[1][2, 7] = float("nan")
+    got = _call(cfg, codes, scales, dy, ad, ids, x, z, dtype=dtype)
+    bad = i == 2
+    bad[:2] = True
+    ok = torch.from_numpy(~bad)
+    assert torch.equal(got[0].cpu()[ok], clean[0].cpu()[ok])
+    assert bool((~torch.isfinite(got[0].cpu()[~ok])).all())
+    for k in (1, 2):
+        for e in (0, 4):
+            assert torch.equal(got[k][e], clean[k][e])
+        for e in (1, 3):
+            assert not bool(torch.isfinite(got[k][e]).all())
+    rows = [r for r in range(N) if r != 5 and not (act == "swiglu" and r == 5 + N // 2)]
+    assert torch.equal(got[2][1][rows], clean[2][1][rows])
+    assert torch.equal(got[1][3][:, :7], clean[1][3][:, :7]) and torch.equal(got[1][3][:, 8:], clean[1][3][:, 8:])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 80])
+def test_a_gate_near_the_largest_number(T, dtype):
+    """An open gate of 3e38: its derivative is 1, and silu(gate) is the gate; the results go beyond fp32 where W takes them."""
+    N, K = 64, 64
+    rng = np.random.default_rng(3)
+    q, s, codes, scales = H.weights(rng, N, K, 8, 0, whole=True)
+    z = torch.zeros((T, N), device=DEV)
+    z[:, 0], z[:, 32:] = 3e38, 1.0
+    z = z.to(DT[dtype])
+    dy = torch.zeros((T, N // 2), dtype=DT[dtype], device=DEV)
+    dy[:, 0] = 2.0 ** -5
+    dx, _, _ = _call(moe.LinearConfig(N, K, 8, 0, ACT["swiglu"]), codes, scales, dy, z=z, dtype=dtype)
+    w = R.weights(q, s)
+    gate = float(z[0, 0].double())
+    want = 2.0 ** -5 * (w[0] + gate * w[32])
+    top, got = float(torch.finfo(DT[dtype]).max), dx.double().cpu().numpy()
+    assert (np.abs(want) > 1.01 * top).any() and (np.abs(want) < 0.99 * top).any()
+    near = np.abs(np.abs(want) / top - 1.0) < 0.01  # either is right next to the border
+    for t in range(T):
+        far = np.abs(want) > top
+        assert np.array_equal(got[t][far & ~near], np.sign(want[far & ~near]) * math.inf)
+        fin = ~far & ~near
+        # one rounding to fp16 of dz, in two halves for fp32, and one to the type
+        step = 2.0 ** -21 if dtype == "f32" else 2.0 ** -11 + 2.0 ** -8 + 2.0 ** -19
+        low = 2.0 ** -38 * 2.0 * gate * (np.abs(q[0]) + np.abs(q[32]))  # of the token's largest dz times scale
+        assert np.all(np.abs(got[t] - want)[fin] <= (2.0 ** -5 * (step * (np.abs(gate * w[32]) + np.abs(w[0])) + low))[fin])
