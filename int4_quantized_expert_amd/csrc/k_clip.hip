@@ -48,7 +48,7 @@ int64_t chunks_of(const moe_grad& g) { return g.n == 0 ? 0 : (g.n + skip_of(g) +
 
 struct TableArgs {
   ClipEntry e[kTableArgs];
-  int32_t first, count;
+  int32_t first;
   ClipEntry* entries;
   int32_t* owner;
 };
@@ -223,14 +223,14 @@ hipError_t launch_clip_table(const moe_grad* g, int count, void* table, hipStrea
   for (int at = 0; at < count; at += kTableArgs) {
     TableArgs a;
     a.first = at;
-    a.count = count - at < kTableArgs ? count - at : kTableArgs;
+    const int n = count - at < kTableArgs ? count - at : kTableArgs;
     a.entries = reinterpret_cast<ClipEntry*>(w + p.entries);
     a.owner = reinterpret_cast<int32_t*>(w + p.owner);
-    for (int i = 0; i < a.count; ++i) {
+    for (int i = 0; i < n; ++i) {
       a.e[i] = ClipEntry{g[at + i].g, g[at + i].out, g[at + i].n, chunk, g[at + i].dtype, skip_of(g[at + i])};
       chunk += chunks_of(g[at + i]);
     }
-    k_clip_table<<<a.count, 256, 0, st>>>(a);
+    k_clip_table<<<n, 256, 0, st>>>(a);
   }
   return hipGetLastError();
 }
