@@ -403,7 +403,8 @@ int32_t moe_linear(const moe_linear_config* cfg, const uint8_t* codes, const flo
  * through frozen codes.
  *   z = W x + bias + scale[e] B_e (A_e x),   e = ids[t];   y = act(z) + residual
  * A token whose id is outside [0, n_adapters) has no adapter. ids NULL: adapter 0 for every token. The adapters' sums
- * are fp32, and so is scale (A x) between the two.
+ * are fp32, and so is scale (A x) between the two; where 16-bit types take the matrix instructions for the second of them,
+ * 16 bits of it are multiplied, and of fp16 adapters not all low bits with all of its own (2^-17 of a term, fp16 2^-15).
  * ---------------------------------------------------------------------- */
 typedef struct moe_adapters {
   int32_t n_adapters; /* 1..1024 */
@@ -437,11 +438,13 @@ size_t moe_linear_backward_workspace_bytes(const moe_linear_config* cfg, const m
  * d_a and d_b may each be NULL, not all of them; x is read for d_a and d_b. All are of the call's type. residual may be
  * NULL or dx itself: the gradients of several products of one x are added so. The gradient of the forward call's residual
  * is dy. The weights, the bias and the scales have none. dx overlaps no input but residual, d_a and d_b none.
- * W^T dz is summed in fp32 over one rounding of dz times its row's scale (2^-12 of each term, fp32 2^-23); group scales
- * cost 2^-10 more of each weight for bf16, 2^-19 for fp16 and fp32, and a scale below 2^-26 of its row's largest is taken
- * to 2^-36 of that one. A token whose dz holds an infinity or NaN
- * has a dx of them, and so have the gradients of its adapter; others are not touched. Sums run in a fixed order: equal calls
- * give equal bits. Errors: MOE_E_NULL, MOE_E_SHAPE, MOE_E_ARG, MOE_E_WORKSPACE, MOE_E_HIP. */
+ * W^T dz is summed in fp32 over one rounding of dz times its row's scale: 2^-11 of each term (fp32 2^-23), or the code times
+ * 2^-38 of the token's largest dz times scale (2^-125 where that largest is below 2^-86) if that is more. Group scales cost
+ * each weight 2^-10 more for bf16, 2^-18 for fp16 and 2^-17 for fp32, or the code times 2^-35 of its row's largest scale if
+ * that is more. The adapters' sums take dz in fp32, not rounded to the call's type, and scale (A x) and scale (B^T dz) as the
+ * forward call takes the former. A token whose dz holds an infinity or NaN has a dx of them, and so have its adapter's d_a
+ * and those rows of its d_b; others are not touched. Sums run in a fixed order: equal calls give equal bits.
+ * Errors: MOE_E_NULL, MOE_E_SHAPE, MOE_E_ARG, MOE_E_WORKSPACE, MOE_E_HIP. */
 int32_t moe_linear_backward(const moe_linear_config* cfg, const uint8_t* codes, const float* scales,
                             const moe_adapters* adapters, const int32_t* ids, const void* x, int64_t ldx, int32_t T,
                             int32_t dtype, const void* pre, int64_t ldp, const void* dy, int64_t ldd,
@@ -451,7 +454,9 @@ int32_t moe_linear_backward(const moe_linear_config* cfg, const uint8_t* codes, 
 /* ------------------------------------------------------------------------
  * The norm over many gradients (adapters', a router's), and the gradients scaled to a largest norm:
  *   norm = sqrt(sum over all tensors of g^2);  out = g * min(1, max_norm / norm)
- * A program lays out a table of its tensors once and clips them each step with two launches.
+ * A program lays out a table of its tensors once and clips them each step with two launches. The table holds addresses:
+ * gradients that are allocated anew each step need a new one each step (a loop on the host and a launch for every 64
+ * tensors), and a captured step replays the addresses that it was captured with.
  * ---------------------------------------------------------------------- */
 typedef struct moe_grad {
   const void* g;
@@ -475,7 +480,8 @@ int32_t moe_grad_table(const moe_grad* grads /* host */, int32_t count, void* ta
                        hipStream_t stream);
 /* norm [1] fp32 (device). max_norm > 0; infinity: the norm alone (in place; else a copy). Squares are summed in 64 bits in
  * a fixed order. An infinite or NaN norm leaves the gradients as they are (out: a copy). The table holds the sums
- * between the two launches: calls on one table must not overlap, as those on one list of gradients do not. */
+ * between the two launches: calls on one table must not overlap, as those on one list of gradients do not. norm is no part
+ * of a tensor of the list. */
 int32_t moe_grad_clip(const moe_grads* grads, float max_norm, float* norm, hipStream_t stream);
 
 /* ------------------------------------------------------------------------

@@ -762,7 +762,8 @@ def moe_linear_backward(cfg: LinearConfig, codes, scales, dy, dx, ws, pre=None, 
 
 class GradTable:
     """moe_grad_table of a list of contiguous gradients (kept alive here) and where they go: `out`, as many tensors of the
-    same sizes and types, or None for in place. Building it waits for the current stream."""
+    same sizes and types, or None for in place. It holds their addresses: gradients that a program allocates anew each step
+    need a table each step. Building it waits for the current stream."""
 
     def __init__(self, grads, out=None):
         grads = list(grads)

@@ -156,7 +156,7 @@ __device__ __forceinline__ void put_h(const AdaptDown& a, const AdaptDown::Part&
 }
 
 // Few tokens: a workgroup takes a token and 4 rows of its A; its lanes share the columns, all loads in flight at once.
-// across: A lies as [C][R]. One token of 6144 columns, rank 16: 3.4 us, 191 of 2048, rank 8: 4.0; a launch and its loads.
+// across: A lies as [C][R]. One token of 6144 columns, rank 16: 3.4 us, 191 of 2048, rank 8: 4.6; a launch and its loads.
 template <class TX>
 struct alignas(4 * sizeof(TX)) Four {
   TX v[4];
@@ -358,7 +358,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_adapt_down(AdaptDown a) 
 // exchanges halves of words between two positions, which gives the operands of 8 products (column l + j of every eight
 // columns in product j). v comes with eight
 // positions of a row next to each other. As in the product's epilogue v has two bf16 parts, bf16 m one and fp16 m
-// two. fp32 (a kept dz too) is multiplied as it is, 4 columns a lane. 2,000 tokens of four adapters, rank 32, 4096 columns of
+// two, and the product of the low ones is left out. fp32 (a kept dz too) is multiplied as it is, 4 columns a lane. 2,000 tokens of four adapters, rank 32, 4096 columns of
 // fp32 and 6144 of bf16: 20.4 us for 57 MB, 16.0 for 41 with both in bf16; two workgroups a compute unit fit the registers, and each waits for chunk, order and rows in turn.
 __device__ __forceinline__ size_t outer_at(const AdaptOuter& a, const AdaptOuter::Part& d, int e, int r, int c) {
   return d.rows ? ((size_t)e * d.C + c) * a.R + r : ((size_t)e * a.R + r) * d.C + c;

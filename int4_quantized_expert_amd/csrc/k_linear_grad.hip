@@ -1,10 +1,15 @@
 // k_linear_grad.hip — gradients of y = act(W x + b + s B (A x)) for frozen codes W: with dz = dy act'(z),
 //   dx = W^T dz + s A^T (B^T dz),  dB = sum over tokens of dz (s A x)^T,  dA = sum over tokens of (s B^T dz) x^T.
 // W^T dz runs in the product's tiles, summing over the weight rows. Row scales are multiplied into dz, in fp32 before its
-// one rounding to fp16 (relative 2^-12; fp32 gradients keep two halves, 2^-23). Group scales differ along a row: the power
-// of two of a row's largest is multiplied into dz, without loss, what is left of them, at most 2^12 (times a code of at
-// most 8 it fits fp16), into the codes, as fp16 (relative 2^-11, or 2^-36 of the row's largest for scales that are less than
-// 2^-26 of it; fp16 and fp32 gradients keep two parts, 2^-19). For the adapters' sums dz is kept in fp32: rounded to the call's
+// one rounding to fp16 (relative 2^-11; fp32 gradients keep two halves, 2^-23). Two halves for fp16 gradients too would make
+// them as exact as their type (2.1e-4 in the 2-norm for 2.9e-4) and take 1.8 times as long: 2,048 tokens 12288 x 6144 SwiGLU
+// 327 us, 599 in fp32; bf16's own rounding is 1.7e-3. Group scales differ along a row: the power of two of a row's largest
+// is multiplied into dz, without loss, what is left of them, at most 2^12 (times a code of at most 8 it fits fp16), into the
+// codes. bf16 gradients take it as one fp16 (two roundings, 2^-10 of a weight). fp16 and fp32 gradients take eight bits of it,
+// whose product with a code is exact, and the rest as a second fp16 (its rounding and its product's, 2^-20 and 2^-19); the
+// product of that with the second half of an fp32 dz, 2^-19 more, is left out. Below fp16's normal range, for scales less
+// than 2^-25 of their row's largest and in two parts 2^-17, both roundings are 2^-25 in place, 2^-36 of that largest each at
+// most. For the adapters' sums dz is kept in fp32: rounded to the call's
 // type it made bf16 d_a and d_b 1.4 times as far off (2.3e-3 in the 2-norm for 1.7e-3), and fp16 values beyond 65504 infinite
 // (2,000 tokens, 4096 rows, SwiGLU, rank 32: dz, s (B^T dz) and d_a, d_b take 61 us, and took 50).
 #define MOE_ADAPTED 1

@@ -55,7 +55,8 @@ struct LinearArgs {
   int32_t vec_p;
 
   // kTransposed with group scales: those of each row over the power of two that was multiplied into the activations,
-  // [rows / 64][groups][64] as fp16 in the codes' order; gs_low further on what fp16 left over (fp32 activations only)
+  // [rows / 64][groups][64] as fp16 in the codes' order: for bf16 calls the scale, for fp16 and fp32 calls eight bits of it,
+  // and gs_low further on the rest
   const _Float16* gs;
   int64_t gs_low;
 };

@@ -102,7 +102,7 @@ __device__ __forceinline__ int column_at(int j) {
 // and the power of two of the tile's sums; 0 for positions without one. One product for each adapter that the positions
 // have, of all 32 of them, whose results are taken by the adapter's own positions only: what another adapter holds,
 // infinities and NaN included, stays out of theirs. h has two bf16 parts (2^-17 of its value is lost), a bf16 b one and an
-// fp16 b two (all its bits); fp32 is multiplied as it is.
+// fp16 b two; the product of the two low parts, up to 2^-16 of a term, is left out. fp32 is multiplied as it is.
 template <class TX>
 __device__ __forceinline__ void adapter_frags(const LinearArgs& a, int p0, const int (&row)[2], int lane, f16v (&d)[2]) {
   const int r = lane & 31, g = lane >> 5, p = min(p0 + r, a.T - 1);
