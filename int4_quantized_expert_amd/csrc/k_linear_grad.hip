@@ -70,7 +70,9 @@ __device__ __forceinline__ void dz8(const DzArgs& d, int64_t t, int n, f8v (&o)[
       const float c = zv[i] != zv[i] ? zv[i] : fminf(fmaxf(zv[i], -1e9f), 1e9f);
       float s, miss;
       sigmoid2(c, s, miss);
-      o[0][i] = v[i] * fmaf(c * s, miss, s) * uv[i];  // dy up may be beyond fp32 where a closed gate leaves little of it
+      // dy up may be beyond fp32 where a closed gate leaves little of it; then dy is above 1, and dy silu'(gate) in range
+      const float d = fmaf(c * s, miss, s), both = v[i] * uv[i];
+      o[0][i] = fabsf(both) < INFINITY ? both * d : v[i] * d * uv[i];
       o[1][i] = v[i] * (zv[i] < -1e9f ? 0.0f : zv[i] * s);
     }
   }

@@ -624,3 +624,20 @@ def test_a_gate_near_the_largest_number(T, dtype):
         step = 2.0 ** -21 if dtype == "f32" else 2.0 ** -11 + 2.0 ** -8 + 2.0 ** -19
         low = 2.0 ** -38 * 2.0 * gate * (np.abs(q[0]) + np.abs(q[32]))  # of the token's largest dz times scale
         assert np.all(np.abs(got[t] - want)[fin] <= (2.0 ** -5 * (step * (np.abs(gate * w[32]) + np.abs(w[0])) + low))[fin])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [2, 100])
+def test_a_small_gradient_times_a_large_up_part_of_a_closed_gate(T, dtype):
+    """dy times the gate's derivative is below fp32's normal range, dy up times it is not."""
+    rng = np.random.default_rng(T)
+    N, K = 128, 64
+    q, s, codes, scales = H.weights(rng, N, K, 8, 0)
+    dy, z = rng.uniform(0.5, 1.0, (T, N // 2)) * 2.0 ** -96, np.empty((T, N))
+    z[:, : N // 2], z[:, N // 2:] = rng.uniform(-40.0, -30.0, (T, N // 2)), rng.uniform(0.5, 1.0, (T, N // 2)) * 2.0 ** 68
+    dy, z = (torch.from_numpy(v.astype(np.float32)).to(DT[dtype]) for v in (dy, z))
+    dx, _, _ = _call(moe.LinearConfig(N, K, 8, 0, ACT["swiglu"]), codes, scales, dy.to(DEV), z=z.to(DEV), dtype=dtype)
+    dz, _ = R.grad_in(dy.double().numpy(), z.double().numpy(), "swiglu")
+    size = np.abs(dz) * 128 * R.UNIT  # as above
+    (v, err), _, _ = R.backward(q, s, None, None, None, None, None, dz, None, dtype)
+    assert R.within(dx.double().cpu().numpy(), v, err + size @ np.abs(R.weights(q, s)), dtype).all()
