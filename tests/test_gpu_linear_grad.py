@@ -641,3 +641,24 @@ def test_a_small_gradient_times_a_large_up_part_of_a_closed_gate(T, dtype):
     size = np.abs(dz) * 128 * R.UNIT  # as above
     (v, err), _, _ = R.backward(q, s, None, None, None, None, None, dz, None, dtype)
     assert R.within(dx.double().cpu().numpy(), v, err + size @ np.abs(R.weights(q, s)), dtype).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("how", ["none", "one", "mix"])
+@pytest.mark.parametrize("T,n,Rk", [(40, 70, 40), (300, 90, 8), (300, 3, 40)])
+def test_adapters_without_tokens_get_zeros_behind_an_activation(T, n, Rk, how, dtype):
+    rng = np.random.default_rng(T + n)
+    N, K = 192, 160
+    _, _, codes, scales = H.weights(rng, N, K, 4, 0)
+    ad, *_ = H.adapters(rng, n, Rk, N, K, dtype)
+    ids, i = H.ids_of(rng, T, n, how)
+    x, _ = H.matrix(rng, T, K, dtype)
+    dy, _ = H.matrix(rng, T, N // 2, dtype)
+    z, _ = H.matrix(rng, T, N, dtype, spread=False)
+    _, da, db = _call(moe.LinearConfig(N, K, act=ACT["swiglu"]), codes, scales, dy, ad, ids, x, z, dtype=dtype)
+    at = R.chosen(i, n, T)
+    have = torch.zeros(n, dtype=torch.bool)
+    have[torch.from_numpy(at[at >= 0])] = True
+    for g in (da, db):
+        flat = g.view(n, -1).float().cpu()
+        assert not bool(flat[~have].any()) and bool((flat[have] != 0).any(dim=1).all())
