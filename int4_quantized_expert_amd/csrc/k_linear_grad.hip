@@ -9,9 +9,9 @@
 // whose product with a code is exact, and the rest as a second fp16 (its rounding and its product's, 2^-20 and 2^-19); the
 // product of that with the second half of an fp32 dz, 2^-19 more, is left out. Below fp16's normal range, for scales less
 // than 2^-25 of their row's largest and in two parts 2^-17, both roundings are 2^-25 in place, 2^-36 of that largest each at
-// most. For the adapters' sums dz is kept in fp32: rounded to the call's
-// type it made bf16 d_a and d_b 1.4 times as far off (2.3e-3 in the 2-norm for 1.7e-3), and fp16 values beyond 65504 infinite
-// (2,000 tokens, 4096 rows, SwiGLU, rank 32: dz, s (B^T dz) and d_a, d_b take 61 us, and took 50).
+// most. For the adapters' sums dz is kept in fp32: rounding it to the call's type makes bf16 d_a and d_b 1.4 times as far off
+// (2.3e-3 in the 2-norm for 1.7e-3), and fp16 values beyond 65504 infinite (2,000 tokens, 4096 rows, SwiGLU, rank 32: dz,
+// s (B^T dz) and d_a, d_b take 61 us, 50 with it).
 #define MOE_ADAPTED 1
 #define MOE_TRANSPOSED 1
 #include "linear_kernels.h"
